@@ -1,7 +1,9 @@
-"""Build libllmoe.so (the CUDA library behind include/llmoe.h) for sm_103a.
+"""Build libllmoe.so (the CUDA library behind include/llmoe.h and
+include/llmoe_block.h) for sm_103a.
 
-One translation unit, one -gencode; nvcc cross-compiles without a GPU.  The
-library links the CUDA runtime statically and exports only the llmoe_* C ABI.
+One -gencode, the translation units compiled in parallel; nvcc cross-compiles
+without a GPU.  The library links the CUDA runtime statically and exports only
+the llmoe_* C ABI.
 """
 from __future__ import annotations
 
@@ -12,8 +14,10 @@ import sys
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SRC = os.path.join(PKG, "csrc", "llmoe.cu")
-HDR = os.path.join(ROOT, "include", "llmoe.h")
+CSRC = os.path.join(PKG, "csrc")
+SRCS = [os.path.join(CSRC, f) for f in ("llmoe.cu", "block_rows.cu", "block_router.cu", "block_product.cu")]
+HDRS = [os.path.join(ROOT, "include", "llmoe.h"), os.path.join(ROOT, "include", "llmoe_block.h"),
+        os.path.join(CSRC, "block_common.cuh")]
 OUT_DIR = os.path.join(PKG, "_build")
 SO = os.path.join(OUT_DIR, "libllmoe.so")
 # the phase-trace build (-DLLMOE_PHASE_TRACE=1): the same library with per-CTA
@@ -23,7 +27,7 @@ TRACE_SO = os.path.join(OUT_DIR, "libllmoe_trace.so")
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",
     "-O3", "-lineinfo", "-std=c++17",
-    "-Xcompiler", "-fPIC,-fvisibility=hidden", "-shared",
+    "-Xcompiler", "-fPIC,-fvisibility=hidden", "-shared", "--threads", "0",
 ]
 
 
@@ -39,11 +43,11 @@ def build(force: bool = False, verbose: bool = False, trace: bool = False) -> st
     it is newer than its sources; returns the path of the shared object."""
     out = TRACE_SO if trace else SO
     os.makedirs(OUT_DIR, exist_ok=True)
-    newest = max(os.path.getmtime(SRC), os.path.getmtime(HDR))
+    newest = max(os.path.getmtime(f) for f in SRCS + HDRS)
     if not force and os.path.exists(out) and os.path.getmtime(out) >= newest:
         return out
     tmp = f"{out}.{os.getpid()}.tmp"
-    cmd = [nvcc(), *NVCC_FLAGS, "-I", os.path.join(ROOT, "include"), "-o", tmp, SRC]
+    cmd = [nvcc(), *NVCC_FLAGS, "-I", os.path.join(ROOT, "include"), "-o", tmp, *SRCS]
     if trace:
         cmd.insert(1, "-DLLMOE_PHASE_TRACE=1")
     if verbose:

@@ -1,4 +1,4 @@
-"""Python binding of libllmoe.so (include/llmoe.h).
+"""Python binding of libllmoe.so (include/llmoe.h, include/llmoe_block.h).
 
 Argument marshalling only: every step of the data path runs in the CUDA
 kernels of the library.  Importing this module loads the library and raises
@@ -51,10 +51,17 @@ EXPORTS = ("llmoe_layout_bytes", "llmoe_layout_bytes_dtype", "llmoe_layout_offse
            "llmoe_dispatch_unpack",
            "llmoe_signal_workspace_bytes", "llmoe_dispatch_signaled", "llmoe_dispatch_signaled_static", "llmoe_clean",
            "llmoe_get_error",
-           "llmoe_status_string")
+           "llmoe_status_string",
+           "llmoe_row_bytes", "llmoe_pack_mx8", "llmoe_add_rmsnorm", "llmoe_topk_router", "llmoe_expert_product")
 
 LLMOE_DTYPE_BF16, LLMOE_DTYPE_FP16, LLMOE_DTYPE_FP32 = 0, 1, 2
 DTYPE_CODES = {"bf16": LLMOE_DTYPE_BF16, "fp16": LLMOE_DTYPE_FP16, "fp32": LLMOE_DTYPE_FP32}
+LLMOE_DTYPE_MX8 = 3  # 8-bit rows with scales: a row type of the block operators, not a payload type
+ROW_DTYPE_CODES = {**DTYPE_CODES, "mx8": LLMOE_DTYPE_MX8}
+LLMOE_MAX_ROW_VALUES = 32768
+LLMOE_SCORE_SIGMOID, LLMOE_SCORE_SOFTMAX = 0, 1
+LLMOE_ROUTER_RENORM = 1
+LLMOE_PRODUCT_SWIGLU = 1
 DTYPE_BYTES = {LLMOE_DTYPE_BF16: 2, LLMOE_DTYPE_FP16: 2, LLMOE_DTYPE_FP32: 4}
 
 
@@ -108,6 +115,19 @@ _lib.llmoe_clean.argtypes = [_BS, _P]
 _lib.llmoe_clean.restype = _I
 _lib.llmoe_get_error.argtypes = [_BS, _P, ctypes.POINTER(ctypes.c_int32), _I]
 _lib.llmoe_get_error.restype = _I
+_L = ctypes.c_int64
+_F = ctypes.c_float
+_U = ctypes.c_uint32
+_lib.llmoe_row_bytes.argtypes = [_I, _I]
+_lib.llmoe_row_bytes.restype = ctypes.c_size_t
+_lib.llmoe_pack_mx8.argtypes = [_P, _P, _L, _I, _I, _P]
+_lib.llmoe_pack_mx8.restype = _I
+_lib.llmoe_add_rmsnorm.argtypes = [_P, _P, _P, _F, _P, _P, _L, _I, _I, _I, _P]
+_lib.llmoe_add_rmsnorm.restype = _I
+_lib.llmoe_topk_router.argtypes = [_P, _P, _P, _P, _P, _L, _I, _I, _I, _I, _U, _F, _P]
+_lib.llmoe_topk_router.restype = _I
+_lib.llmoe_expert_product.argtypes = [_P, _P, _P, _P, _I, _I, _I, _I, _U, _BS, _P]
+_lib.llmoe_expert_product.restype = _I
 _lib.llmoe_status_string.argtypes = [_I]
 _lib.llmoe_status_string.restype = ctypes.c_char_p
 
@@ -129,6 +149,8 @@ _DTYPES = {
     "i64": (torch.int64,),
     "i32": (torch.int32,),
     "f32": (torch.float32,),
+    "u8": (torch.uint8, torch.bool),
+    "rows": (torch.bfloat16, torch.float16, torch.int16, torch.uint16, torch.float32, torch.uint8),
 }
 
 
@@ -246,6 +268,44 @@ def llmoe_get_error(bs: llmoe_buf_set_t, stream=None, reset: bool = False) -> in
     _check(_lib.llmoe_get_error(ctypes.byref(bs), _stream(stream), ctypes.byref(code), int(reset)),
            "llmoe_get_error")
     return code.value
+
+
+def llmoe_row_bytes(n: int, dtype: int) -> int:
+    """Bytes of a row of n values of a row type; 0 where there is no such row."""
+    return int(_lib.llmoe_row_bytes(n, dtype))
+
+
+def llmoe_pack_mx8(x, out, rows: int, hidden: int, dtype: int, stream=None) -> None:
+    _check(_lib.llmoe_pack_mx8(_addr(x, "payload"), _addr(out, "rows"), rows, hidden, dtype, _stream(stream)),
+           "llmoe_pack_mx8")
+
+
+def llmoe_add_rmsnorm(x, residual, weight, eps: float, residual_out, out, rows: int, hidden: int, dtype: int,
+                      out_dtype: int, stream=None) -> None:
+    _check(_lib.llmoe_add_rmsnorm(_addr(x, "payload"), _addr(residual, "payload"), _addr(weight, "payload"), eps,
+                                  _addr(residual_out, "payload"), _addr(out, "rows"), rows, hidden, dtype, out_dtype,
+                                  _stream(stream)), "llmoe_add_rmsnorm")
+
+
+def llmoe_topk_router(logits, bias, active, topk_idx, topk_w, rows: int, num_experts: int, num_topk: int, dtype: int,
+                      scoring: int, flags: int, scale: float, stream=None) -> None:
+    _check(_lib.llmoe_topk_router(_addr(logits, "payload"), _addr(bias, "f32"), _addr(active, "u8"),
+                                  _addr(topk_idx, "i64"), _addr(topk_w, "f32"), rows, num_experts, num_topk, dtype,
+                                  scoring, flags, scale, _stream(stream)), "llmoe_topk_router")
+
+
+def llmoe_expert_product(x, w, y, counts, in_features: int, out_features: int, dtype: int, out_dtype: int, flags: int,
+                         bs: llmoe_buf_set_t, stream=None) -> None:
+    _check(_lib.llmoe_expert_product(_addr(x, "rows"), _addr(w, "rows"), _addr(y, "rows"), _addr(counts, "i64"),
+                                     in_features, out_features, dtype, out_dtype, flags, ctypes.byref(bs),
+                                     _stream(stream)), "llmoe_expert_product")
+
+
+def geometry(num_max_tokens: int, num_ranks: int, num_experts: int, err=None) -> llmoe_buf_set_t:
+    """The geometry of a product whose counts are an argument: no rank buffers
+    behind it, so no dispatch or combine takes it."""
+    return llmoe_buf_set_t(num_max_tokens=num_max_tokens, num_ranks=num_ranks, num_experts=num_experts,
+                           err=None if err is None else _addr(err, "i32"))
 
 
 class Bound:

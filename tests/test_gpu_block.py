@@ -1,0 +1,391 @@
+"""GPU tests of the block operators (norm, router, expert products) against
+their definitions in 64 bits (tests/block_reference.py).
+
+Tolerances, derived from the arithmetic each call documents:
+- fp32 norm: a thread sums at most 64 squares in a row, then ten levels of
+  pairwise sums; halved by the square root, plus a square root, a division and
+  two products: 48 roundings of 2^-24, 3e-6 in all;
+- a result rounded to bf16 / fp16 / fp32 may be off by half an ulp more
+  (of 8, 11 and 24 significant bits: 2^-8, 2^-11 and 2^-24 of the value; the
+  least subnormal's half below);
+- router weights: exponential, sum and division, one rounding each per term;
+- products: an fp32 sum of n products, each addition within 2^-23 of the sum
+  of the magnitudes (the tensor cores truncate), and the rounding to the output
+  type.
+"""
+import numpy as np
+import pytest
+import torch
+
+import block_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+TORCH = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+HALF_ULP = {"bf16": 2.0 ** -8, "fp16": 2.0 ** -11, "fp32": 2.0 ** -24}
+TINY = {"bf16": 2.0 ** -134, "fp16": 2.0 ** -25, "fp32": 2.0 ** -150}
+NORM_ERR = 3e-6
+
+
+@pytest.fixture(scope="module")
+def L():
+    from combine_routing_count_prefix_gb300 import build
+
+    build.build()
+    from combine_routing_count_prefix_gb300 import llmoe
+
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    return llmoe
+
+
+def rnd(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def wide(t):
+    return t.cpu().to(torch.float64).numpy()
+
+
+def close(got, want, err, dtype):
+    """got within err of want, and half an ulp of dtype (of got's size)."""
+    tol = err + (np.abs(want) + err) * HALF_ULP[dtype] + TINY[dtype]
+    bad = ~(np.abs(got - want) <= tol)
+    assert not bad.any(), (int(bad.sum()), np.abs(got - want)[bad][:4], tol[bad][:4])
+
+
+# ---------------------------------------------------------------------------
+# rows: norm and packing
+# ---------------------------------------------------------------------------
+
+NORM_SHAPES = [(1, 64), (3, 96), (5, 2048), (2, 7168), (1, 32768), (700, 224), (2048, 32)]
+
+
+@pytest.mark.parametrize("out", ["same", "mx8"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("rows,hidden", NORM_SHAPES)
+def test_add_rmsnorm(L, rows, hidden, dtype, out):
+    g = rnd(rows * 7 + hidden)
+    x = torch.randn(rows, hidden, generator=g).to(TORCH[dtype])
+    res = (3 * torch.randn(rows, hidden, generator=g)).to(TORCH[dtype])
+    w = (1 + 0.2 * torch.randn(hidden, generator=g)).to(TORCH[dtype])
+    x[rows // 2] = 0  # a row whose sum may be the residual alone
+    if rows > 1:
+        res[0] = -x[0]  # and one whose sum is zero: eps alone under the root
+    h = (x.float() + res.float()).to(TORCH[dtype])
+    od = dtype if out == "same" else "mx8"
+    code = L.ROW_DTYPE_CODES
+    rb = L.llmoe_row_bytes(hidden, code[od])
+    got = torch.full((rows * rb + 16,), 0xA5, dtype=torch.uint8, device="cuda")
+    hout = torch.empty_like(x, device="cuda")
+    L.llmoe_add_rmsnorm(x.cuda(), res.cuda(), w.cuda(), 1e-5, hout, got[:-16], rows, hidden, code[dtype], code[od])
+    assert torch.equal(hout.cpu(), h)
+    assert (got[-16:] == 0xA5).all()
+    v = ref.rmsnorm(wide(h), wide(w), 1e-5)
+    if out == "mx8":
+        ref.check_mx8(got[:-16].reshape(rows, rb).cpu().numpy(), v, np.abs(v) * NORM_ERR)
+    else:
+        close(wide(got[:-16].view(TORCH[dtype]).reshape(rows, hidden)), v, np.abs(v) * NORM_ERR, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_add_rmsnorm_in_place_and_without_residual(L, dtype):
+    rows, hidden = 37, 1056
+    g = rnd(5)
+    x = torch.randn(rows, hidden, generator=g).to(TORCH[dtype])
+    res = torch.randn(rows, hidden, generator=g).to(TORCH[dtype])
+    w = torch.randn(hidden, generator=g).to(TORCH[dtype])
+    c = L.ROW_DTYPE_CODES[dtype]
+    # no residual: h = x; out over x
+    a = x.cuda()
+    L.llmoe_add_rmsnorm(a, None, w.cuda(), 0.0, None, a, rows, hidden, c, c)
+    v = ref.rmsnorm(wide(x), wide(w), 0.0)
+    close(wide(a), v, np.abs(v) * NORM_ERR, dtype)
+    # the stored sum over the residual, then over x
+    h = (x.float() + res.float()).to(TORCH[dtype])
+    v = ref.rmsnorm(wide(h), wide(w), 1e-6)
+    for over in ("residual", "x"):
+        a, b, o = x.cuda(), res.cuda(), torch.empty_like(x, device="cuda")
+        L.llmoe_add_rmsnorm(a, b, w.cuda(), 1e-6, b if over == "residual" else a, o, rows, hidden, c, c)
+        assert torch.equal((b if over == "residual" else a).cpu(), h)
+        close(wide(o), v, np.abs(v) * NORM_ERR, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("rows,hidden", [(1, 32), (9, 512), (4, 7168), (3, 544)])
+def test_pack_mx8_is_exact(L, rows, hidden, dtype):
+    g = rnd(rows + hidden)
+    x = (torch.randn(rows, hidden, generator=g) * torch.exp2(torch.randint(-12, 9, (rows, hidden // 32, 1), generator=g)
+         .float()).expand(-1, -1, 32).reshape(rows, hidden)).to(TORCH[dtype])
+    x[0, :32] = 0  # a group of zeros
+    if hidden >= 512:
+        x[0, 32:64] = 0
+        x[0, 32] = 448  # exactly e4m3's largest at scale 1
+        x[0, 64:96] = 0
+        x[0, 64] = -452  # above it: the next scale
+        x[0, 96:128] = torch.tensor([17.0, 19.0, 21.0, 23.0] * 8) / 16  # midpoints of e4m3 at some scales
+        x[0, 96] = 448
+    got = torch.empty(rows, L.llmoe_row_bytes(hidden, L.LLMOE_DTYPE_MX8), dtype=torch.uint8, device="cuda")
+    L.llmoe_pack_mx8(x.cuda(), got, rows, hidden, L.ROW_DTYPE_CODES[dtype])
+    want = ref.pack_mx8(wide(x))
+    got = got.cpu().numpy()
+    assert np.array_equal(got[:, hidden:], want[:, hidden:])
+    assert np.array_equal(ref.E4M3[got[:, :hidden]], ref.E4M3[want[:, :hidden]])
+
+
+def test_pack_mx8_of_nan_and_infinity(L):
+    x = torch.ones(1, 128, dtype=torch.bfloat16)
+    x[0, 5], x[0, 70] = float("nan"), float("-inf")
+    got = torch.empty(1, 144, dtype=torch.uint8, device="cuda")
+    L.llmoe_pack_mx8(x.cuda(), got, 1, 128, L.LLMOE_DTYPE_BF16)
+    assert got.cpu()[0, 128:132].tolist() == [255, 119, 255, 119]  # 1 = 256 * 2^-8
+
+
+def test_norm_no_rows(L):
+    w = torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    L.llmoe_add_rmsnorm(None, None, w, 1e-6, None, None, 0, 64, 0, 0)
+    L.llmoe_pack_mx8(None, None, 0, 64, 0)
+    torch.cuda.synchronize()
+
+
+# ---------------------------------------------------------------------------
+# router
+# ---------------------------------------------------------------------------
+
+def run_router(L, logits, bias, active, K, dtype, scoring, renorm, scale):
+    rows, E = logits.shape
+    idx = torch.full((rows, K), -7, dtype=torch.int64, device="cuda")
+    w = torch.full((rows, K), float("nan"), device="cuda")
+    L.llmoe_topk_router(logits.cuda(), None if bias is None else bias.cuda(), None if active is None else active.cuda(),
+                        idx, w, rows, E, K, L.DTYPE_CODES[dtype],
+                        L.LLMOE_SCORE_SIGMOID if scoring == "sigmoid" else L.LLMOE_SCORE_SOFTMAX,
+                        L.LLMOE_ROUTER_RENORM if renorm else 0, scale)
+    return idx.cpu().numpy(), w.cpu().numpy().astype(np.float64)
+
+
+@pytest.mark.parametrize("scoring,bias", [("sigmoid", True), ("sigmoid", False), ("softmax", True), ("softmax", False)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("rows,E,K", [(1, 1, 1), (5, 8, 8), (3, 33, 2), (64, 64, 6), (17, 256, 8), (9, 511, 32),
+                                      (4, 513, 8), (3, 2049, 9), (2, 8192, 32)])
+def test_router(L, rows, E, K, dtype, scoring, bias):
+    g = rnd(rows * 31 + E)
+    # eighths: exact in every type, and so many that keys tie
+    logits = torch.randint(-24, 25, (rows, E), generator=g).float() / 8
+    b = torch.randint(-1, 2, (E,), generator=g).float() / 4 if bias else None
+    active = (torch.rand(rows, generator=g) < 0.8).to(torch.uint8) if rows > 4 else None
+    renorm = rows % 2 == 1
+    idx, w, gap = ref.router(logits.numpy(), None if b is None else b.numpy(), None if active is None else active.numpy(),
+                             K, scoring, renorm, 2.5)
+    assert gap > 1e-6  # so that fp32 keys order as the exact ones do
+    gi, gw = run_router(L, logits.to(TORCH[dtype]), b, active, K, dtype, scoring, renorm, 2.5)
+    assert np.array_equal(gi, idx)
+    assert (np.abs(gw - w) <= w * (E / 32 + K + 32) * 2.0 ** -23).all()
+
+
+@pytest.mark.parametrize("scoring", ["sigmoid", "softmax"])
+def test_router_masked_experts(L, scoring):
+    inf, nan = float("inf"), float("nan")
+    E, K = 40, 4
+    logits = torch.zeros(6, E)
+    logits[0] = -inf  # nothing can be chosen
+    logits[1] = -inf
+    logits[1, 7], logits[1, 39] = 0.5, 1.5  # two can
+    logits[2] = nan
+    logits[2, 3] = -2.0
+    logits[3, 20:] = nan  # NaN beside ordinary ones
+    logits[4, 11] = logits[4, 30] = inf  # two of the largest
+    logits[5] = torch.finfo(torch.float32).min  # a mask of the type's lowest value, over the whole row
+    bias = torch.zeros(E)
+    bias[2] = -inf  # masked by the bias
+    for b in (None, bias):
+        idx, w, _ = ref.router(np.where(np.isnan(logits.numpy()), -np.inf, logits.numpy()),
+                               None if b is None else b.numpy(), None, K, scoring, True, 1.0)
+        gi, gw = run_router(L, logits, b, None, K, "fp32", scoring, True, 1.0)
+        assert np.array_equal(gi, idx)
+        assert np.allclose(gw, w, rtol=64 * 2.0 ** -23, atol=0)
+
+
+def test_router_no_rows(L):
+    L.llmoe_topk_router(None, None, None, None, None, 0, 8, 2, L.LLMOE_DTYPE_FP32, 0, 0, 1.0)
+    torch.cuda.synchronize()
+
+
+# ---------------------------------------------------------------------------
+# expert products
+# ---------------------------------------------------------------------------
+
+def some_counts(E, R, T, kind, seed):
+    r = np.random.RandomState(seed)
+    if kind == "full":
+        return np.full((E, R), T, np.int64)
+    if kind == "none":
+        return np.zeros((E, R), np.int64)
+    if kind == "one":  # a single row in the whole call
+        c = np.zeros((E, R), np.int64)
+        c[E - 1, R // 2] = 1
+        return c
+    c = r.randint(0, T + 1, (E, R))
+    c[r.rand(E, R) < 0.3] = 0
+    c[r.randint(E)] = 0  # an expert without rows
+    c[r.randint(E), r.randint(R)] = T
+    return c.astype(np.int64)
+
+
+def make_rows(L, n_rows, n, dtype, seed, scale=1.0):
+    """Device rows of a row type and their 64-bit values."""
+    v = torch.randn(n_rows, n, generator=rnd(seed)) * scale
+    if dtype == "mx8":
+        rows = ref.pack_mx8(v.double().numpy())
+        return torch.from_numpy(rows).cuda(), ref.mx8_values(rows, n)
+    t = v.to(TORCH[dtype])
+    return t.cuda(), wide(t)
+
+
+def check_product(L, R, T, E, n_in, n_out, dtype, out_dtype, swiglu, counts, bs=None, call_counts="given", stream=None):
+    rows = E * R * T
+    x, xv = make_rows(L, rows, n_in, dtype, 11 * E + n_in)
+    w, wv = make_rows(L, E * n_out * (1 + swiglu), n_in, dtype, 13 * E + n_out, n_in ** -0.5)
+    at, v, err = ref.product(xv, wv.reshape(E, -1, n_in), counts, T, swiglu)
+    # rows that were not received hold anything: NaN here (0xFF codes and scales)
+    unused = np.ones(rows, bool)
+    unused[at] = False
+    if dtype == "mx8":
+        x[torch.from_numpy(unused)] = 0xFF
+    else:
+        x[torch.from_numpy(unused)] = float("nan")
+    code = L.ROW_DTYPE_CODES
+    rb = L.llmoe_row_bytes(n_out, code[out_dtype])
+    y = torch.full((rows + 1, rb), 0xA5, dtype=torch.uint8, device="cuda")
+    e = torch.zeros(1, dtype=torch.int32, device="cuda")
+    if bs is None:
+        bs = L.geometry(T, R, E, err=e)
+    c = torch.from_numpy(counts).cuda() if call_counts == "given" else None
+    torch.cuda.synchronize()
+    L.llmoe_expert_product(x, w, y[:rows], c, n_in, n_out, code[dtype], code[out_dtype],
+                           L.LLMOE_PRODUCT_SWIGLU if swiglu else 0, bs, stream)
+    torch.cuda.synchronize()
+    assert int(e) == 0
+    y = y.cpu()
+    assert (y[rows] == 0xA5).all() and (y[:rows][torch.from_numpy(unused)] == 0xA5).all()
+    got = y[:rows][torch.from_numpy(at)]
+    if not len(at):
+        return
+    if out_dtype == "mx8":
+        ref.check_mx8(got.numpy(), v, err)
+    else:
+        close(wide(got.contiguous().view(TORCH[out_dtype])), v, err, out_dtype)
+
+
+PRODUCT_TYPES = [("bf16", "bf16"), ("fp16", "fp16"), ("bf16", "fp32"), ("mx8", "bf16"), ("mx8", "fp16"),
+                 ("mx8", "fp32"), ("mx8", "mx8")]
+# in, out: below one tile, odd multiples, one tile, past a tile's edge in either
+PRODUCT_SIZES = [(32, 32), (96, 160), (128, 256), (544, 288), (256, 32)]
+
+
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("dtype,out_dtype", PRODUCT_TYPES)
+@pytest.mark.parametrize("n_in,n_out", PRODUCT_SIZES)
+def test_product_types_and_sizes(L, n_in, n_out, dtype, out_dtype, swiglu):
+    if out_dtype == "mx8" and not swiglu:
+        pytest.skip("MX8 output belongs to the SwiGLU product")
+    R, T, E = 2, 21, 4
+    check_product(L, R, T, E, n_in, n_out, dtype, out_dtype, swiglu, some_counts(E, R, T, "ragged", n_in))
+
+
+@pytest.mark.parametrize("kind", ["ragged", "full", "none", "one"])
+@pytest.mark.parametrize("dtype", ["bf16", "mx8"])
+@pytest.mark.parametrize("R,T,E", [(1, 1, 1), (1, 300, 3), (8, 5, 16), (40, 3, 40), (4, 130, 4), (3, 1, 96)])
+def test_product_geometries(L, R, T, E, dtype, kind):
+    out_dtype = "bf16"
+    check_product(L, R, T, E, 160, 96, dtype, out_dtype, False, some_counts(E, R, T, kind, R + T))
+    check_product(L, R, T, E, 160, 96, dtype, "mx8" if dtype == "mx8" else out_dtype, True,
+                  some_counts(E, R, T, kind, R + T + 1))
+
+
+@pytest.mark.parametrize("n_in,n_out,swiglu", [(8, 8, False), (24, 40, True), (72, 520, False), (1032, 264, True)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_product_odd_sizes_16_bit(L, n_in, n_out, swiglu, dtype):
+    check_product(L, 2, 33, 4, n_in, n_out, dtype, dtype, swiglu, some_counts(4, 2, 33, "ragged", 3))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "mx8"])
+def test_product_long_inner_dimension(L, dtype):
+    check_product(L, 1, 40, 2, 4096, 64, dtype, "bf16", False, some_counts(2, 1, 40, "full", 0))
+
+
+def test_product_on_another_stream(L):
+    s = torch.cuda.Stream()
+    check_product(L, 2, 17, 4, 128, 128, "bf16", "bf16", True, some_counts(4, 2, 17, "ragged", 9), stream=s)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "mx8"])
+def test_product_is_reproducible_and_captures(L, dtype):
+    """The same bits on every call, eager and replayed from a CUDA graph."""
+    R, T, E, n_in, n_out = 2, 70, 6, 256, 320
+    x, _ = make_rows(L, E * R * T, n_in, dtype, 1)
+    w, _ = make_rows(L, E * 2 * n_out, n_in, dtype, 2, 0.1)
+    c = torch.from_numpy(some_counts(E, R, T, "ragged", 4)).cuda()
+    code = L.ROW_DTYPE_CODES
+    bs = L.geometry(T, R, E)
+    ys = [torch.zeros(E * R * T, n_out, dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+
+    def call(y):
+        L.llmoe_expert_product(x, w, y, c, n_in, n_out, code[dtype], code["bf16"], L.LLMOE_PRODUCT_SWIGLU, bs)
+
+    call(ys[0])
+    call(ys[1])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(ys[2])
+    ys[2].fill_(0)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(ys[0], ys[1]) and torch.equal(ys[0], ys[2])
+
+
+@pytest.mark.parametrize("bad", [-3, 18])
+def test_product_bad_count_is_reported_and_clamped(L, bad):
+    R, T, E = 1, 17, 2
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    x, xv = make_rows(L, E * R * T, 64, "bf16", 1)
+    w, wv = make_rows(L, E * 64, 64, "bf16", 2)
+    y = torch.zeros(E * R * T + 1, 64, dtype=torch.bfloat16, device="cuda")
+    bs = L.geometry(T, R, E, err=err)
+    c = torch.tensor([[2], [bad]], dtype=torch.int64, device="cuda")
+    L.llmoe_expert_product(x, w, y[:-1], c, 64, 64, 0, 0, 0, bs)
+    assert L.llmoe_get_error(bs) == L.LLMOE_DEV_SLOT_RANGE
+    clamped = np.array([[2], [min(max(bad, 0), T)]])
+    at, v, e = ref.product(xv, wv.reshape(E, 64, 64), clamped, T, False)
+    close(wide(y)[at], v, e, "bf16")
+    rest = np.ones(len(y), bool)
+    rest[at] = False
+    assert not wide(y)[rest].any()
+
+
+# ---------------------------------------------------------------------------
+# one MoE block: norm, router, dispatch, products, combine
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["bf16", "mx8"])
+def test_counts_from_the_rank_buffers(L, dtype):
+    """The product driven by a dispatch's own count words (counts NULL)."""
+    R, T, E, K, n_in, n_out = 2, 9, 6, 2, 512, 64
+    code = L.ROW_DTYPE_CODES
+    rb_in = L.llmoe_row_bytes(n_in, code[dtype])
+    x, _ = make_rows(L, R * T, n_in, dtype, 3)
+    w, _ = make_rows(L, E * n_out, n_in, dtype, 4, 0.05)
+    idx = torch.rand(R, T, E, generator=rnd(1)).argsort(-1)[..., :K].contiguous()
+    idx[0, 3, 1] = -1
+    rb = L.RankBuffers(T, rb_in // 2, R, E, fill=0xA5)
+    recv = torch.zeros(E * R * T, rb_in, dtype=torch.uint8, device="cuda")
+    src = torch.zeros(E * R * T, dtype=torch.int32, device="cuda")
+    for s in (0, 1):
+        bs = rb.buf_set(s, K)
+        L.llmoe_clean(bs)
+        L.llmoe_dispatch_unpack(x.view(torch.uint8).view(torch.bfloat16), idx.cuda(), recv.view(torch.bfloat16), src, bs)
+        counts = torch.empty(E, R, dtype=torch.int64, device="cuda")
+        slot = torch.empty(R, T, K, dtype=torch.int32, device="cuda")
+        L.llmoe_route(idx.cuda(), slot, counts, bs)
+        ya, yb = (torch.zeros(E * R * T, n_out, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        L.llmoe_expert_product(recv, w, ya, None, n_in, n_out, code[dtype], 0, 0, bs)
+        L.llmoe_expert_product(recv, w, yb, counts, n_in, n_out, code[dtype], 0, 0, L.geometry(T, R, E))
+        assert torch.equal(ya, yb) and bool(ya.any())
