@@ -17,7 +17,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 SRCS = [os.path.join(CSRC, f) for f in ("llmoe.cu", "block_rows.cu", "block_router.cu", "block_product.cu")]
 HDRS = [os.path.join(ROOT, "include", "llmoe.h"), os.path.join(ROOT, "include", "llmoe_block.h"),
-        os.path.join(CSRC, "block_common.cuh")]
+        os.path.join(CSRC, "block_common.cuh"), os.path.join(CSRC, "block_tensor.cuh")]
 OUT_DIR = os.path.join(PKG, "_build")
 SO = os.path.join(OUT_DIR, "libllmoe.so")
 # the phase-trace build (-DLLMOE_PHASE_TRACE=1): the same library with per-CTA
