@@ -10,15 +10,21 @@
 // features and half of the rows in shared memory and 128 x N sums in its tensor
 // memory (tcgen05, cta_group::2).
 //
+// The rows of an expert lie in R buckets of consecutive rows.  A tile takes
+// them in groups of four (a bucket's last group may reach past its count: those
+// columns are computed from whatever lies there and never stored), and runs of
+// groups load as boxes of 4 to 128 rows.
+//
 // Persistent pairs; every pair takes tiles pair, pair + pairs, ... of a list
 // that each CTA derives from the counts in its prologue.  Inside a CTA:
-//   warp 0     loads: one TMA tile of w and TMA gathers of x rows (four rows of
-//              any index per instruction) per 128 bytes of K, into a ring
-//   warp 1     (first CTA of the pair) issues the products
-//   warp 2     plans: the tile's expert, features and received rows
-//   warp 3     8-bit operands: moves the scales into the ring
-//   warps 4-7  epilogue: sums from tensor memory, SwiGLU, rounding, stores,
-//              while the next tile's products run into the other accumulator
+//   warp 0      loads: one TMA box of w and a few of x per 128 bytes of K, into
+//               a ring
+//   warp 1      (first CTA of the pair) issues the products
+//   warp 2      plans: the tile's expert, features and received rows
+//   warp 3      allocates tensor memory
+//   warps 4-7   epilogue: sums from tensor memory, SwiGLU, rounding, stores,
+//               while the next tile's products run into the other accumulator
+//   warps 8-11  8-bit operands: move the scales to shared memory
 // Every wait is bounded (kSpinLimit cycles); on expiry the role records
 // LLMOE_DEV_TIMEOUT and leaves its loop, the others follow when their own waits
 // expire, and all meet at the end to free the tensor memory.  A copy in flight
@@ -27,23 +33,31 @@
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kPlanDepth = 4;   // planned tiles in flight
+constexpr int kPlanDepth = 4;       // planned tiles in flight
 constexpr int kMaxStages = 8;
 constexpr int kTileFeatures = 256;  // rows of w per tile: 128 in each CTA
+constexpr int kGroup = 4;           // rows of x taken together
+constexpr int kBoxes = 6;           // x loads of 1, 2, .. 32 groups
 
 // Per operand type: the most rows per tile and the ring stage's layout (128
 // bytes of K: 64 values of 16 bits or 128 of 8 bits).
 template <bool kMx>
 struct Shape {
-  // two accumulators of kMaxRows columns; 8-bit scales need 12 more for each stage
+  static constexpr int kThreads = kMx ? 384 : 256;
+  // two accumulators of kMaxRows columns
   static constexpr int kMaxRows = kMx ? 192 : 256;
   static constexpr int kBytesA = 128 * 128, kBytesB = kMaxRows / 2 * 128;
   static constexpr int kStage = kBytesA + kBytesB;
-  static constexpr int kScales = kMx ? 512 + 1024 : 0;  // of 128 w rows, of up to 256 x rows
-  static constexpr int kScaleColumns = 12;
   static constexpr int kStages = kMx ? 7 : 6;
-  static_assert(2 * kMaxRows + (kMx ? kStages * kScaleColumns : 0) <= 512, "tensor memory has 512 columns");
+  // 8-bit operands: scales in slots of four steps; a step's are 512 bytes for
+  // the CTA's 128 rows of w and 1024 for up to 256 rows of x, and 12 columns
+  // of tensor memory, kept for kScaleRing steps (more than there are stages, so
+  // the step that used them before has finished)
+  static constexpr int kSlots = kMx ? 3 : 0;
+  static constexpr int kSlot = 4 * (512 + 1024);
+  static constexpr int kScaleColumns = 12, kScaleRing = 8;
+  static_assert(2 * kMaxRows + (kMx ? kScaleRing * kScaleColumns : 0) <= 512, "tensor memory has 512 columns");
+  static_assert(kScaleRing > kStages, "a step's scale columns outlive its stage");
 };
 
 struct ProductArgs {
@@ -64,6 +78,10 @@ struct ProductArgs {
   uint32_t idesc;  // instruction descriptor without N and scale ids
 };
 
+struct ProductMaps {
+  CUtensorMap w, x[kBoxes];
+};
+
 __device__ __forceinline__ int bucket_count(const ProductArgs& a, int e, int src) {
   const int64_t* p = a.counts != nullptr
                          ? a.counts + (int64_t)e * a.R + src
@@ -73,14 +91,17 @@ __device__ __forceinline__ int bucket_count(const ProductArgs& a, int e, int src
   if (c < 0 || c > a.T) report(a.err, LLMOE_DEV_SLOT_RANGE);
   return (int)max((int64_t)0, min(c, (int64_t)a.T));
 }
+__device__ __forceinline__ int bucket_groups(const ProductArgs& a, int e, int src) {
+  return (bucket_count(a, e, src) + kGroup - 1) / kGroup;
+}
 
 // A planned tile; its rows are in the plan's row list.
 struct __align__(16) Tile {
-  int expert, block, rows;
+  int expert, block, groups;
 };
 
 // Columns of a tile's product: a CTA pair's N is a multiple of 32.
-__device__ __forceinline__ int padded(int rows) { return (rows + 31) / 32 * 32; }
+__device__ __forceinline__ int columns(int groups) { return (groups * kGroup + 31) / 32 * 32; }
 
 // Byte offsets in dynamic shared memory, from its first 1024-byte boundary.
 struct SmemLayout {
@@ -91,13 +112,13 @@ __host__ __device__ inline SmemLayout smem_layout(int stages, int E) {
   using S = Shape<kMx>;
   SmemLayout l;
   uint32_t at = stages * S::kStage;
-  l.scales = at, at += stages * S::kScales;
+  l.scales = at, at += S::kSlots * S::kSlot;
   l.rows = at, at += kPlanDepth * S::kMaxRows * 4;
   l.tiles = at, at += kPlanDepth * 16;
   l.amax = at, at += 2 * 4 * 16 * 4;
-  l.bars = at, at += (2 * kMaxStages + 4 + 2 * kPlanDepth + 2) * 8;
+  l.bars = at, at += (2 * kMaxStages + 4 + 2 * kPlanDepth + 2 + 2 * 4) * 8;
   l.tmem = at, at += 16;
-  l.part = at, at += 32;
+  l.part = at, at += 64;
   l.prefix = at, at += (E + 1) * 4;
   l.total = at + 1024;  // the base may have to move up to its boundary
   return l;
@@ -109,20 +130,20 @@ __host__ __device__ inline SmemLayout smem_layout(int stages, int E) {
 // prefix[e] = tiles of the experts before e (prefix[E]: all tiles).
 template <bool kMx>
 __device__ void count_tiles(const ProductArgs& a, int* prefix, int* part) {
+  constexpr int kThreads = Shape<kMx>::kThreads, kMost = Shape<kMx>::kMaxRows / kGroup;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int kMaxRows = Shape<kMx>::kMaxRows;
   if (a.R >= 32) {
     for (int e = warp; e < a.E; e += kThreads / 32) {
       int n = 0;
-      for (int s = lane; s < a.R; s += 32) n += bucket_count(a, e, s);
+      for (int s = lane; s < a.R; s += 32) n += bucket_groups(a, e, s);
       n = __reduce_add_sync(0xffffffffu, n);
-      if (lane == 0) prefix[e] = (n + kMaxRows - 1) / kMaxRows * a.blocks;
+      if (lane == 0) prefix[e] = (n + kMost - 1) / kMost * a.blocks;
     }
   } else {
     for (int e = tid; e < a.E; e += kThreads) {
       int n = 0;
-      for (int s = 0; s < a.R; ++s) n += bucket_count(a, e, s);
-      prefix[e] = (n + kMaxRows - 1) / kMaxRows * a.blocks;
+      for (int s = 0; s < a.R; ++s) n += bucket_groups(a, e, s);
+      prefix[e] = (n + kMost - 1) / kMost * a.blocks;
     }
   }
   __syncthreads();
@@ -152,15 +173,15 @@ __device__ void count_tiles(const ProductArgs& a, int* prefix, int* part) {
 // ---------------------------------------------------------------------------
 // plan: one warp turns a tile's number into its expert, features and rows
 // ---------------------------------------------------------------------------
-// Rows of expert e in compact order: source ranks ascending, slots ascending.
-// The tile's share [r0, r1) goes to list, padded to a multiple of 32 with its
-// last row (the columns of the padding are never stored).
-__device__ void plan_rows(const ProductArgs& a, int e, int r0, int r1, int* list) {
+// Groups of expert e in order: source ranks ascending, slots ascending.  The
+// tile's share [g0, g1) goes to list, one entry per column: the row of x and y,
+// or -1 where there is none.
+__device__ void plan_rows(const ProductArgs& a, int e, int g0, int g1, int* list) {
   const int lane = threadIdx.x & 31;
-  int before = 0, last = 0;
-  for (int s0 = 0; s0 < a.R && before < r1; s0 += 32) {
-    const int c = s0 + lane < a.R ? bucket_count(a, e, s0 + lane) : 0;
-    int incl = c;
+  int before = 0;
+  for (int s0 = 0; s0 < a.R && before < g1; s0 += 32) {
+    const int c = s0 + lane < a.R ? bucket_count(a, e, s0 + lane) : 0, g = (c + kGroup - 1) / kGroup;
+    int incl = g;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int v = __shfl_up_sync(0xffffffffu, incl, d);
@@ -169,16 +190,16 @@ __device__ void plan_rows(const ProductArgs& a, int e, int r0, int r1, int* list
     const int n = min(32, a.R - s0);
     for (int j = 0; j < n; ++j) {
       const int end = before + __shfl_sync(0xffffffffu, incl, j), cnt = __shfl_sync(0xffffffffu, c, j);
-      const int beg = end - cnt, lo = max(beg, r0), hi = min(end, r1);
-      if (lo >= hi) continue;
-      const int first = (e * a.R + s0 + j) * a.T - beg;  // row of compact index i: first + i
-      for (int i = lo + lane; i < hi; i += 32) list[i - r0] = first + i;
-      last = first + hi - 1;
+      const int beg = end - (cnt + kGroup - 1) / kGroup, lo = max(beg, g0), hi = min(end, g1);
+      const int first = (e * a.R + s0 + j) * a.T;
+      for (int i = lo * kGroup + lane; i < hi * kGroup; i += 32) {
+        const int slot = i - beg * kGroup;
+        list[i - g0 * kGroup] = slot < cnt ? first + slot : -1;
+      }
     }
     before += __shfl_sync(0xffffffffu, incl, 31);
   }
-  const int pad = padded(r1 - r0);
-  for (int i = r1 - r0 + lane; i < pad; i += 32) list[i] = last;
+  for (int i = (g1 - g0) * kGroup + lane; i < columns(g1 - g0); i += 32) list[i] = -1;
 }
 
 template <bool kMx>
@@ -193,13 +214,34 @@ __device__ void plan_tile(const ProductArgs& a, const int* prefix, int t, Tile* 
   const int e = lo, shares = (prefix[e + 1] - prefix[e]) / a.blocks;
   const int local = t - prefix[e], share = local % shares;
   int total = 0;
-  for (int s = lane; s < a.R; s += 32) total += bucket_count(a, e, s);
+  for (int s = lane; s < a.R; s += 32) total += bucket_groups(a, e, s);
   total = __reduce_add_sync(0xffffffffu, total);
   // equal shares: an expert of 300 rows is two tiles of 150
-  const int r0 = (int)((int64_t)total * share / shares), r1 = (int)((int64_t)total * (share + 1) / shares);
+  const int g0 = (int)((int64_t)total * share / shares), g1 = (int)((int64_t)total * (share + 1) / shares);
   static_assert(kMaxRows % 32 == 0, "a share of at most kMaxRows rows pads to at most kMaxRows");
-  plan_rows(a, e, r0, r1, list);
-  if (lane == 0) *tile = Tile{e, local / shares, r1 - r0};
+  plan_rows(a, e, g0, g1, list);
+  if (lane == 0) *tile = Tile{e, local / shares, g1 - g0};
+}
+
+// The box that starts at this lane's group, as the power of two of its groups,
+// or -1: the CTA's share of a tile is `groups` groups, lane g's starting at row
+// `row`; runs of consecutive rows are cut into boxes, largest first.
+__device__ __forceinline__ int plan_box(int row, int groups) {
+  const int lane = threadIdx.x & 31;
+  const int prev = __shfl_up_sync(0xffffffffu, row, 1);
+  const uint32_t heads = __ballot_sync(0xffffffffu, lane < groups && (lane == 0 || row != prev + kGroup));
+  if (lane >= groups) return -1;
+  const int head = 31 - __clz(heads & (0xffffffffu >> (31 - lane)));
+  const uint32_t later = lane == 31 ? 0 : heads >> (lane + 1);
+  const int len = (later ? lane + __ffs(later) : groups) - head, p = lane - head;
+  int box = -1, at = 0;
+#pragma unroll
+  for (int b = kBoxes - 1; b >= 0; --b)
+    if (len >> b & 1) {
+      if (p == at) box = b;
+      at += 1 << b;
+    }
+  return box;
 }
 
 // ---------------------------------------------------------------------------
@@ -221,14 +263,13 @@ __device__ __forceinline__ void store2(uint8_t* p, float lo, float hi, int out_d
 }
 
 // 16 columns (rows of y) of 32 features: lane l holds feature first + l.
-// list: the 16 rows; n of them are stored.
-__device__ __forceinline__ void store_plain(const ProductArgs& a, const float (&v)[16], int first, const int* list,
-                                            int n) {
+// list: the columns' rows, -1 where nothing is stored.
+__device__ __forceinline__ void store_plain(const ProductArgs& a, const float (&v)[16], int first, const int* list) {
   const int lane = threadIdx.x & 31;
   if (a.out_dtype == LLMOE_DTYPE_FP32) {
 #pragma unroll
     for (int j = 0; j < 16; ++j)
-      if (j < n && first + lane < a.out)
+      if (list[j] >= 0 && first + lane < a.out)
         reinterpret_cast<float*>(a.y + list[j] * a.y_row)[first + lane] = v[j];
     return;
   }
@@ -239,27 +280,27 @@ __device__ __forceinline__ void store_plain(const ProductArgs& a, const float (&
 #pragma unroll
   for (int j = 0; j < 16; j += 2) {
     const float got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
-    const int col = odd ? j + 1 : j;
-    if (col < n && feature < a.out)
-      store2(a.y + list[col] * a.y_row + (uint64_t)feature * 2, odd ? got : v[j], odd ? v[j + 1] : got, a.out_dtype);
+    const int row = list[odd ? j + 1 : j];
+    if (row >= 0 && feature < a.out)
+      store2(a.y + row * a.y_row + (uint64_t)feature * 2, odd ? got : v[j], odd ? v[j + 1] : got, a.out_dtype);
   }
 }
 
-// 16 columns of 16 gate (lanes 0-15) and 16 up (lanes 16-31) features.  The
-// halves swap so that lanes 0-15 end with h of even columns and lanes 16-31 of
-// odd ones, for output feature first + lane % 16.
-// MX8 output: amax is the exchange's buffer, bar its barrier, parity its phase;
-// false when the wait expired.
+// 16 columns of 16 gate and 16 up features, eight of each in turn: lane l holds
+// gate (l & 8 == 0) or up of output feature first + l / 16 * 8 + l % 8.  The
+// two swap so that gate lanes end with h of even columns and up lanes of odd
+// ones.  MX8 output: amax is the exchange's buffer, bar its barrier, parity its
+// phase; false when the wait expired.
 __device__ __forceinline__ bool store_swiglu(const ProductArgs& a, const float (&v)[16], int first, const int* list,
-                                             int n, uint32_t* amax, int warp, uint32_t bar, uint32_t parity) {
-  const int lane = threadIdx.x & 31, half = lane >> 4;
+                                             uint32_t* amax, int warp, uint32_t bar, uint32_t parity) {
+  const int lane = threadIdx.x & 31, up = lane >> 3 & 1;
   float h[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float got = __shfl_xor_sync(0xffffffffu, half ? v[2 * i] : v[2 * i + 1], 16);
-    h[i] = half ? silu(got) * v[2 * i + 1] : silu(v[2 * i]) * got;
+    const float got = __shfl_xor_sync(0xffffffffu, up ? v[2 * i] : v[2 * i + 1], 8);
+    h[i] = up ? silu(got) * v[2 * i + 1] : silu(v[2 * i]) * got;
   }
-  const int feature = first + (lane & 15);
+  const int feature = first + (lane >> 4) * 8 + (lane & 7);
   if (a.out_dtype == LLMOE_DTYPE_MX8) {
     // a group of 32 outputs is this warp's 16 and its neighbour's: the two
     // exchange their largest magnitudes through shared memory
@@ -268,8 +309,9 @@ __device__ __forceinline__ bool store_swiglu(const ProductArgs& a, const float (
     for (int i = 0; i < 8; ++i) {
       m[i] = magnitude(h[i]);
 #pragma unroll
-      for (int d = 8; d; d >>= 1) m[i] = max(m[i], __shfl_xor_sync(0xffffffffu, m[i], d));
-      if ((lane & 15) == i) amax[warp * 16 + 2 * i + half] = m[i];
+      for (int d = 1; d <= 16; d <<= 1)
+        if (d != 8) m[i] = max(m[i], __shfl_xor_sync(0xffffffffu, m[i], d));
+      if ((lane & 7) == i && lane < 16) amax[warp * 16 + 2 * i + up] = m[i];
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
@@ -277,12 +319,12 @@ __device__ __forceinline__ bool store_swiglu(const ProductArgs& a, const float (
     const bool store = feature < a.out;  // whole groups: out is a multiple of 32
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int col = 2 * i + half;
+      const int col = 2 * i + up;
       const uint32_t code = scale_code(max(m[i], amax[(warp ^ 1) * 16 + col]));
-      if (col >= n || !store) continue;
+      if (list[col] < 0 || !store) continue;
       uint8_t* row = a.y + list[col] * a.y_row;
       row[feature] = (uint8_t)pack_e4m3x2(h[i] * scale_inverse(code), 0.0f);
-      if ((lane & 15) == 0 && !(warp & 1)) {
+      if ((lane & 23) == 0 && !(warp & 1)) {
         uint8_t* s = row + a.out + feature / 32;
         *s = (uint8_t)code;
         if (feature + 32 == a.out)
@@ -293,9 +335,10 @@ __device__ __forceinline__ bool store_swiglu(const ProductArgs& a, const float (
   }
   if (a.out_dtype == LLMOE_DTYPE_FP32) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (2 * i + half < n && feature < a.out)
-        reinterpret_cast<float*>(a.y + list[2 * i + half] * a.y_row)[feature] = h[i];
+    for (int i = 0; i < 8; ++i) {
+      const int row = list[2 * i + up];
+      if (row >= 0 && feature < a.out) reinterpret_cast<float*>(a.y + row * a.y_row)[feature] = h[i];
+    }
     return true;
   }
   const bool odd = lane & 1;
@@ -303,10 +346,9 @@ __device__ __forceinline__ bool store_swiglu(const ProductArgs& a, const float (
 #pragma unroll
   for (int i = 0; i < 8; i += 2) {
     const float got = __shfl_xor_sync(0xffffffffu, odd ? h[i] : h[i + 1], 1);
-    const int col = 2 * (odd ? i + 1 : i) + half;
-    if (col < n && even_feature < a.out)
-      store2(a.y + list[col] * a.y_row + (uint64_t)even_feature * 2, odd ? got : h[i], odd ? h[i + 1] : got,
-             a.out_dtype);
+    const int row = list[2 * (odd ? i + 1 : i) + up];
+    if (row >= 0 && even_feature < a.out)
+      store2(a.y + row * a.y_row + (uint64_t)even_feature * 2, odd ? got : h[i], odd ? h[i + 1] : got, a.out_dtype);
   }
   return true;
 }
@@ -315,9 +357,8 @@ __device__ __forceinline__ bool store_swiglu(const ProductArgs& a, const float (
 // the kernel
 // ---------------------------------------------------------------------------
 template <bool kMx, bool kSwiglu>
-__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
-    product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ CUtensorMap map_x,
-                   const __grid_constant__ CUtensorMap map_w) {
+__global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1, 1)
+    product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ ProductMaps maps) {
   using S = Shape<kMx>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
@@ -333,15 +374,18 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   int* prefix = reinterpret_cast<int*>(smem + l.prefix);
   const uint32_t full = sbase + l.bars, empty = full + 8 * kMaxStages, acc_full = empty + 8 * kMaxStages,
                  acc_empty = acc_full + 16, plan_full = acc_empty + 16, plan_empty = plan_full + 8 * kPlanDepth,
-                 halves = plan_empty + 8 * kPlanDepth;
+                 halves = plan_empty + 8 * kPlanDepth, scale_full = halves + 16, scale_empty = scale_full + 32;
 
   release_next_grid();
   if (threadIdx.x == 0) {
-    tma_prefetch_map(&map_x);
-    tma_prefetch_map(&map_w);
+    tma_prefetch_map(&maps.w);
     for (int s = 0; s < a.stages; ++s) {
-      mbar_init(full + 8 * s, kMx ? 3 : 1);  // the leader's bytes-expected, each CTA's scales
+      mbar_init(full + 8 * s, 1);
       mbar_init(empty + 8 * s, 1);
+    }
+    for (int s = 0; s < S::kSlots; ++s) {
+      mbar_init(scale_full + 8 * s, 8);  // the scale warps of both CTAs
+      mbar_init(scale_empty + 8 * s, 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(halves + 8 * b, 2);  // the two epilogue warps of an output group
@@ -350,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     }
     for (int p = 0; p < kPlanDepth; ++p) {
       mbar_init(plan_full + 8 * p, 1);
-      mbar_init(plan_empty + 8 * p, 5 + (leader ? 1 : 0) + (kMx ? 1 : 0));  // warps that read a plan
+      mbar_init(plan_empty + 8 * p, 5 + (leader ? 1 : 0) + (kMx ? 4 : 0));  // warps that read a plan
     }
     mbar_init_fence();
   }
@@ -374,25 +418,25 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       const int slot = i % kPlanDepth;
       if (!(ok = mbar_wait(plan_full + 8 * slot, (i / kPlanDepth) & 1, a.err))) break;
       const Tile tile = tiles[slot];
-      const int half = padded(tile.rows) / 2;  // rows this CTA loads
-      const int* list = rows + slot * S::kMaxRows + rank * half;
-      int4 r = make_int4(0, 0, 0, 0);
-      if (4 * lane < half) r = make_int4(list[4 * lane], list[4 * lane + 1], list[4 * lane + 2], list[4 * lane + 3]);
+      const int half = columns(tile.groups) / 2;  // columns each CTA loads
+      const int mine = max(0, min(tile.groups - (int)rank * (half / kGroup), half / kGroup));
+      const int row = lane < mine ? rows[slot * S::kMaxRows + rank * half + lane * kGroup] : 0;
+      const int box = plan_box(row, mine);
       __syncwarp();
       if (lane == 0) mbar_arrive(plan_empty + 8 * slot);
-      // first row of w per load: one load of 128 rows, or with gate and up
-      // eight of 16 rows, gate and up in turn, so that a tensor-memory lane and
-      // the lane 16 further hold gate and up of one output
-      const int feature = kSwiglu ? (lane & 1) * a.out + tile.block * 128 + (int)rank * 64 + (lane >> 1) * 16
-                                  : tile.block * kTileFeatures + (int)rank * 128;
+      const uint32_t bytes = 2 * S::kBytesA + tile.groups * (kGroup * 128);  // both CTAs'
       for (int k = 0; k < a.steps; ++k) {
         if (!(ok = mbar_wait(empty + 8 * stage, phase ^ 1, a.err))) break;
         const uint32_t data = sbase + stage * S::kStage, bar = map_rank(full + 8 * stage, 0);
         const int k0 = k * (kMx ? 128 : 64);
-        if (leader && lane == 0) mbar_expect_tx(full + 8 * stage, 2 * (S::kBytesA + half * 128));
-        __syncwarp();
-        if (lane < (kSwiglu ? 8 : 1)) tma_tile(data + (kSwiglu ? lane * 2048 : 0), &map_w, k0, feature, tile.expert, bar);
-        if (4 * lane < half) tma_gather4(data + S::kBytesA + lane * 512, &map_x, k0, r, bar);
+        if (lane == 0) {
+          if (leader) mbar_expect_tx(full + 8 * stage, bytes);
+          if constexpr (kSwiglu)
+            tma_tile5(data, &maps.w, k0, 0, 0, tile.block * 16 + (int)rank * 8, tile.expert, bar);
+          else
+            tma_tile3(data, &maps.w, k0, tile.block * kTileFeatures + (int)rank * 128, tile.expert, bar);
+        }
+        if (box >= 0) tma_rows(data + S::kBytesA + lane * (kGroup * 128), &maps.x[box], k0, row, bar);
         __syncwarp();
         if (++stage == a.stages) stage = 0, phase ^= 1;
       }
@@ -405,30 +449,33 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     }
   } else if (warp == 1 && leader) {
     // ---- products ------------------------------------------------------------
-    int stage = 0, i = 0;
-    uint32_t phase = 0;
+    int stage = 0, i = 0, sslot = 0, ring = 0;
+    uint32_t phase = 0, sphase = 0;
     bool ok = true;
     for (int t = pair; t < ntiles && ok; t += pairs, ++i) {
       const int slot = i % kPlanDepth, buf = i & 1;
       if (!(ok = mbar_wait(plan_full + 8 * slot, (i / kPlanDepth) & 1, a.err))) break;
-      const int n = padded(tiles[slot].rows);
+      const int n = columns(tiles[slot].groups);
       __syncwarp();
       if (lane == 0) mbar_arrive(plan_empty + 8 * slot);
       if (!(ok = mbar_wait(acc_empty + 8 * buf, ((i >> 1) & 1) ^ 1, a.err))) break;
       tc_fence_after();
       const uint32_t d = tmem + buf * S::kMaxRows, idesc = a.idesc | (uint32_t)(n >> 3) << 17;
       for (int k = 0; k < a.steps; ++k) {
+        const bool last = k == a.steps - 1;
+        if (kMx && (k & 3) == 0 && !(ok = mbar_wait(scale_full + 8 * sslot, sphase, a.err))) break;
         if (!(ok = mbar_wait(full + 8 * stage, phase, a.err))) break;
         tc_fence_after();
         if (lane == 0) {
           const uint32_t data = sbase + stage * S::kStage;
           const uint64_t da = tile_desc(data), db = tile_desc(data + S::kBytesA);
           if constexpr (kMx) {
-            const uint32_t sc = sbase + l.scales + stage * S::kScales;
-            const uint32_t ta = tmem + 2 * S::kMaxRows + stage * S::kScaleColumns, tb = ta + 4;
-            copy_scales(ta, scale_desc(sc));
-            copy_scales(tb, scale_desc(sc + 512));
-            if (n > 128) copy_scales(tb + 4, scale_desc(sc + 1024));
+            const uint32_t sa = sbase + l.scales + sslot * S::kSlot + (k & 3) * 512,
+                           sb = sbase + l.scales + sslot * S::kSlot + 2048 + (k & 3) * 1024;
+            const uint32_t ta = tmem + 2 * S::kMaxRows + ring * S::kScaleColumns, tb = ta + 4;
+            copy_scales(ta, scale_desc(sa));
+            copy_scales(tb, scale_desc(sb));
+            if (n > 128) copy_scales(tb + 4, scale_desc(sb + 512));
 #pragma unroll
             for (int j = 0; j < 4; ++j)  // 32 bytes of K; scale j of each row's four
               mma_mx8(d, da + 2 * j, db + 2 * j, idesc | (uint32_t)j << 4 | (uint32_t)j << 29, ta, tb, k > 0 || j > 0);
@@ -437,10 +484,16 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             for (int j = 0; j < 4; ++j) mma_16bit(d, da + 2 * j, db + 2 * j, idesc, k > 0 || j > 0);
           }
           mma_commit_pair(empty + 8 * stage);
-          if (k == a.steps - 1) mma_commit_pair(acc_full + 8 * buf);
+          if (kMx && ((k & 3) == 3 || last)) mma_commit_pair(scale_empty + 8 * sslot);
+          if (last) mma_commit_pair(acc_full + 8 * buf);
         }
         __syncwarp();
         if (++stage == a.stages) stage = 0, phase ^= 1;
+        if (kMx) {
+          ring = (ring + 1) % S::kScaleRing;
+          if ((k & 3) == 3 || last)
+            if (++sslot == S::kSlots) sslot = 0, sphase ^= 1;
+        }
       }
     }
   } else if (warp == 2) {
@@ -449,80 +502,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     for (int t = pair; t < ntiles; t += pairs, ++i) {
       const int slot = i % kPlanDepth;
       if (!mbar_wait(plan_empty + 8 * slot, ((i / kPlanDepth) & 1) ^ 1, a.err)) break;
-      plan_tile<kMx>(a, prefix, t, tiles + slot,
-                     rows + slot * S::kMaxRows);
+      plan_tile<kMx>(a, prefix, t, tiles + slot, rows + slot * S::kMaxRows);
       __syncwarp();
       if (lane == 0) mbar_arrive(plan_full + 8 * slot);
     }
-  } else if (warp == 3 && kMx) {
-    // ---- scales ------------------------------------------------------------------
-    // Lane l moves the scales of w rows l, l + 32, l + 64, l + 96 and of x rows
-    // l, l + 32, ...: 4 bytes of each row per stage, which together are the 16
-    // bytes that lane l's tensor-memory lane takes.  16 bytes of a row are read
-    // at a time, for four stages, one such chunk ahead.
-    int stage = 0, i = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    const int nscale = a.in / 32, chunks = (a.steps + 3) / 4;
-    for (int t = pair; t < ntiles && ok; t += pairs, ++i) {
-      const int slot = i % kPlanDepth;
-      if (!(ok = mbar_wait(plan_full + 8 * slot, (i / kPlanDepth) & 1, a.err))) break;
-      const Tile tile = tiles[slot];
-      const int n = padded(tile.rows);
-      const uint8_t* src[12];  // 4 rows of w, 8 of x
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int m = lane + 32 * j;  // row of this CTA's 128
-        int f = kSwiglu ? (m >> 4 & 1) * a.out + tile.block * 128 + (int)rank * 64 + (m >> 5) * 16 + (m & 15)
-                        : tile.block * kTileFeatures + (int)rank * 128 + m;
-        f = min(f, a.n - 1);  // past the expert's last row: its products are not stored
-        src[j] = a.w + ((uint64_t)tile.expert * a.n + f) * a.x_row + a.in;
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        src[4 + j] = a.x + rows[slot * S::kMaxRows + min(lane + 32 * j, n - 1)] * a.x_row + a.in;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(plan_empty + 8 * slot);
-      const int nx = n > 128 ? 12 : 8;
-      uint4 q[12];
-#pragma unroll
-      for (int j = 0; j < 12; ++j)
-        if (j < nx) q[j] = __ldg(reinterpret_cast<const uint4*>(src[j]));
-      for (int c = 0; c < chunks && ok; ++c) {
-        uint4 now[12];
-#pragma unroll
-        for (int j = 0; j < 12; ++j) now[j] = q[j];
-        if (c + 1 < chunks) {
-#pragma unroll
-          for (int j = 0; j < 12; ++j)
-            if (j < nx) q[j] = __ldg(reinterpret_cast<const uint4*>(src[j] + 16 * (c + 1)));
-        }
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const int k = 4 * c + b;
-          if (k >= a.steps || !ok) break;
-          // scales past the row's last are 1: the codes there are zeros, and 0 * NaN would not be
-          const int have = nscale - 4 * k;
-          const uint32_t keep = have >= 4 ? 0xffffffffu : (1u << 8 * have) - 1, fill = 0x7f7f7f7fu & ~keep;
-          uint32_t word[12];
-#pragma unroll
-          for (int j = 0; j < 12; ++j) {
-            const uint32_t u = b == 0 ? now[j].x : b == 1 ? now[j].y : b == 2 ? now[j].z : now[j].w;
-            word[j] = (u & keep) | fill;
-          }
-          if (!(ok = mbar_wait(empty + 8 * stage, phase ^ 1, a.err))) break;
-          uint4* dst = reinterpret_cast<uint4*>(smem + l.scales + stage * S::kScales) + lane;
-          dst[0] = make_uint4(word[0], word[1], word[2], word[3]);
-          dst[32] = make_uint4(word[4], word[5], word[6], word[7]);
-          if (n > 128) dst[64] = make_uint4(word[8], word[9], word[10], word[11]);
-          fence_async_shared();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(map_rank(full + 8 * stage, 0));
-          if (++stage == a.stages) stage = 0, phase ^= 1;
-        }
-      }
-    }
-  } else if (warp >= 4) {
+  } else if (warp >= 4 && warp < 8) {
     // ---- epilogue ------------------------------------------------------------------
     const int w = warp & 3;  // tensor-memory lanes 32 w ..
     uint32_t* amax = reinterpret_cast<uint32_t*>(smem + l.amax);
@@ -538,16 +522,16 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       tc_fence_after();
       const uint32_t acc = tmem + ((uint32_t)(32 * w) << 16) + buf * S::kMaxRows;
       bool ok = true;
-      for (int c = 0; c < tile.rows && ok; c += 16) {
+      for (int c = 0; c < tile.groups * kGroup && ok; c += 16) {
         float v[16];
         tmem_load16(acc + c, v);
         if constexpr (kSwiglu) {
           // two buffers in turn: a warp that fills one again has met its
           // neighbour at the other since, so the neighbour has read it
-          ok = store_swiglu(a, v, first, list + c, tile.rows - c, amax + 64 * flip, w, halves + 8 * (w >> 1), flip);
+          ok = store_swiglu(a, v, first, list + c, amax + 64 * flip, w, halves + 8 * (w >> 1), flip);
           flip ^= 1;
         } else {
-          store_plain(a, v, first, list + c, tile.rows - c);
+          store_plain(a, v, first, list + c);
         }
       }
       if (!ok) break;
@@ -557,6 +541,78 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         mbar_arrive_cluster(map_rank(acc_empty + 8 * buf, 0));
         mbar_arrive(plan_empty + 8 * slot);
       }
+    }
+  } else if (kMx && warp >= 8) {
+    // ---- scales ------------------------------------------------------------------
+    // Warp q's lane l moves the scales of row 32 q + l of the CTA's 128 rows of w
+    // and of columns 32 q + l and 128 + 32 q + l: 16 bytes of a row at a time,
+    // for four steps, kAhead such chunks ahead.  A step's scales of 128 rows are
+    // 32 lines of 16 bytes, line l holding rows l, l + 32, l + 64, l + 96: what
+    // lane l of tensor memory takes.
+    constexpr int kAhead = 3;
+    const int q = warp & 3, nscale = a.in / 32, chunks = (a.steps + 3) / 4;
+    int i = 0, sslot = 0;
+    uint32_t sphase = 0;
+    bool ok = true;
+    for (int t = pair; t < ntiles && ok; t += pairs, ++i) {
+      const int slot = i % kPlanDepth;
+      if (!(ok = mbar_wait(plan_full + 8 * slot, (i / kPlanDepth) & 1, a.err))) break;
+      const Tile tile = tiles[slot];
+      const int n = columns(tile.groups), m = 32 * q + lane;
+      const int f = min(kSwiglu ? (m >> 3 & 1) * a.out + tile.block * 128 + (int)rank * 64 + (m >> 4) * 8 + (m & 7)
+                                : tile.block * kTileFeatures + (int)rank * 128 + m,
+                        a.n - 1);  // past the expert's last row: its products are not stored
+      const int r0 = m < n ? rows[slot * S::kMaxRows + m] : -1;
+      const int r1 = 128 + m < n ? rows[slot * S::kMaxRows + 128 + m] : -1;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(plan_empty + 8 * slot);
+      const uint4* src[3] = {
+          reinterpret_cast<const uint4*>(a.w + ((uint64_t)tile.expert * a.n + f) * a.x_row + a.in),
+          reinterpret_cast<const uint4*>(a.x + (uint64_t)max(r0, 0) * a.x_row + a.in),
+          reinterpret_cast<const uint4*>(a.x + (uint64_t)max(r1, 0) * a.x_row + a.in)};
+      const bool have[3] = {true, r0 >= 0, r1 >= 0};
+      uint4 ahead[kAhead][3];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+          ahead[u][j] = make_uint4(0, 0, 0, 0);
+          if (have[j] && u < chunks) ahead[u][j] = __ldg(src[j] + u);
+        }
+      for (int c0 = 0; c0 < chunks && ok; c0 += kAhead) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          const int c = c0 + u;
+          if (c >= chunks || !ok) break;
+          if (!(ok = mbar_wait(scale_empty + 8 * sslot, sphase ^ 1, a.err))) break;
+          uint8_t* dst = smem + l.scales + sslot * S::kSlot + lane * 16 + q * 4;
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            // scales past the row's last are 1: the codes there are zeros, and 0 * NaN would not be
+            const int left = nscale - 4 * (4 * c + b);
+            const uint32_t keep = left >= 4 ? 0xffffffffu : left <= 0 ? 0u : (1u << 8 * left) - 1;
+#pragma unroll
+            for (int j = 0; j < 3; ++j) {
+              const uint4& v = ahead[u][j];
+              const uint32_t word = b == 0 ? v.x : b == 1 ? v.y : b == 2 ? v.z : v.w;
+              if (have[j])
+                *reinterpret_cast<uint32_t*>(dst + (j == 0 ? b * 512 : 2048 + b * 1024 + (j - 1) * 512)) =
+                    (word & keep) | (0x7f7f7f7fu & ~keep);
+            }
+          }
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(map_rank(scale_full + 8 * sslot, 0));
+          if (++sslot == S::kSlots) sslot = 0, sphase ^= 1;
+#pragma unroll
+          for (int j = 0; j < 3; ++j)
+            if (have[j] && c + kAhead < chunks) ahead[u][j] = __ldg(src[j] + c + kAhead);
+        }
+      }
+    }
+    for (int s = 0; s < S::kSlots && ok; ++s) {  // as the ring
+      ok = mbar_wait(scale_empty + 8 * sslot, sphase ^ 1, a.err);
+      if (++sslot == S::kSlots) sslot = 0, sphase ^= 1;
     }
   }
   __syncwarp();
@@ -590,7 +646,7 @@ int product_args(const void* x, const void* w, void* y, const int64_t* counts, i
     default: return LLMOE_ERR_INVALID_ARGUMENT;
   }
   const uint64_t xr = row_bytes(in, dtype), yr = row_bytes(out, out_dtype);
-  if (xr == 0 || yr == 0 || out > INT32_MAX / 2) return LLMOE_ERR_INVALID_ARGUMENT;
+  if (xr == 0 || yr == 0 || out > INT32_MAX / 2 || (swiglu && out % 8 != 0)) return LLMOE_ERR_INVALID_ARGUMENT;
   if (x == nullptr || w == nullptr || y == nullptr || !aligned(x, 16) || !aligned(w, 16) || !aligned(y, 16) ||
       !aligned(counts, 8))
     return LLMOE_ERR_INVALID_ARGUMENT;
@@ -659,7 +715,7 @@ bool make_map(CUtensorMap* m, const void* base, int dtype, const cuuint64_t* dim
   const CUtensorMapDataType type = dtype == LLMOE_DTYPE_BF16   ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                    : dtype == LLMOE_DTYPE_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                                : CU_TENSOR_MAP_DATA_TYPE_UINT8;
-  const cuuint32_t ones[3] = {1, 1, 1};
+  const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
   return encode(m, type, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, ones,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -683,7 +739,7 @@ int resident_pairs(size_t smem) {
   int n = 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * num_sms());
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(Shape<kMx>::kThreads);
   cfg.dynamicSmemBytes = smem;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -706,7 +762,9 @@ int launch_product(ProductArgs& a, llmoe_stream_t stream) {
   using S = Shape<kMx>;
   a.steps = (int)(((int64_t)a.in * (kMx ? 1 : 2) + 127) / 128);
   a.blocks = (a.n + kTileFeatures - 1) / kTileFeatures;
-  const uint64_t most = ((uint64_t)a.R * a.T + S::kMaxRows - 1) / S::kMaxRows * a.E * a.blocks;  // tiles at full counts
+  // tiles at full counts
+  const uint64_t groups = (uint64_t)((a.T + kGroup - 1) / kGroup) * a.R, share = S::kMaxRows / kGroup;
+  const uint64_t most = (groups + share - 1) / share * a.E * a.blocks;
   if (most > INT32_MAX) return LLMOE_ERR_INVALID_ARGUMENT;
   a.stages = S::kStages;
   while (smem_layout<kMx>(a.stages, a.E).total > kMaxSmem) --a.stages;
@@ -715,25 +773,31 @@ int launch_product(ProductArgs& a, llmoe_stream_t stream) {
   const uint32_t type = a.dtype == LLMOE_DTYPE_BF16 ? 1 : 0;
   a.idesc = (uint32_t)(kTileFeatures >> 4) << 24 | type << 7 | type << 10 | (kMx ? 1u << 23 : 1u << 4);
 
-  CUtensorMap map_x, map_w;
+  ProductMaps maps;
   const cuuint32_t k_box = kMx ? 128 : 64;
-  {
+  for (int b = 0; b < kBoxes; ++b) {
     const cuuint64_t dims[2] = {(cuuint64_t)a.in, (cuuint64_t)a.E * a.R * a.T}, strides[1] = {a.x_row};
-    const cuuint32_t box[2] = {k_box, 1};
-    if (!make_map(&map_x, a.x, a.dtype, dims, strides, box, 2)) return LLMOE_ERR_CUDA;
+    const cuuint32_t box[2] = {k_box, (cuuint32_t)kGroup << b};
+    if (!make_map(&maps.x[b], a.x, a.dtype, dims, strides, box, 2)) return LLMOE_ERR_CUDA;
   }
-  {
+  if (kSwiglu) {
+    // gate and up in turn, eight rows of each: a box is (K, 8 rows, gate / up, 8 such)
+    const cuuint64_t dims[5] = {(cuuint64_t)a.in, 8, 2, (cuuint64_t)a.out / 8, (cuuint64_t)a.E},
+                     strides[4] = {a.x_row, a.x_row * (uint64_t)a.out, a.x_row * 8, a.x_row * (uint64_t)a.n};
+    const cuuint32_t box[5] = {k_box, 8, 2, 8, 1};
+    if (!make_map(&maps.w, a.w, a.dtype, dims, strides, box, 5)) return LLMOE_ERR_CUDA;
+  } else {
     const cuuint64_t dims[3] = {(cuuint64_t)a.in, (cuuint64_t)a.n, (cuuint64_t)a.E},
                      strides[2] = {a.x_row, a.x_row * (uint64_t)a.n};
-    const cuuint32_t box[3] = {k_box, kSwiglu ? 16u : 128u, 1};
-    if (!make_map(&map_w, a.w, a.dtype, dims, strides, box, 3)) return LLMOE_ERR_CUDA;
+    const cuuint32_t box[3] = {k_box, 128, 1};
+    if (!make_map(&maps.w, a.w, a.dtype, dims, strides, box, 3)) return LLMOE_ERR_CUDA;
   }
   const int pairs = resident_pairs<kMx, kSwiglu>(smem);
   if (pairs < 1) return LLMOE_ERR_CUDA;
 
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * (unsigned)std::min<uint64_t>(most, pairs));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(S::kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = (cudaStream_t)stream;
   cudaLaunchAttribute attr[1];
@@ -741,7 +805,7 @@ int launch_product(ProductArgs& a, llmoe_stream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, product_kernel<kMx, kSwiglu>, a, map_x, map_w) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, product_kernel<kMx, kSwiglu>, a, maps) != cudaSuccess) {
     cudaGetLastError();
     return LLMOE_ERR_CUDA;
   }

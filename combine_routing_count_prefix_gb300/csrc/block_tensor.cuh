@@ -70,19 +70,26 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int32_t
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* m) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
 }
-__device__ __forceinline__ void tma_tile(uint32_t dst, const CUtensorMap* m, int k, int row, int group, uint32_t bar) {
+__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* m, int k, int row, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(m), "r"(k), "r"(row), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_tile3(uint32_t dst, const CUtensorMap* m, int k, int row, int group, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
       "l"(m), "r"(k), "r"(row), "r"(group), "r"(bar)
       : "memory");
 }
-// Four rows of any index, one after another at dst.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* m, int k, const int4& rows, uint32_t bar) {
+__device__ __forceinline__ void tma_tile5(uint32_t dst, const CUtensorMap* m, int k, int c1, int c2, int c3, int c4,
+                                          uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-      "l"(m), "r"(k), "r"(rows.x), "r"(rows.y), "r"(rows.z), "r"(rows.w), "r"(bar)
+      "l"(m), "r"(k), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar)
       : "memory");
 }
 // Makes this thread's shared-memory writes visible to the asynchronous proxy.

@@ -123,7 +123,8 @@ LLMOE_API int llmoe_topk_router(const void* logits, const float* bias, const uin
  *   bs      geometry: num_max_tokens, num_ranks, num_experts, and err; with
  *           counts NULL also base, rank_stride, hidden, dtype and set.
  * x, w, y 16-byte aligned; llmoe_row_bytes(in_features, dtype) and
- * llmoe_row_bytes(out_features, out_dtype) not 0; E * R * T < 2^31. */
+ * llmoe_row_bytes(out_features, out_dtype) not 0; out_features a multiple of
+ * 8 with LLMOE_PRODUCT_SWIGLU; E * R * T < 2^31. */
 LLMOE_API int llmoe_expert_product(const void* x, const void* w, void* y, const int64_t* counts, int in_features,
                                    int out_features, int dtype, int out_dtype, uint32_t flags,
                                    const llmoe_buf_set_t* bs, llmoe_stream_t stream);

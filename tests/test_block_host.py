@@ -81,7 +81,7 @@ def product(lib, bs=None, **kw):
     dict(n_in=0), dict(n_in=12), dict(n_out=0), dict(n_out=12), dict(n_in=-8), dict(n_out=-8), dict(dtype=2),
     dict(dtype=4), dict(out_dtype=1), dict(out_dtype=3), dict(dtype=1, out_dtype=0), dict(flags=2), dict(flags=4),
     dict(dtype=3, n_in=40), dict(dtype=3, out_dtype=3), dict(dtype=3, out_dtype=3, flags=1, n_out=40),
-    dict(dtype=3, out_dtype=4), dict(out_dtype=-1),
+    dict(dtype=3, out_dtype=4), dict(out_dtype=-1), dict(flags=1, out_dtype=2, n_out=20),
     dict(y=A), dict(y=A + 512), dict(y=2 * A), dict(y=2 * A + 4096), dict(n_out=2**30 + 8),
     dict(counts=None),  # and no rank buffers to read them from
 ])
