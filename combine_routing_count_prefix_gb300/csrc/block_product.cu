@@ -17,11 +17,10 @@
 //
 // Persistent pairs; every pair takes tiles pair, pair + pairs, ... of a list
 // that each CTA derives from the counts in its prologue.  Inside a CTA:
-//   warp 0      loads: one TMA box of w and a few of x per 128 bytes of K, into
-//               a ring
+//   warps 0, 3  load: one TMA box of w, and a few of x, per 128 bytes of K into
+//               a ring (warp 3 also allocates the tensor memory)
 //   warp 1      (first CTA of the pair) issues the products
 //   warp 2      plans: the tile's expert, features and received rows
-//   warp 3      allocates tensor memory
 //   warps 4-7   epilogue: sums from tensor memory, SwiGLU, rounding, stores,
 //               while the next tile's products run into the other accumulator
 //   warps 8-11  8-bit operands: move the scales to shared memory
@@ -98,6 +97,13 @@ __device__ __forceinline__ int bucket_groups(const ProductArgs& a, int e, int sr
 // A planned tile; its rows are in the plan's row list.
 struct __align__(16) Tile {
   int expert, block, groups;
+  int boxes;  // loads of x rows in this CTA
+};
+
+// One load of consecutive x rows: offset in the stage's rows, first row, and
+// the power of two of its groups.
+struct __align__(16) Box {
+  int offset, row, size, unused;
 };
 
 // Columns of a tile's product: a CTA pair's N is a multiple of 32.
@@ -105,7 +111,7 @@ __device__ __forceinline__ int columns(int groups) { return (groups * kGroup + 3
 
 // Byte offsets in dynamic shared memory, from its first 1024-byte boundary.
 struct SmemLayout {
-  uint32_t scales, rows, tiles, amax, bars, tmem, part, prefix, total;
+  uint32_t scales, boxes, rows, tiles, amax, bars, tmem, part, prefix, total;
 };
 template <bool kMx>
 __host__ __device__ inline SmemLayout smem_layout(int stages, int E) {
@@ -113,6 +119,7 @@ __host__ __device__ inline SmemLayout smem_layout(int stages, int E) {
   SmemLayout l;
   uint32_t at = stages * S::kStage;
   l.scales = at, at += S::kSlots * S::kSlot;
+  l.boxes = at, at += kPlanDepth * 32 * 16;
   l.rows = at, at += kPlanDepth * S::kMaxRows * 4;
   l.tiles = at, at += kPlanDepth * 16;
   l.amax = at, at += 2 * 4 * 16 * 4;
@@ -202,27 +209,6 @@ __device__ void plan_rows(const ProductArgs& a, int e, int g0, int g1, int* list
   for (int i = (g1 - g0) * kGroup + lane; i < columns(g1 - g0); i += 32) list[i] = -1;
 }
 
-template <bool kMx>
-__device__ void plan_tile(const ProductArgs& a, const int* prefix, int t, Tile* tile, int* list) {
-  constexpr int kMaxRows = Shape<kMx>::kMaxRows;
-  const int lane = threadIdx.x & 31;
-  int lo = 0, hi = a.E - 1;  // the largest e with prefix[e] <= t: it has tiles, for t < prefix[e + 1]
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (prefix[mid] <= t) lo = mid; else hi = mid - 1;
-  }
-  const int e = lo, shares = (prefix[e + 1] - prefix[e]) / a.blocks;
-  const int local = t - prefix[e], share = local % shares;
-  int total = 0;
-  for (int s = lane; s < a.R; s += 32) total += bucket_groups(a, e, s);
-  total = __reduce_add_sync(0xffffffffu, total);
-  // equal shares: an expert of 300 rows is two tiles of 150
-  const int g0 = (int)((int64_t)total * share / shares), g1 = (int)((int64_t)total * (share + 1) / shares);
-  static_assert(kMaxRows % 32 == 0, "a share of at most kMaxRows rows pads to at most kMaxRows");
-  plan_rows(a, e, g0, g1, list);
-  if (lane == 0) *tile = Tile{e, local / shares, g1 - g0};
-}
-
 // The box that starts at this lane's group, as the power of two of its groups,
 // or -1: the CTA's share of a tile is `groups` groups, lane g's starting at row
 // `row`; runs of consecutive rows are cut into boxes, largest first.
@@ -242,6 +228,34 @@ __device__ __forceinline__ int plan_box(int row, int groups) {
       at += 1 << b;
     }
   return box;
+}
+
+template <bool kMx>
+__device__ void plan_tile(const ProductArgs& a, const int* prefix, int t, int rank, Tile* tile, int* list, Box* boxes) {
+  constexpr int kMaxRows = Shape<kMx>::kMaxRows;
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = a.E - 1;  // the largest e with prefix[e] <= t: it has tiles, for t < prefix[e + 1]
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (prefix[mid] <= t) lo = mid; else hi = mid - 1;
+  }
+  const int e = lo, shares = (prefix[e + 1] - prefix[e]) / a.blocks;
+  const int local = t - prefix[e], share = local % shares;
+  int total = 0;
+  for (int s = lane; s < a.R; s += 32) total += bucket_groups(a, e, s);
+  total = __reduce_add_sync(0xffffffffu, total);
+  // equal shares: an expert of 300 rows is two tiles of 150
+  const int g0 = (int)((int64_t)total * share / shares), g1 = (int)((int64_t)total * (share + 1) / shares);
+  static_assert(kMaxRows % 32 == 0, "a share of at most kMaxRows rows pads to at most kMaxRows");
+  plan_rows(a, e, g0, g1, list);
+  __syncwarp();
+  // this CTA's half of the columns
+  const int half = columns(g1 - g0) / 2, mine = max(0, min(g1 - g0 - rank * (half / kGroup), half / kGroup));
+  const int row = lane < mine ? list[rank * half + lane * kGroup] : 0;
+  const int box = plan_box(row, mine);
+  const uint32_t all = __ballot_sync(0xffffffffu, box >= 0);
+  if (box >= 0) boxes[__popc(all & ((1u << lane) - 1))] = Box{lane * (kGroup * 128), row, box, 0};
+  if (lane == 0) *tile = Tile{e, local / shares, g1 - g0, __popc(all)};
 }
 
 // ---------------------------------------------------------------------------
@@ -370,6 +384,7 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
   const bool leader = rank == 0;
 
   int* rows = reinterpret_cast<int*>(smem + l.rows);
+  Box* boxes = reinterpret_cast<Box*>(smem + l.boxes);
   Tile* tiles = reinterpret_cast<Tile*>(smem + l.tiles);
   int* prefix = reinterpret_cast<int*>(smem + l.prefix);
   const uint32_t full = sbase + l.bars, empty = full + 8 * kMaxStages, acc_full = empty + 8 * kMaxStages,
@@ -394,7 +409,7 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
     }
     for (int p = 0; p < kPlanDepth; ++p) {
       mbar_init(plan_full + 8 * p, 1);
-      mbar_init(plan_empty + 8 * p, 5 + (leader ? 1 : 0) + (kMx ? 4 : 0));  // warps that read a plan
+      mbar_init(plan_empty + 8 * p, 6 + (leader ? 1 : 0) + (kMx ? 4 : 0));  // warps that read a plan
     }
     mbar_init_fence();
   }
@@ -410,42 +425,71 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, ntiles = prefix[a.E];
 
   if (warp == 0) {
-    // ---- loads -------------------------------------------------------------
+    // ---- loads of w: one thread ---------------------------------------------------
     int stage = 0, i = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (int t = pair; t < ntiles && ok; t += pairs, ++i) {
-      const int slot = i % kPlanDepth;
-      if (!(ok = mbar_wait(plan_full + 8 * slot, (i / kPlanDepth) & 1, a.err))) break;
-      const Tile tile = tiles[slot];
-      const int half = columns(tile.groups) / 2;  // columns each CTA loads
-      const int mine = max(0, min(tile.groups - (int)rank * (half / kGroup), half / kGroup));
-      const int row = lane < mine ? rows[slot * S::kMaxRows + rank * half + lane * kGroup] : 0;
-      const int box = plan_box(row, mine);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(plan_empty + 8 * slot);
-      const uint32_t bytes = 2 * S::kBytesA + tile.groups * (kGroup * 128);  // both CTAs'
-      for (int k = 0; k < a.steps; ++k) {
-        if (!(ok = mbar_wait(empty + 8 * stage, phase ^ 1, a.err))) break;
-        const uint32_t data = sbase + stage * S::kStage, bar = map_rank(full + 8 * stage, 0);
-        const int k0 = k * (kMx ? 128 : 64);
-        if (lane == 0) {
+    if (elect_one()) {
+      for (int t = pair; t < ntiles && ok; t += pairs, ++i) {
+        const int slot = i % kPlanDepth;
+        if (!(ok = mbar_wait(plan_full + 8 * slot, (i / kPlanDepth) & 1, a.err))) break;
+        const Tile tile = tiles[slot];
+        mbar_arrive(plan_empty + 8 * slot);
+        const uint32_t bytes = 2 * S::kBytesA + tile.groups * (kGroup * 128);  // both CTAs', w and x
+        for (int k = 0; k < a.steps; ++k) {
+          if (!(ok = mbar_wait(empty + 8 * stage, phase ^ 1, a.err))) break;
+          const uint32_t data = sbase + stage * S::kStage, bar = map_rank(full + 8 * stage, 0);
+          const int k0 = k * (kMx ? 128 : 64);
           if (leader) mbar_expect_tx(full + 8 * stage, bytes);
           if constexpr (kSwiglu)
             tma_tile5(data, &maps.w, k0, 0, 0, tile.block * 16 + (int)rank * 8, tile.expert, bar);
           else
             tma_tile3(data, &maps.w, k0, tile.block * kTileFeatures + (int)rank * 128, tile.expert, bar);
+          if (++stage == a.stages) stage = 0, phase ^= 1;
         }
-        if (box >= 0) tma_rows(data + S::kBytesA + lane * (kGroup * 128), &maps.x[box], k0, row, bar);
-        __syncwarp();
+      }
+      // the ring drains: no product reads shared memory, and no arrival is under
+      // way to this CTA, once every stage has been handed back
+      for (int s = 0; s < a.stages && ok; ++s) {
+        ok = mbar_wait(empty + 8 * stage, phase ^ 1, a.err);
         if (++stage == a.stages) stage = 0, phase ^= 1;
       }
     }
-    // the ring drains: no product reads shared memory, and no arrival is under
-    // way to this CTA, once every stage has been handed back
-    for (int s = 0; s < a.stages && ok; ++s) {
-      ok = mbar_wait(empty + 8 * stage, phase ^ 1, a.err);
-      if (++stage == a.stages) stage = 0, phase ^= 1;
+  } else if (warp == 3) {
+    // ---- loads of x: one thread ---------------------------------------------------
+    int stage = 0, i = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    if (elect_one()) {
+      for (int t = pair; t < ntiles && ok; t += pairs, ++i) {
+        const int slot = i % kPlanDepth;
+        if (!(ok = mbar_wait(plan_full + 8 * slot, (i / kPlanDepth) & 1, a.err))) break;
+        const int n = tiles[slot].boxes;
+        // the first boxes stay in registers: read from shared memory at every
+        // step, each load would wait for its box
+        constexpr int kKept = 6;
+        Box kept[kKept];
+#pragma unroll
+        for (int b = 0; b < kKept; ++b) kept[b] = b < n ? boxes[32 * slot + b] : Box{};
+        for (int k = 0; k < a.steps; ++k) {
+          if (!(ok = mbar_wait(empty + 8 * stage, phase ^ 1, a.err))) break;
+          const uint32_t data = sbase + stage * S::kStage + S::kBytesA, bar = map_rank(full + 8 * stage, 0);
+          const int k0 = k * (kMx ? 128 : 64);
+#pragma unroll
+          for (int b = 0; b < kKept; ++b)
+            if (b < n) tma_rows(data + kept[b].offset, &maps.x[kept[b].size], k0, kept[b].row, bar);
+          for (int b = kKept; b < n; b += 4) {
+            Box q[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) q[u] = b + u < n ? boxes[32 * slot + b + u] : Box{};
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              if (b + u < n) tma_rows(data + q[u].offset, &maps.x[q[u].size], k0, q[u].row, bar);
+          }
+          if (++stage == a.stages) stage = 0, phase ^= 1;
+        }
+        mbar_arrive(plan_empty + 8 * slot);
+      }
     }
   } else if (warp == 1 && leader) {
     // ---- products ------------------------------------------------------------
@@ -466,7 +510,7 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
         if (kMx && (k & 3) == 0 && !(ok = mbar_wait(scale_full + 8 * sslot, sphase, a.err))) break;
         if (!(ok = mbar_wait(full + 8 * stage, phase, a.err))) break;
         tc_fence_after();
-        if (lane == 0) {
+        if (elect_one()) {
           const uint32_t data = sbase + stage * S::kStage;
           const uint64_t da = tile_desc(data), db = tile_desc(data + S::kBytesA);
           if constexpr (kMx) {
@@ -502,7 +546,7 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
     for (int t = pair; t < ntiles; t += pairs, ++i) {
       const int slot = i % kPlanDepth;
       if (!mbar_wait(plan_empty + 8 * slot, ((i / kPlanDepth) & 1) ^ 1, a.err)) break;
-      plan_tile<kMx>(a, prefix, t, tiles + slot, rows + slot * S::kMaxRows);
+      plan_tile<kMx>(a, prefix, t, (int)rank, tiles + slot, rows + slot * S::kMaxRows, boxes + 32 * slot);
       __syncwarp();
       if (lane == 0) mbar_arrive(plan_full + 8 * slot);
     }
