@@ -21,9 +21,9 @@
 //               a ring (warp 3 also allocates the tensor memory)
 //   warp 1      (first CTA of the pair) issues the products
 //   warp 2      plans: the tile's expert, features and received rows
-//   warps 4-7   epilogue: sums from tensor memory, SwiGLU, rounding, stores,
+//   warps 4-11  epilogue: sums from tensor memory, SwiGLU, rounding, stores,
 //               while the next tile's products run into the other accumulator
-//   warps 8-11  8-bit operands: move the scales to shared memory
+//   warps 12-15 8-bit operands: move the scales to shared memory
 // Every wait is bounded (kSpinLimit cycles); on expiry the role records
 // LLMOE_DEV_TIMEOUT and leaves its loop, the others follow when their own waits
 // expire, and all meet at the end to free the tensor memory.  A copy in flight
@@ -42,7 +42,7 @@ constexpr int kBoxes = 6;           // x loads of 1, 2, .. 32 groups
 // bytes of K: 64 values of 16 bits or 128 of 8 bits).
 template <bool kMx>
 struct Shape {
-  static constexpr int kThreads = kMx ? 384 : 256;
+  static constexpr int kThreads = kMx ? 512 : 384;
   // two accumulators of kMaxRows columns
   static constexpr int kMaxRows = kMx ? 192 : 256;
   static constexpr int kBytesA = 128 * 128, kBytesB = kMaxRows / 2 * 128;
@@ -98,6 +98,7 @@ __device__ __forceinline__ int bucket_groups(const ProductArgs& a, int e, int sr
 struct __align__(16) Tile {
   int expert, block, groups;
   int boxes;  // loads of x rows in this CTA
+  int bytes;  // that the loads of x rows of both CTAs bring
 };
 
 // One load of consecutive x rows: offset in the stage's rows, first row, and
@@ -121,9 +122,9 @@ __host__ __device__ inline SmemLayout smem_layout(int stages, int E) {
   l.scales = at, at += S::kSlots * S::kSlot;
   l.boxes = at, at += kPlanDepth * 32 * 16;
   l.rows = at, at += kPlanDepth * S::kMaxRows * 4;
-  l.tiles = at, at += kPlanDepth * 16;
-  l.amax = at, at += 2 * 4 * 16 * 4;
-  l.bars = at, at += (2 * kMaxStages + 4 + 2 * kPlanDepth + 2 + 2 * 4) * 8;
+  l.tiles = at, at += kPlanDepth * (uint32_t)sizeof(Tile);
+  l.amax = at, at += 2 * 8 * 16 * 4;
+  l.bars = at, at += (2 * kMaxStages + 4 + 2 * kPlanDepth + 4 + 2 * 4) * 8;
   l.tmem = at, at += 16;
   l.part = at, at += 64;
   l.prefix = at, at += (E + 1) * 4;
@@ -210,8 +211,10 @@ __device__ void plan_rows(const ProductArgs& a, int e, int g0, int g1, int* list
 }
 
 // The box that starts at this lane's group, as the power of two of its groups,
-// or -1: the CTA's share of a tile is `groups` groups, lane g's starting at row
-// `row`; runs of consecutive rows are cut into boxes, largest first.
+// or -1: a CTA's share of a tile is `groups` groups, lane g's starting at row
+// `row`.  A run of consecutive rows is one box, or two of the same size that
+// overlap where its length is no power of two (the rows in both are written
+// twice, with the same values): loads are bound by their number.
 __device__ __forceinline__ int plan_box(int row, int groups) {
   const int lane = threadIdx.x & 31;
   const int prev = __shfl_up_sync(0xffffffffu, row, 1);
@@ -220,14 +223,8 @@ __device__ __forceinline__ int plan_box(int row, int groups) {
   const int head = 31 - __clz(heads & (0xffffffffu >> (31 - lane)));
   const uint32_t later = lane == 31 ? 0 : heads >> (lane + 1);
   const int len = (later ? lane + __ffs(later) : groups) - head, p = lane - head;
-  int box = -1, at = 0;
-#pragma unroll
-  for (int b = kBoxes - 1; b >= 0; --b)
-    if (len >> b & 1) {
-      if (p == at) box = b;
-      at += 1 << b;
-    }
-  return box;
+  const int size = 31 - __clz(len);
+  return p == 0 || p == len - (1 << size) ? size : -1;
 }
 
 template <bool kMx>
@@ -249,13 +246,22 @@ __device__ void plan_tile(const ProductArgs& a, const int* prefix, int t, int ra
   static_assert(kMaxRows % 32 == 0, "a share of at most kMaxRows rows pads to at most kMaxRows");
   plan_rows(a, e, g0, g1, list);
   __syncwarp();
-  // this CTA's half of the columns
-  const int half = columns(g1 - g0) / 2, mine = max(0, min(g1 - g0 - rank * (half / kGroup), half / kGroup));
-  const int row = lane < mine ? list[rank * half + lane * kGroup] : 0;
-  const int box = plan_box(row, mine);
-  const uint32_t all = __ballot_sync(0xffffffffu, box >= 0);
-  if (box >= 0) boxes[__popc(all & ((1u << lane) - 1))] = Box{lane * (kGroup * 128), row, box, 0};
-  if (lane == 0) *tile = Tile{e, local / shares, g1 - g0, __popc(all)};
+  // the loads of each CTA's half of the columns
+  const int half = columns(g1 - g0) / 2;
+  int bytes = 0, count = 0;
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const int mine = max(0, min(g1 - g0 - r * (half / kGroup), half / kGroup));
+    const int row = lane < mine ? list[r * half + lane * kGroup] : 0;
+    const int box = plan_box(row, mine);
+    const uint32_t all = __ballot_sync(0xffffffffu, box >= 0);
+    bytes += __reduce_add_sync(0xffffffffu, box >= 0 ? kGroup * 128 << box : 0);
+    if (r == rank) {
+      count = __popc(all);
+      if (box >= 0) boxes[__popc(all & ((1u << lane) - 1))] = Box{lane * (kGroup * 128), row, box, 0};
+    }
+  }
+  if (lane == 0) *tile = Tile{e, local / shares, g1 - g0, count, bytes};
 }
 
 // ---------------------------------------------------------------------------
@@ -389,7 +395,7 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
   int* prefix = reinterpret_cast<int*>(smem + l.prefix);
   const uint32_t full = sbase + l.bars, empty = full + 8 * kMaxStages, acc_full = empty + 8 * kMaxStages,
                  acc_empty = acc_full + 16, plan_full = acc_empty + 16, plan_empty = plan_full + 8 * kPlanDepth,
-                 halves = plan_empty + 8 * kPlanDepth, scale_full = halves + 16, scale_empty = scale_full + 32;
+                 halves = plan_empty + 8 * kPlanDepth, scale_full = halves + 32, scale_empty = scale_full + 32;
 
   release_next_grid();
   if (threadIdx.x == 0) {
@@ -399,17 +405,18 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
       mbar_init(empty + 8 * s, 1);
     }
     for (int s = 0; s < S::kSlots; ++s) {
-      mbar_init(scale_full + 8 * s, 8);  // the scale warps of both CTAs
+      // this CTA's scale warps; in the first CTA also the other's relay
+      mbar_init(scale_full + 8 * s, leader ? 5 : 4);
       mbar_init(scale_empty + 8 * s, 1);
     }
+    for (int b = 0; b < 4; ++b) mbar_init(halves + 8 * b, 2);  // the two epilogue warps of an output group
     for (int b = 0; b < 2; ++b) {
-      mbar_init(halves + 8 * b, 2);  // the two epilogue warps of an output group
       mbar_init(acc_full + 8 * b, 1);
-      mbar_init(acc_empty + 8 * b, 8);  // the epilogue warps of both CTAs
+      mbar_init(acc_empty + 8 * b, 16);  // the epilogue warps of both CTAs
     }
     for (int p = 0; p < kPlanDepth; ++p) {
       mbar_init(plan_full + 8 * p, 1);
-      mbar_init(plan_empty + 8 * p, 6 + (leader ? 1 : 0) + (kMx ? 4 : 0));  // warps that read a plan
+      mbar_init(plan_empty + 8 * p, 10 + (leader ? 1 : 0) + (kMx ? 4 : 0));  // warps that read a plan
     }
     mbar_init_fence();
   }
@@ -435,7 +442,7 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
         if (!(ok = mbar_wait(plan_full + 8 * slot, (i / kPlanDepth) & 1, a.err))) break;
         const Tile tile = tiles[slot];
         mbar_arrive(plan_empty + 8 * slot);
-        const uint32_t bytes = 2 * S::kBytesA + tile.groups * (kGroup * 128);  // both CTAs', w and x
+        const uint32_t bytes = 2 * S::kBytesA + tile.bytes;  // both CTAs', w and x
         for (int k = 0; k < a.steps; ++k) {
           if (!(ok = mbar_wait(empty + 8 * stage, phase ^ 1, a.err))) break;
           const uint32_t data = sbase + stage * S::kStage, bar = map_rank(full + 8 * stage, 0);
@@ -540,6 +547,19 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
         }
       }
     }
+  } else if (kMx && warp == 1) {
+    // ---- relay: this CTA's scales are in place, told to the first CTA ---------------
+    // (by a thread with no loads of its own: publishing to the cluster waits for
+    // them, 2600 cycles at a time in the scale warps)
+    int sslot = 0;
+    uint32_t sphase = 0;
+    bool ok = true;
+    for (int t = pair; t < ntiles && ok; t += pairs)
+      for (int c = 0; c < (a.steps + 3) / 4; ++c) {
+        if (!(ok = mbar_wait(scale_full + 8 * sslot, sphase, a.err))) break;
+        if (elect_one()) mbar_arrive_cluster(map_rank(scale_full + 8 * sslot, 0));
+        if (++sslot == S::kSlots) sslot = 0, sphase ^= 1;
+      }
   } else if (warp == 2) {
     // ---- plan ------------------------------------------------------------------
     int i = 0;
@@ -550,10 +570,11 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
       __syncwarp();
       if (lane == 0) mbar_arrive(plan_full + 8 * slot);
     }
-  } else if (warp >= 4 && warp < 8) {
+  } else if (warp >= 4 && warp < 12) {
     // ---- epilogue ------------------------------------------------------------------
-    const int w = warp & 3;  // tensor-memory lanes 32 w ..
-    uint32_t* amax = reinterpret_cast<uint32_t*>(smem + l.amax);
+    // two sets of four warps, each taking every other 16 columns
+    const int w = warp & 3, set = warp >= 8;  // tensor-memory lanes 32 w ..
+    uint32_t* amax = reinterpret_cast<uint32_t*>(smem + l.amax) + set * 128;
     int i = 0, flip = 0;
     for (int t = pair; t < ntiles; t += pairs, ++i) {
       const int slot = i % kPlanDepth, buf = i & 1;
@@ -566,13 +587,13 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
       tc_fence_after();
       const uint32_t acc = tmem + ((uint32_t)(32 * w) << 16) + buf * S::kMaxRows;
       bool ok = true;
-      for (int c = 0; c < tile.groups * kGroup && ok; c += 16) {
+      for (int c = 16 * set; c < tile.groups * kGroup && ok; c += 32) {
         float v[16];
         tmem_load16(acc + c, v);
         if constexpr (kSwiglu) {
           // two buffers in turn: a warp that fills one again has met its
           // neighbour at the other since, so the neighbour has read it
-          ok = store_swiglu(a, v, first, list + c, amax + 64 * flip, w, halves + 8 * (w >> 1), flip);
+          ok = store_swiglu(a, v, first, list + c, amax + 64 * flip, w, halves + 8 * (2 * set + (w >> 1)), flip);
           flip ^= 1;
         } else {
           store_plain(a, v, first, list + c);
@@ -582,11 +603,11 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive_cluster(map_rank(acc_empty + 8 * buf, 0));
+        mbar_arrive_read(map_rank(acc_empty + 8 * buf, 0));
         mbar_arrive(plan_empty + 8 * slot);
       }
     }
-  } else if (kMx && warp >= 8) {
+  } else if (kMx && warp >= 12) {
     // ---- scales ------------------------------------------------------------------
     // Warp q's lane l moves the scales of row 32 q + l of the CTA's 128 rows of w
     // and of columns 32 q + l and 128 + 32 q + l: 16 bytes of a row at a time,
@@ -646,7 +667,7 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
           }
           fence_async_shared();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(map_rank(scale_full + 8 * sslot, 0));
+          if (lane == 0) mbar_arrive(scale_full + 8 * sslot);
           if (++sslot == S::kSlots) sslot = 0, sphase ^= 1;
 #pragma unroll
           for (int j = 0; j < 3; ++j)

@@ -45,7 +45,13 @@ __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// bar: an address of the cluster's window (map_rank), so possibly the peer's.
+// Arrival on a barrier of the cluster's window (map_rank), possibly the peer's:
+// for what this thread has read (tensor memory), nothing written is published ...
+__device__ __forceinline__ void mbar_arrive_read(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// ... or publishing writes to the cluster, which waits for all of the thread's
+// loads and stores in flight.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
