@@ -181,31 +181,46 @@ __device__ void count_tiles(const ProductArgs& a, int* prefix, int* part) {
 // ---------------------------------------------------------------------------
 // plan: one warp turns a tile's number into its expert, features and rows
 // ---------------------------------------------------------------------------
+// One expert's buckets, 32 source ranks at a time: lane s holds rank s0 + s's
+// rows, and the groups of the ranks up to and with it.
+struct Buckets {
+  int expert, s0;
+  int rows, incl;
+};
+__device__ __forceinline__ void load_buckets(const ProductArgs& a, int e, int s0, Buckets& b) {
+  if (b.expert == e && b.s0 == s0) return;  // the previous tile's
+  const int lane = threadIdx.x & 31;
+  b.expert = e;
+  b.s0 = s0;
+  b.rows = s0 + lane < a.R ? bucket_count(a, e, s0 + lane) : 0;
+  b.incl = (b.rows + kGroup - 1) / kGroup;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, b.incl, d);
+    if (lane >= d) b.incl += v;
+  }
+}
+
 // Groups of expert e in order: source ranks ascending, slots ascending.  The
 // tile's share [g0, g1) goes to list, one entry per column: the row of x and y,
 // or -1 where there is none.
-__device__ void plan_rows(const ProductArgs& a, int e, int g0, int g1, int* list) {
+__device__ void plan_rows(const ProductArgs& a, int e, int g0, int g1, Buckets& b, int* list) {
   const int lane = threadIdx.x & 31;
   int before = 0;
   for (int s0 = 0; s0 < a.R && before < g1; s0 += 32) {
-    const int c = s0 + lane < a.R ? bucket_count(a, e, s0 + lane) : 0, g = (c + kGroup - 1) / kGroup;
-    int incl = g;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, d);
-      if (lane >= d) incl += v;
-    }
-    const int n = min(32, a.R - s0);
-    for (int j = 0; j < n; ++j) {
-      const int end = before + __shfl_sync(0xffffffffu, incl, j), cnt = __shfl_sync(0xffffffffu, c, j);
-      const int beg = end - (cnt + kGroup - 1) / kGroup, lo = max(beg, g0), hi = min(end, g1);
-      const int first = (e * a.R + s0 + j) * a.T;
+    load_buckets(a, e, s0, b);
+    const int end = before + b.incl, beg = end - (b.rows + kGroup - 1) / kGroup;
+    for (uint32_t left = __ballot_sync(0xffffffffu, max(beg, g0) < min(end, g1)); left; left &= left - 1) {
+      const int j = __ffs(left) - 1;
+      const int jbeg = __shfl_sync(0xffffffffu, beg, j), jend = __shfl_sync(0xffffffffu, end, j),
+                cnt = __shfl_sync(0xffffffffu, b.rows, j);
+      const int lo = max(jbeg, g0), hi = min(jend, g1), first = (e * a.R + s0 + j) * a.T;
       for (int i = lo * kGroup + lane; i < hi * kGroup; i += 32) {
-        const int slot = i - beg * kGroup;
+        const int slot = i - jbeg * kGroup;
         list[i - g0 * kGroup] = slot < cnt ? first + slot : -1;
       }
     }
-    before += __shfl_sync(0xffffffffu, incl, 31);
+    before += __shfl_sync(0xffffffffu, b.incl, 31);
   }
   for (int i = (g1 - g0) * kGroup + lane; i < columns(g1 - g0); i += 32) list[i] = -1;
 }
@@ -228,7 +243,8 @@ __device__ __forceinline__ int plan_box(int row, int groups) {
 }
 
 template <bool kMx>
-__device__ void plan_tile(const ProductArgs& a, const int* prefix, int t, int rank, Tile* tile, int* list, Box* boxes) {
+__device__ void plan_tile(const ProductArgs& a, const int* prefix, int t, int rank, Buckets& b, Tile* tile, int* list,
+                          Box* boxes) {
   constexpr int kMaxRows = Shape<kMx>::kMaxRows;
   const int lane = threadIdx.x & 31;
   int lo = 0, hi = a.E - 1;  // the largest e with prefix[e] <= t: it has tiles, for t < prefix[e + 1]
@@ -239,12 +255,21 @@ __device__ void plan_tile(const ProductArgs& a, const int* prefix, int t, int ra
   const int e = lo, shares = (prefix[e + 1] - prefix[e]) / a.blocks;
   const int local = t - prefix[e], share = local % shares;
   int total = 0;
-  for (int s = lane; s < a.R; s += 32) total += bucket_groups(a, e, s);
-  total = __reduce_add_sync(0xffffffffu, total);
-  // equal shares: an expert of 300 rows is two tiles of 150
-  const int g0 = (int)((int64_t)total * share / shares), g1 = (int)((int64_t)total * (share + 1) / shares);
+  if (a.R <= 32) {
+    load_buckets(a, e, 0, b);
+    total = __shfl_sync(0xffffffffu, b.incl, 31);
+  } else {
+    for (int s = lane; s < a.R; s += 32) total += bucket_groups(a, e, s);
+    total = __reduce_add_sync(0xffffffffu, total);
+  }
+  // shares of whole 32s of columns, as equal as that allows, the remainder
+  // last: 1040 rows are 4 x 224 + 144 columns, 1056 as padded (five equal
+  // shares would pad to 1120).  shares is the fewest that hold the total, so the
+  // last is never empty.
+  const int per = columns((total + shares - 1) / shares) / kGroup;
+  const int g0 = share * per, g1 = min(total, g0 + per);
   static_assert(kMaxRows % 32 == 0, "a share of at most kMaxRows rows pads to at most kMaxRows");
-  plan_rows(a, e, g0, g1, list);
+  plan_rows(a, e, g0, g1, b, list);
   __syncwarp();
   // the loads of each CTA's half of the columns
   const int half = columns(g1 - g0) / 2;
@@ -405,8 +430,7 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
       mbar_init(empty + 8 * s, 1);
     }
     for (int s = 0; s < S::kSlots; ++s) {
-      // this CTA's scale warps; in the first CTA also the other's relay
-      mbar_init(scale_full + 8 * s, leader ? 5 : 4);
+      mbar_init(scale_full + 8 * s, 8);  // the scale warps of both CTAs
       mbar_init(scale_empty + 8 * s, 1);
     }
     for (int b = 0; b < 4; ++b) mbar_init(halves + 8 * b, 2);  // the two epilogue warps of an output group
@@ -547,26 +571,14 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
         }
       }
     }
-  } else if (kMx && warp == 1) {
-    // ---- relay: this CTA's scales are in place, told to the first CTA ---------------
-    // (by a thread with no loads of its own: publishing to the cluster waits for
-    // them, 2600 cycles at a time in the scale warps)
-    int sslot = 0;
-    uint32_t sphase = 0;
-    bool ok = true;
-    for (int t = pair; t < ntiles && ok; t += pairs)
-      for (int c = 0; c < (a.steps + 3) / 4; ++c) {
-        if (!(ok = mbar_wait(scale_full + 8 * sslot, sphase, a.err))) break;
-        if (elect_one()) mbar_arrive_cluster(map_rank(scale_full + 8 * sslot, 0));
-        if (++sslot == S::kSlots) sslot = 0, sphase ^= 1;
-      }
   } else if (warp == 2) {
     // ---- plan ------------------------------------------------------------------
     int i = 0;
+    Buckets buckets{-1, 0, 0, 0};
     for (int t = pair; t < ntiles; t += pairs, ++i) {
       const int slot = i % kPlanDepth;
       if (!mbar_wait(plan_empty + 8 * slot, ((i / kPlanDepth) & 1) ^ 1, a.err)) break;
-      plan_tile<kMx>(a, prefix, t, (int)rank, tiles + slot, rows + slot * S::kMaxRows, boxes + 32 * slot);
+      plan_tile<kMx>(a, prefix, t, (int)rank, buckets, tiles + slot, rows + slot * S::kMaxRows, boxes + 32 * slot);
       __syncwarp();
       if (lane == 0) mbar_arrive(plan_full + 8 * slot);
     }
@@ -603,7 +615,7 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive_read(map_rank(acc_empty + 8 * buf, 0));
+        mbar_arrive_peer(map_rank(acc_empty + 8 * buf, 0));
         mbar_arrive(plan_empty + 8 * slot);
       }
     }
@@ -667,7 +679,7 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
           }
           fence_async_shared();
           __syncwarp();
-          if (lane == 0) mbar_arrive(scale_full + 8 * sslot);
+          if (lane == 0) mbar_arrive_peer(map_rank(scale_full + 8 * sslot, 0));
           if (++sslot == S::kSlots) sslot = 0, sphase ^= 1;
 #pragma unroll
           for (int j = 0; j < 3; ++j)

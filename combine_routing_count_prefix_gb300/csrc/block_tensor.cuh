@@ -45,15 +45,14 @@ __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// Arrival on a barrier of the cluster's window (map_rank), possibly the peer's:
-// for what this thread has read (tensor memory), nothing written is published ...
-__device__ __forceinline__ void mbar_arrive_read(uint32_t bar) {
+// Arrival on a barrier of the cluster's window (map_rank), possibly the peer's.
+// It publishes nothing to the peer's threads: a release to the cluster waits
+// for all of the thread's memory operations in flight (2600 cycles in a warp
+// that loads ahead).  Its uses need none: tensor memory that has been read, and
+// shared memory that only the tensor core of this SM reads, which the writers'
+// fence_async_shared has made visible to it.
+__device__ __forceinline__ void mbar_arrive_peer(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-// ... or publishing writes to the cluster, which waits for all of the thread's
-// loads and stores in flight.
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   uint32_t done;
