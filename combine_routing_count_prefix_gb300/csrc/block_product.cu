@@ -523,52 +523,54 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
       }
     }
   } else if (warp == 1 && leader) {
-    // ---- products ------------------------------------------------------------
-    int stage = 0, i = 0, sslot = 0, ring = 0;
-    uint32_t phase = 0, sphase = 0;
-    bool ok = true;
-    for (int t = pair; t < ntiles && ok; t += pairs, ++i) {
-      const int slot = i % kPlanDepth, buf = i & 1;
-      if (!(ok = mbar_wait(plan_full + 8 * slot, (i / kPlanDepth) & 1, a.err))) break;
-      const int n = columns(tiles[slot].groups);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(plan_empty + 8 * slot);
-      if (!(ok = mbar_wait(acc_empty + 8 * buf, ((i >> 1) & 1) ^ 1, a.err))) break;
-      tc_fence_after();
-      const uint32_t d = tmem + buf * S::kMaxRows, idesc = a.idesc | (uint32_t)(n >> 3) << 17;
-      for (int k = 0; k < a.steps; ++k) {
-        const bool last = k == a.steps - 1;
-        if (kMx && (k & 3) == 0 && !(ok = mbar_wait(scale_full + 8 * sslot, sphase, a.err))) break;
-        if (!(ok = mbar_wait(full + 8 * stage, phase, a.err))) break;
+    // ---- products: one thread -----------------------------------------------------
+    if (elect_one()) {
+      int stage = 0, i = 0, sslot = 0, ring = 0;
+      uint32_t phase = 0, sphase = 0;
+      bool ok = true;
+      const uint64_t desc = tile_desc(sbase), sdesc = scale_desc(sbase + l.scales);
+      for (int t = pair; t < ntiles && ok; t += pairs, ++i) {
+        const int slot = i % kPlanDepth, buf = i & 1;
+        if (!(ok = mbar_wait(plan_full + 8 * slot, (i / kPlanDepth) & 1, a.err))) break;
+        const int n = columns(tiles[slot].groups);
+        mbar_arrive(plan_empty + 8 * slot);
+        if (!(ok = mbar_wait(acc_empty + 8 * buf, ((i >> 1) & 1) ^ 1, a.err))) break;
         tc_fence_after();
-        if (elect_one()) {
-          const uint32_t data = sbase + stage * S::kStage;
-          const uint64_t da = tile_desc(data), db = tile_desc(data + S::kBytesA);
+        const uint32_t d = tmem + buf * S::kMaxRows, idesc = a.idesc | (uint32_t)(n >> 3) << 17;
+        for (int k = 0; k < a.steps; ++k) {
+          const bool last = k == a.steps - 1;
+          // descriptors count 16 bytes
+          const uint64_t da = desc + (uint32_t)(stage * (S::kStage >> 4)), db = da + (S::kBytesA >> 4);
           if constexpr (kMx) {
-            const uint32_t sa = sbase + l.scales + sslot * S::kSlot + (k & 3) * 512,
-                           sb = sbase + l.scales + sslot * S::kSlot + 2048 + (k & 3) * 1024;
+            const int b = k & 3;
+            if (b == 0 && !(ok = mbar_wait(scale_full + 8 * sslot, sphase, a.err))) break;
+            const uint64_t sa = sdesc + (uint32_t)((sslot * S::kSlot + b * 512) >> 4),
+                           sb = sdesc + (uint32_t)((sslot * S::kSlot + 2048 + b * 1024) >> 4);
             const uint32_t ta = tmem + 2 * S::kMaxRows + ring * S::kScaleColumns, tb = ta + 4;
-            copy_scales(ta, scale_desc(sa));
-            copy_scales(tb, scale_desc(sb));
-            if (n > 128) copy_scales(tb + 4, scale_desc(sb + 512));
+            copy_scales(ta, sa);
+            copy_scales(tb, sb);
+            if (n > 128) copy_scales(tb + 4, sb + (512 >> 4));
+            if (!(ok = mbar_wait(full + 8 * stage, phase, a.err))) break;
+            tc_fence_after();
 #pragma unroll
             for (int j = 0; j < 4; ++j)  // 32 bytes of K; scale j of each row's four
               mma_mx8(d, da + 2 * j, db + 2 * j, idesc | (uint32_t)j << 4 | (uint32_t)j << 29, ta, tb, k > 0 || j > 0);
+            mma_commit_pair(empty + 8 * stage);
+            if (b == 3 || last) {
+              mma_commit_pair(scale_empty + 8 * sslot);
+              if (++sslot == S::kSlots) sslot = 0, sphase ^= 1;
+            }
+            ring = (ring + 1) % S::kScaleRing;
           } else {
+            if (!(ok = mbar_wait(full + 8 * stage, phase, a.err))) break;
+            tc_fence_after();
 #pragma unroll
             for (int j = 0; j < 4; ++j) mma_16bit(d, da + 2 * j, db + 2 * j, idesc, k > 0 || j > 0);
+            mma_commit_pair(empty + 8 * stage);
           }
-          mma_commit_pair(empty + 8 * stage);
-          if (kMx && ((k & 3) == 3 || last)) mma_commit_pair(scale_empty + 8 * sslot);
-          if (last) mma_commit_pair(acc_full + 8 * buf);
+          if (++stage == a.stages) stage = 0, phase ^= 1;
         }
-        __syncwarp();
-        if (++stage == a.stages) stage = 0, phase ^= 1;
-        if (kMx) {
-          ring = (ring + 1) % S::kScaleRing;
-          if ((k & 3) == 3 || last)
-            if (++sslot == S::kSlots) sslot = 0, sphase ^= 1;
-        }
+        if (ok) mma_commit_pair(acc_full + 8 * buf);
       }
     }
   } else if (warp == 2) {
