@@ -69,7 +69,8 @@ struct ProductArgs {
   int32_t* err;
   int T, R, E, L;
   int in, out, n;  // n: rows of w per expert
-  uint64_t x_row, y_row;  // bytes
+  uint64_t x_row;  // bytes of a row
+  uint32_t y_row;
   int dtype, out_dtype;
   int blocks;   // feature tiles per expert
   int steps;    // 128-byte steps of K
@@ -123,7 +124,7 @@ __host__ __device__ inline SmemLayout smem_layout(int stages, int E) {
   l.boxes = at, at += kPlanDepth * 32 * 16;
   l.rows = at, at += kPlanDepth * S::kMaxRows * 4;
   l.tiles = at, at += kPlanDepth * (uint32_t)sizeof(Tile);
-  l.amax = at, at += 2 * 8 * 16 * 4;
+  l.amax = at, at += 2 * 8 * 32 * 4;
   l.bars = at, at += (2 * kMaxStages + 4 + 2 * kPlanDepth + 4 + 2 * 4) * 8;
   l.tmem = at, at += 16;
   l.part = at, at += 64;
@@ -292,108 +293,144 @@ __device__ void plan_tile(const ProductArgs& a, const int* prefix, int t, int ra
 // ---------------------------------------------------------------------------
 // epilogue
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ float silu(float v) { return v / (1.0f + expf(-v)); }
+// v / (1 + exp(-v)) with the hardware's exponential and division, each within a
+// few units of the last fp32 place (the exponential's also grow by |v| halves of
+// one); a denominator above 2^126 gives 0 for what is below 2^-118.
+__device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.0f + __expf(-v)); }
 
-// Two values of one row at `p`, of out_dtype BF16 or FP16.
-__device__ __forceinline__ void store2(uint8_t* p, float lo, float hi, int out_dtype) {
-  uint32_t u;
-  if (out_dtype == LLMOE_DTYPE_FP16) {
+// Two values as BF16 or FP16, the first in the low half.
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, bool fp16) {
+  if (fp16) {
     const __half2 h = __floats2half2_rn(lo, hi);
-    u = *reinterpret_cast<const uint32_t*>(&h);
-  } else {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    u = *reinterpret_cast<const uint32_t*>(&h);
+    return *reinterpret_cast<const uint32_t*>(&h);
   }
-  *reinterpret_cast<uint32_t*>(p) = u;
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// 16 columns (rows of y) of 32 features: lane l holds feature first + l.
-// list: the columns' rows, -1 where nothing is stored.
-__device__ __forceinline__ void store_plain(const ProductArgs& a, const float (&v)[16], int first, const int* list) {
+__device__ __forceinline__ uint8_t* y_row(const ProductArgs& a, int row) {
+  return a.y + (uint64_t)(uint32_t)row * a.y_row;
+}
+
+// 32 columns (rows of y) of 32 features: lane l holds feature first + l.
+// list: the columns' rows, -1 where nothing is stored (read before the stores,
+// which the compiler cannot tell from writes to it).
+__device__ __forceinline__ void store_plain(const ProductArgs& a, const float (&v)[32], int first, const int* list) {
   const int lane = threadIdx.x & 31;
   if (a.out_dtype == LLMOE_DTYPE_FP32) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
-      if (list[j] >= 0 && first + lane < a.out)
-        reinterpret_cast<float*>(a.y + list[j] * a.y_row)[first + lane] = v[j];
+    for (int j = 0; j < 32; ++j) {
+      const int row = list[j];
+      if (row >= 0 && first + lane < a.out) reinterpret_cast<float*>(y_row(a, row))[first + lane] = v[j];
+    }
     return;
   }
   // neighbours swap so that a lane holds two features of one column: even
   // lanes the first column of a pair, odd lanes the second
-  const bool odd = lane & 1;
+  const bool odd = lane & 1, fp16 = a.out_dtype == LLMOE_DTYPE_FP16;
   const int feature = first + (lane & ~1);
+  int row[16];
 #pragma unroll
-  for (int j = 0; j < 16; j += 2) {
-    const float got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
-    const int row = list[odd ? j + 1 : j];
-    if (row >= 0 && feature < a.out)
-      store2(a.y + row * a.y_row + (uint64_t)feature * 2, odd ? got : v[j], odd ? v[j + 1] : got, a.out_dtype);
+  for (int i = 0; i < 16; ++i) row[i] = feature < a.out ? list[2 * i + odd] : -1;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    // both columns of this lane's feature in one word: it keeps one half
+    const uint32_t mine = pack2(v[2 * i], v[2 * i + 1], fp16), got = __shfl_xor_sync(0xffffffffu, mine, 1);
+    const uint32_t u = odd ? __byte_perm(got, mine, 0x7632) : __byte_perm(mine, got, 0x5410);
+    if (row[i] >= 0) *reinterpret_cast<uint32_t*>(y_row(a, row[i]) + (uint32_t)feature * 2) = u;
   }
 }
 
-// 16 columns of 16 gate and 16 up features, eight of each in turn: lane l holds
+// 32 columns of 16 gate and 16 up features, eight of each in turn: lane l holds
 // gate (l & 8 == 0) or up of output feature first + l / 16 * 8 + l % 8.  The
 // two swap so that gate lanes end with h of even columns and up lanes of odd
 // ones.  MX8 output: amax is the exchange's buffer, bar its barrier, parity its
 // phase; false when the wait expired.
-__device__ __forceinline__ bool store_swiglu(const ProductArgs& a, const float (&v)[16], int first, const int* list,
+__device__ __forceinline__ bool store_swiglu(const ProductArgs& a, const float (&v)[32], int first, const int* list,
                                              uint32_t* amax, int warp, uint32_t bar, uint32_t parity) {
   const int lane = threadIdx.x & 31, up = lane >> 3 & 1;
-  float h[8];
+  float h[16];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 16; ++i) {
     const float got = __shfl_xor_sync(0xffffffffu, up ? v[2 * i] : v[2 * i + 1], 8);
     h[i] = up ? silu(got) * v[2 * i + 1] : silu(v[2 * i]) * got;
   }
   const int feature = first + (lane >> 4) * 8 + (lane & 7);
   if (a.out_dtype == LLMOE_DTYPE_MX8) {
-    // a group of 32 outputs is this warp's 16 and its neighbour's: the two
-    // exchange their largest magnitudes through shared memory
-    uint32_t m[8];
+    // a group of 32 outputs is this warp's 16 and its neighbour's.  The largest
+    // magnitudes: lanes of the same columns halve the columns they keep at each
+    // of four exchanges, so that lane at = 0..15 of them ends with column
+    // 2 at + up's, and the two warps swap through shared memory
+    uint32_t m[16];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      m[i] = magnitude(h[i]);
+    for (int i = 0; i < 16; ++i) m[i] = magnitude(h[i]);
+    int at = 0;
 #pragma unroll
-      for (int d = 1; d <= 16; d <<= 1)
-        if (d != 8) m[i] = max(m[i], __shfl_xor_sync(0xffffffffu, m[i], d));
-      if ((lane & 7) == i && lane < 16) amax[warp * 16 + 2 * i + up] = m[i];
+    for (int step = 0; step < 4; ++step) {
+      const int d = step == 3 ? 16 : 1 << step, keep = 8 >> step;  // lane bits 0, 1, 2, 4
+      const bool high = lane & d;
+#pragma unroll
+      for (int i = 0; i < keep; ++i) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? m[i] : m[i + keep], d);
+        m[i] = max(high ? m[i + keep] : m[i], got);
+      }
+      at += high ? keep : 0;
     }
+    amax[warp * 32 + up * 16 + at] = m[0];
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
     if (!mbar_wait(bar, parity, a.err)) return false;
-    const bool store = feature < a.out;  // whole groups: out is a multiple of 32
+    uint32_t mine = 0;  // the scale code of column 2 at + up
+    uint32_t code[16];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int col = 2 * i + up;
-      const uint32_t code = scale_code(max(m[i], amax[(warp ^ 1) * 16 + col]));
-      if (list[col] < 0 || !store) continue;
-      uint8_t* row = a.y + list[col] * a.y_row;
-      row[feature] = (uint8_t)pack_e4m3x2(h[i] * scale_inverse(code), 0.0f);
-      if ((lane & 23) == 0 && !(warp & 1)) {
-        uint8_t* s = row + a.out + feature / 32;
-        *s = (uint8_t)code;
-        if (feature + 32 == a.out)
-          for (uint8_t* end = row + a.y_row; ++s < end;) *s = 0;
-      }
+    for (int i = 0; i < 16; ++i) {
+      code[i] = scale_code(max(amax[warp * 32 + up * 16 + i], amax[(warp ^ 1) * 32 + up * 16 + i]));
+      if (i == at) mine = code[i];
+    }
+    const bool store = feature < a.out;  // whole groups: out is a multiple of 32
+    const int q = lane & 3;
+    int row[4];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) row[g] = store ? list[2 * (4 * g + q) + up] : -1;
+    const int my_row = store && !(warp & 1) ? list[2 * at + up] : -1;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      // four columns of one feature, turned over four lanes into four features of one column
+      uint32_t b = pack_e4m3x2(h[4 * g] * scale_inverse(code[4 * g]), h[4 * g + 1] * scale_inverse(code[4 * g + 1])) |
+                   pack_e4m3x2(h[4 * g + 2] * scale_inverse(code[4 * g + 2]),
+                               h[4 * g + 3] * scale_inverse(code[4 * g + 3])) << 16;
+      uint32_t got = __shfl_xor_sync(0xffffffffu, b, 1);
+      b = __byte_perm(b, got, lane & 1 ? 0x3715 : 0x6240);
+      got = __shfl_xor_sync(0xffffffffu, b, 2);
+      b = __byte_perm(b, got, lane & 2 ? 0x3276 : 0x5410);
+      if (row[g] >= 0) *reinterpret_cast<uint32_t*>(y_row(a, row[g]) + (uint32_t)(feature - q)) = b;
+    }
+    if (my_row >= 0) {
+      uint8_t* s = y_row(a, my_row) + a.out + first / 32;
+      *s = (uint8_t)mine;
+      if (first + 32 == a.out)
+        for (uint8_t* end = y_row(a, my_row) + a.y_row; ++s < end;) *s = 0;
     }
     return true;
   }
   if (a.out_dtype == LLMOE_DTYPE_FP32) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 16; ++i) {
       const int row = list[2 * i + up];
-      if (row >= 0 && feature < a.out) reinterpret_cast<float*>(a.y + row * a.y_row)[feature] = h[i];
+      if (row >= 0 && feature < a.out) reinterpret_cast<float*>(y_row(a, row))[feature] = h[i];
     }
     return true;
   }
-  const bool odd = lane & 1;
+  const bool odd = lane & 1, fp16 = a.out_dtype == LLMOE_DTYPE_FP16;
   const int even_feature = feature & ~1;
+  int row[8];
 #pragma unroll
-  for (int i = 0; i < 8; i += 2) {
-    const float got = __shfl_xor_sync(0xffffffffu, odd ? h[i] : h[i + 1], 1);
-    const int row = list[2 * (odd ? i + 1 : i) + up];
-    if (row >= 0 && even_feature < a.out)
-      store2(a.y + row * a.y_row + (uint64_t)even_feature * 2, odd ? got : h[i], odd ? h[i + 1] : got, a.out_dtype);
+  for (int i = 0; i < 8; ++i) row[i] = even_feature < a.out ? list[4 * i + 2 * odd + up] : -1;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t mine = pack2(h[2 * i], h[2 * i + 1], fp16), got = __shfl_xor_sync(0xffffffffu, mine, 1);
+    const uint32_t u = odd ? __byte_perm(got, mine, 0x7632) : __byte_perm(mine, got, 0x5410);
+    if (row[i] >= 0) *reinterpret_cast<uint32_t*>(y_row(a, row[i]) + (uint32_t)even_feature * 2) = u;
   }
   return true;
 }
@@ -455,71 +492,55 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
 
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, ntiles = prefix[a.E];
 
-  if (warp == 0) {
-    // ---- loads of w: one thread ---------------------------------------------------
-    int stage = 0, i = 0;
-    uint32_t phase = 0;
-    bool ok = true;
+  if (warp == 0 || warp == 3) {
+    // ---- loads: one thread of each of two warps, on alternate steps ----------------
     if (elect_one()) {
+      int stage = warp == 3, i = 0;
+      int turn = warp == 3;  // steps until this thread's next
+      uint32_t phase = 0;
+      bool ok = true;
       for (int t = pair; t < ntiles && ok; t += pairs, ++i) {
         const int slot = i % kPlanDepth;
         if (!(ok = mbar_wait(plan_full + 8 * slot, (i / kPlanDepth) & 1, a.err))) break;
         const Tile tile = tiles[slot];
-        mbar_arrive(plan_empty + 8 * slot);
         const uint32_t bytes = 2 * S::kBytesA + tile.bytes;  // both CTAs', w and x
-        for (int k = 0; k < a.steps; ++k) {
+        // the first boxes stay in registers: read from shared memory at every
+        // step, each load would wait for its box
+        constexpr int kKept = 6;
+        Box kept[kKept];
+#pragma unroll
+        for (int b = 0; b < kKept; ++b) kept[b] = b < tile.boxes ? boxes[32 * slot + b] : Box{};
+        int k = turn;
+        for (; k < a.steps; k += 2) {
           if (!(ok = mbar_wait(empty + 8 * stage, phase ^ 1, a.err))) break;
-          const uint32_t data = sbase + stage * S::kStage, bar = map_rank(full + 8 * stage, 0);
+          const uint32_t data = sbase + stage * S::kStage, to = data + S::kBytesA, bar = map_rank(full + 8 * stage, 0);
           const int k0 = k * (kMx ? 128 : 64);
           if (leader) mbar_expect_tx(full + 8 * stage, bytes);
           if constexpr (kSwiglu)
             tma_tile5(data, &maps.w, k0, 0, 0, tile.block * 16 + (int)rank * 8, tile.expert, bar);
           else
             tma_tile3(data, &maps.w, k0, tile.block * kTileFeatures + (int)rank * 128, tile.expert, bar);
-          if (++stage == a.stages) stage = 0, phase ^= 1;
+#pragma unroll
+          for (int b = 0; b < kKept; ++b)
+            if (b < tile.boxes) tma_rows(to + kept[b].offset, &maps.x[kept[b].size], k0, kept[b].row, bar);
+          for (int b = kKept; b < tile.boxes; b += 4) {
+            Box q[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) q[u] = b + u < tile.boxes ? boxes[32 * slot + b + u] : Box{};
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              if (b + u < tile.boxes) tma_rows(to + q[u].offset, &maps.x[q[u].size], k0, q[u].row, bar);
+          }
+          if ((stage += 2) >= a.stages) stage -= a.stages, phase ^= 1;
         }
+        turn = k - a.steps;
+        mbar_arrive(plan_empty + 8 * slot);
       }
       // the ring drains: no product reads shared memory, and no arrival is under
       // way to this CTA, once every stage has been handed back
-      for (int s = 0; s < a.stages && ok; ++s) {
+      for (int n = turn; n < a.stages && ok; n += 2) {
         ok = mbar_wait(empty + 8 * stage, phase ^ 1, a.err);
-        if (++stage == a.stages) stage = 0, phase ^= 1;
-      }
-    }
-  } else if (warp == 3) {
-    // ---- loads of x: one thread ---------------------------------------------------
-    int stage = 0, i = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    if (elect_one()) {
-      for (int t = pair; t < ntiles && ok; t += pairs, ++i) {
-        const int slot = i % kPlanDepth;
-        if (!(ok = mbar_wait(plan_full + 8 * slot, (i / kPlanDepth) & 1, a.err))) break;
-        const int n = tiles[slot].boxes;
-        // the first boxes stay in registers: read from shared memory at every
-        // step, each load would wait for its box
-        constexpr int kKept = 6;
-        Box kept[kKept];
-#pragma unroll
-        for (int b = 0; b < kKept; ++b) kept[b] = b < n ? boxes[32 * slot + b] : Box{};
-        for (int k = 0; k < a.steps; ++k) {
-          if (!(ok = mbar_wait(empty + 8 * stage, phase ^ 1, a.err))) break;
-          const uint32_t data = sbase + stage * S::kStage + S::kBytesA, bar = map_rank(full + 8 * stage, 0);
-          const int k0 = k * (kMx ? 128 : 64);
-#pragma unroll
-          for (int b = 0; b < kKept; ++b)
-            if (b < n) tma_rows(data + kept[b].offset, &maps.x[kept[b].size], k0, kept[b].row, bar);
-          for (int b = kKept; b < n; b += 4) {
-            Box q[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) q[u] = b + u < n ? boxes[32 * slot + b + u] : Box{};
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-              if (b + u < n) tma_rows(data + q[u].offset, &maps.x[q[u].size], k0, q[u].row, bar);
-          }
-          if (++stage == a.stages) stage = 0, phase ^= 1;
-        }
-        mbar_arrive(plan_empty + 8 * slot);
+        if ((stage += 2) >= a.stages) stage -= a.stages, phase ^= 1;
       }
     }
   } else if (warp == 1 && leader) {
@@ -586,9 +607,9 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
     }
   } else if (warp >= 4 && warp < 12) {
     // ---- epilogue ------------------------------------------------------------------
-    // two sets of four warps, each taking every other 16 columns
+    // two sets of four warps, each taking every other 32 columns
     const int w = warp & 3, set = warp >= 8;  // tensor-memory lanes 32 w ..
-    uint32_t* amax = reinterpret_cast<uint32_t*>(smem + l.amax) + set * 128;
+    uint32_t* amax = reinterpret_cast<uint32_t*>(smem + l.amax) + set * 256;
     int i = 0, flip = 0;
     for (int t = pair; t < ntiles; t += pairs, ++i) {
       const int slot = i % kPlanDepth, buf = i & 1;
@@ -601,13 +622,13 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
       tc_fence_after();
       const uint32_t acc = tmem + ((uint32_t)(32 * w) << 16) + buf * S::kMaxRows;
       bool ok = true;
-      for (int c = 16 * set; c < tile.groups * kGroup && ok; c += 32) {
-        float v[16];
-        tmem_load16(acc + c, v);
+      for (int c = 32 * set; c < tile.groups * kGroup && ok; c += 64) {
+        float v[32];
+        tmem_load32(acc + c, v);
         if constexpr (kSwiglu) {
           // two buffers in turn: a warp that fills one again has met its
           // neighbour at the other since, so the neighbour has read it
-          ok = store_swiglu(a, v, first, list + c, amax + 64 * flip, w, halves + 8 * (2 * set + (w >> 1)), flip);
+          ok = store_swiglu(a, v, first, list + c, amax + 128 * flip, w, halves + 8 * (2 * set + (w >> 1)), flip);
           flip ^= 1;
         } else {
           store_plain(a, v, first, list + c);
@@ -725,7 +746,7 @@ int product_args(const void* x, const void* w, void* y, const int64_t* counts, i
     default: return LLMOE_ERR_INVALID_ARGUMENT;
   }
   const uint64_t xr = row_bytes(in, dtype), yr = row_bytes(out, out_dtype);
-  if (xr == 0 || yr == 0 || out > INT32_MAX / 2 || (swiglu && out % 8 != 0)) return LLMOE_ERR_INVALID_ARGUMENT;
+  if (xr == 0 || yr == 0 || yr > INT32_MAX || out > INT32_MAX / 2 || (swiglu && out % 8 != 0)) return LLMOE_ERR_INVALID_ARGUMENT;
   if (x == nullptr || w == nullptr || y == nullptr || !aligned(x, 16) || !aligned(w, 16) || !aligned(y, 16) ||
       !aligned(counts, 8))
     return LLMOE_ERR_INVALID_ARGUMENT;
@@ -759,7 +780,7 @@ int product_args(const void* x, const void* w, void* y, const int64_t* counts, i
   a->out = out;
   a->n = (int)n;
   a->x_row = xr;
-  a->y_row = yr;
+  a->y_row = (uint32_t)yr;
   a->dtype = dtype;
   a->out_dtype = out_dtype;
   return LLMOE_SUCCESS;
