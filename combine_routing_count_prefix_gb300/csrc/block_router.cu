@@ -1,10 +1,21 @@
 // block_router.cu -- llmoe_topk_router (include/llmoe_block.h).
 //
 // A group of one warp (a CTA of eight for more experts than a warp holds in
-// registers) owns a token: expert e's key sits in lane e % lanes as a 32-bit
-// integer that orders like the float (0: cannot be chosen).  Each of the K
-// rounds takes the maximum key and, among its holders, the lowest expert, by
-// two warp reductions, so ties go to the lowest index whatever the schedule.
+// registers) owns a token; a lane holds its experts' keys as 32-bit integers
+// that order like the floats (0: cannot be chosen).  The choice is K rounds of
+// two warp reductions, the largest key and, among its holders, the lowest
+// expert, so ties go to the lowest index whatever the schedule.
+//
+// Bytes are few (1 KB a token); what bounds a large batch is the instructions
+// issued.  So a warp first finds the few experts that can be chosen at all: the
+// K-th largest of the 32 lanes' best keys is a bound that at least K keys reach
+// (K = 8 of 256: about ten do), and for that keys from the hardware's
+// exponential and reciprocal are enough, with a margin for their error.  Those
+// few go one to a lane, which computes their fp32 keys as defined, and the
+// rounds run over them.  8192 tokens of 256 experts: 8.6 us with exact keys for
+// all, 7.7 with this.
+#include <float.h>
+
 #include "block_common.cuh"
 
 namespace {
@@ -64,95 +75,185 @@ struct Group {
   }
 };
 
-// W warps per token, V experts per lane.
-template <int W, int V>
-__global__ void __launch_bounds__(256) router_kernel(RouterArgs a) {
+// The expert that lane `lane` of a group holds as its i-th: in order over the
+// lanes, or (kVec) four in a row, so that they load as one.
+template <int W, bool kVec>
+__device__ __forceinline__ int expert_of(int lane, int i) {
+  constexpr int kLanes = 32 * W;
+  return kVec ? (i / 4 * kLanes + lane) * 4 + i % 4 : lane + i * kLanes;
+}
+
+__device__ __forceinline__ float sigmoid_score(float l) { return __frcp_rn(1.0f + expf(-l)); }
+// Of a row whose largest logit is top; logits of +infinity are the limit of
+// equal large ones.
+__device__ __forceinline__ float softmax_score(float l, float top) {
+  return top == INFINITY ? (l == INFINITY ? 1.0f : 0.0f) : expf(l - top);
+}
+
+// A key as an integer of the same order, 0 where the expert cannot be chosen:
+// its logit or key is NaN or -infinity.
+__device__ __forceinline__ uint32_t order(float logit, float key) {
+  key += 0.0f;  // -0 ranks as +0
+  const uint32_t b = __float_as_uint(key);
+  return logit > -INFINITY && key > -INFINITY ? ((b & 0x80000000u) ? ~b : (b | 0x80000000u)) : 0u;
+}
+__device__ __forceinline__ float unorder(uint32_t b) {
+  return __uint_as_float((b & 0x80000000u) ? (b & 0x7fffffffu) : ~b);
+}
+__device__ __forceinline__ uint32_t exact_key(const RouterArgs& a, int e, float l) {
+  float k = a.softmax ? l : sigmoid_score(l);
+  if (a.bias != nullptr) k += __ldg(a.bias + e);
+  return order(l, k);
+}
+
+// W warps per token, V experts per lane; kVec: fp32 logits, rows of whole 16
+// bytes.
+template <int W, int V, bool kVec>
+__global__ void __launch_bounds__(256, W > 1 || V > 8 ? 2 : 5) router_kernel(RouterArgs a) {
   __shared__ uint32_t part[W];
+  __shared__ uint2 gathered[W == 1 ? 8 : 1][32];
   release_next_grid();
   wait_prior_grid();
   const Group<W> group{part};
-  constexpr int kLanes = 32 * W;
   const int lane = W == 1 ? threadIdx.x & 31 : threadIdx.x;
   const int64_t first = W == 1 ? ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5 : blockIdx.x;
   const int64_t step = W == 1 ? ((int64_t)gridDim.x * blockDim.x) >> 5 : gridDim.x;
   for (int64_t row = first; row < a.rows; row += step) {
     const bool on = a.active == nullptr || a.active[row] != 0;
-    float score[V];
-    uint32_t key[V];
-    float top = -INFINITY;
+    float l[V];
+    if constexpr (kVec) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = lane + i * kLanes;
-      score[i] = on && e < a.E ? load_logit(a, row * a.E + e) : -INFINITY;
-      top = fmaxf(top, score[i]);  // a NaN does not count
-    }
-    if (a.softmax) top = group.max_f(top);
-    float total = 0.0f;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = lane + i * kLanes;
-      const float l = score[i];
-      const bool can = l > -INFINITY;  // false for a NaN
-      float k;
-      if (a.softmax) {
-        // logits of +infinity are the limit of equal large ones
-        score[i] = !can ? 0.0f : top == INFINITY ? (l == INFINITY ? 1.0f : 0.0f) : expf(l - top);
-        total += score[i];
-        k = l;
-      } else {
-        score[i] = can ? 1.0f / (1.0f + expf(-l)) : 0.0f;
-        k = score[i];
+      for (int i = 0; i < V; i += 4) {
+        const int e = expert_of<W, kVec>(lane, i);
+        float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (on && e < a.E) q = *reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) + row * a.E + e);
+        l[i] = q.x, l[i + 1] = q.y, l[i + 2] = q.z, l[i + 3] = q.w;
       }
-      if (a.bias != nullptr && e < a.E) k += a.bias[e];
-      k += 0.0f;  // -0 ranks as +0
-      const uint32_t b = __float_as_uint(k);
-      key[i] = can && k > -INFINITY ? ((b & 0x80000000u) ? ~b : (b | 0x80000000u)) : 0u;
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int e = expert_of<W, kVec>(lane, i);
+        l[i] = on && e < a.E ? load_logit(a, row * a.E + e) : -INFINITY;
+      }
     }
+    float top = -INFINITY, total = 0.0f;
     if (a.softmax) {
-      total = group.sum_f(total);
 #pragma unroll
-      for (int i = 0; i < V; ++i) score[i] = total > 0.0f ? score[i] / total : 0.0f;
-    }
-    int my_idx = -1;  // lane k of the first warp keeps the k-th choice
-    float my_score = 0.0f, sum = 0.0f;
-    for (int k = 0; k < a.K; ++k) {
-      uint32_t best = 0;
-#pragma unroll
-      for (int i = 0; i < V; ++i) best = max(best, key[i]);
-      best = group.max_u32(best);
-      if (best == 0) break;  // nothing left to choose: uniform over the group
-      uint32_t at = 0xffffffffu;
-      float s = 0.0f;
-#pragma unroll
-      for (int i = V - 1; i >= 0; --i)
-        if (key[i] == best) at = lane + i * kLanes;
-      const uint32_t win = group.min_u32(at);
+      for (int i = 0; i < V; ++i) top = fmaxf(top, l[i]);  // a NaN does not count
+      top = group.max_f(top);
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (lane + i * kLanes == (int)win) {
-          key[i] = 0;
-          s = score[i];
+        if (l[i] > -INFINITY) total += softmax_score(l[i], top);
+      total = group.sum_f(total);
+    }
+
+    int mine = -1;  // lane k of the first warp keeps the k-th choice
+    bool rounds = true;
+    if constexpr (W == 1 && V > 1) {
+      float near[V], left = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        near[i] = a.softmax ? l[i] : __fdividef(1.0f, 1.0f + __expf(-l[i]));
+        const int e = expert_of<W, kVec>(lane, i);
+        if (a.bias != nullptr && e < a.E) near[i] += __ldg(a.bias + e);
+        if (!(l[i] > -INFINITY)) near[i] = -INFINITY;
+        left = fmaxf(left, near[i]);
+      }
+      uint32_t lane_best = order(left, left), bound = 0;
+      for (int k = 0; k < a.K; ++k) {
+        bound = group.max_u32(lane_best);
+        if (bound == 0) break;
+        if (lane_best == bound) lane_best = 0;
+      }
+      // |near - key| <= 2^-20 + 2^-23 |key|: the exponential is within (2 + 1.2 |l|)
+      // ulp, which s (1 - s) damps, the division within 2 ulp, the sums round.  A
+      // chosen key is at most that below the bound, its near value twice that.
+      float least = -FLT_MAX;
+      if (bound != 0) {
+        const float b = unorder(bound);
+        least = b == INFINITY || a.softmax ? b : b - (0x1p-18f + fabsf(b) * 0x1p-21f);
+      }
+      uint2* list = gathered[threadIdx.x >> 5];
+      int n = 0;
+      __syncwarp();  // the previous row's list has been read
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const bool in = near[i] >= least;
+        const uint32_t who = __ballot_sync(0xffffffffu, in);
+        const int at = n + __popc(who & ((1u << lane) - 1));
+        if (in && at < 32) list[at] = make_uint2(__float_as_uint(l[i]), (uint32_t)expert_of<W, kVec>(lane, i));
+        n += __popc(who);
+      }
+      __syncwarp();
+      if (n <= 32) {
+        rounds = false;
+        const uint2 q = lane < n ? list[lane] : make_uint2(0, 0);
+        uint32_t best = lane < n ? exact_key(a, (int)q.y, __uint_as_float(q.x)) : 0u;
+        for (int k = 0; k < a.K; ++k) {
+          const uint32_t win = group.max_u32(best);
+          if (win == 0) break;
+          const int e = (int)group.min_u32(best == win ? q.y : 0xffffffffu);
+          if (best == win && (int)q.y == e) best = 0;
+          if (lane == k) mine = e;
         }
-      s = W == 1 ? __shfl_sync(0xffffffffu, s, win % 32) : group.sum_f(s);  // the other lanes hold 0
-      sum += s;
-      if (lane == k) {
-        my_idx = (int)win;
-        my_score = s;
       }
     }
-    const float m = a.renorm ? (sum > 0.0f ? a.scale / sum : 0.0f) : a.scale;
+    if (rounds) {  // over all keys: many equal ones at the bound, or a CTA per token
+      uint32_t key[V], best;  // best: this lane's largest key left, and its expert
+      int best_e;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int e = expert_of<W, kVec>(lane, i);
+        key[i] = e < a.E ? exact_key(a, e, l[i]) : 0u;
+      }
+      const auto look = [&] {
+        best = 0, best_e = INT_MAX;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (key[i] > best) best = key[i], best_e = expert_of<W, kVec>(lane, i);
+      };
+      look();
+      for (int k = 0; k < a.K; ++k) {
+        const uint32_t win = group.max_u32(best);
+        if (win == 0) break;  // nothing left to choose: uniform over the group
+        const int e = (int)group.min_u32(best == win ? (uint32_t)best_e : 0xffffffffu);
+        if (best == win && best_e == e) {
+#pragma unroll
+          for (int i = 0; i < V; ++i)
+            if (expert_of<W, kVec>(lane, i) == e) key[i] = 0;
+          look();
+        }
+        if (lane == k) mine = e;
+      }
+    }
+    if (W > 1 && lane >= 32) continue;
+    float score = 0.0f;
+    if (mine >= 0) {
+      const float v = load_logit(a, row * a.E + mine);
+      score = a.softmax ? softmax_score(v, top) / total : sigmoid_score(v);
+    }
+    float m = a.scale;
+    if (a.renorm) {
+      float sum = score;
+#pragma unroll
+      for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      m = sum > 0.0f ? a.scale / sum : 0.0f;
+    }
     if (lane < a.K) {
-      a.topk_idx[row * a.K + lane] = my_idx;
-      a.topk_w[row * a.K + lane] = my_idx < 0 ? 0.0f : my_score * m;
+      a.topk_idx[row * a.K + lane] = mine;
+      a.topk_w[row * a.K + lane] = score * m;
     }
   }
 }
 
+// Experts per lane: a power of two, so that a few kernels serve all E.
 template <int V>
-int launch_router_warp(const RouterArgs& a, llmoe_stream_t stream) {
+int launch_router_warp(const RouterArgs& a, bool vec, llmoe_stream_t stream) {
   const int64_t warps = 8, wave = (int64_t)num_sms() * 8;
   const unsigned grid = (unsigned)std::min<int64_t>(wave, (a.rows + warps - 1) / warps);
-  return launch_block(router_kernel<1, V>, grid, 256, 0, stream, a);
+  if constexpr (V >= 4)
+    if (vec) return launch_block(router_kernel<1, V, true>, grid, 256, 0, stream, a);
+  return launch_block(router_kernel<1, V, false>, grid, 256, 0, stream, a);
 }
 
 }  // namespace
@@ -172,12 +273,13 @@ extern "C" int llmoe_topk_router(const void* logits, const float* bias, const ui
     return LLMOE_ERR_INVALID_ARGUMENT;
   const RouterArgs a{logits,      bias,     active, topk_idx, topk_w, rows, num_experts, num_topk,
                      dtype, scoring == LLMOE_SCORE_SOFTMAX, (flags & LLMOE_ROUTER_RENORM) != 0, scale};
-  if (num_experts <= 32) return launch_router_warp<1>(a, stream);
-  if (num_experts <= 64) return launch_router_warp<2>(a, stream);
-  if (num_experts <= 128) return launch_router_warp<4>(a, stream);
-  if (num_experts <= 256) return launch_router_warp<8>(a, stream);
-  if (num_experts <= 512) return launch_router_warp<16>(a, stream);
+  const bool vec = dtype == LLMOE_DTYPE_FP32 && num_experts % 4 == 0 && aligned(logits, 16);
+  if (num_experts <= 32) return launch_router_warp<1>(a, vec, stream);
+  if (num_experts <= 64) return launch_router_warp<2>(a, vec, stream);
+  if (num_experts <= 128) return launch_router_warp<4>(a, vec, stream);
+  if (num_experts <= 256) return launch_router_warp<8>(a, vec, stream);
+  if (num_experts <= 512) return launch_router_warp<16>(a, vec, stream);
   const unsigned grid = (unsigned)std::min<int64_t>((int64_t)num_sms() * 8, rows);
-  if (num_experts <= 2048) return launch_block(router_kernel<8, 8>, grid, 256, 0, stream, a);
-  return launch_block(router_kernel<8, 32>, grid, 256, 0, stream, a);
+  if (num_experts <= 2048) return launch_block(router_kernel<8, 8, false>, grid, 256, 0, stream, a);
+  return launch_block(router_kernel<8, 32, false>, grid, 256, 0, stream, a);
 }

