@@ -57,7 +57,8 @@ def close(got, want, err, dtype):
 # rows: norm and packing
 # ---------------------------------------------------------------------------
 
-NORM_SHAPES = [(1, 64), (3, 96), (5, 2048), (2, 7168), (1, 32768), (700, 224), (2048, 32)]
+NORM_SHAPES = [(1, 64), (3, 96), (5, 2048), (2, 7168), (1, 32768), (700, 224), (2048, 32), (410, 7168), (1300, 2080),
+               (153, 16384), (160, 32768)]
 
 
 @pytest.mark.parametrize("out", ["same", "mx8"])
@@ -87,9 +88,9 @@ def test_add_rmsnorm(L, rows, hidden, dtype, out):
         close(wide(got[:-16].view(TORCH[dtype]).reshape(rows, hidden)), v, np.abs(v) * NORM_ERR, dtype)
 
 
+@pytest.mark.parametrize("rows,hidden", [(37, 1056), (900, 1056), (350, 4104)])
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
-def test_add_rmsnorm_in_place_and_without_residual(L, dtype):
-    rows, hidden = 37, 1056
+def test_add_rmsnorm_in_place_and_without_residual(L, dtype, rows, hidden):
     g = rnd(5)
     x = torch.randn(rows, hidden, generator=g).to(TORCH[dtype])
     res = torch.randn(rows, hidden, generator=g).to(TORCH[dtype])
@@ -111,7 +112,7 @@ def test_add_rmsnorm_in_place_and_without_residual(L, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
-@pytest.mark.parametrize("rows,hidden", [(1, 32), (9, 512), (4, 7168), (3, 544)])
+@pytest.mark.parametrize("rows,hidden", [(1, 32), (9, 512), (4, 7168), (3, 544), (500, 1056), (5000, 96)])
 def test_pack_mx8_is_exact(L, rows, hidden, dtype):
     g = rnd(rows + hidden)
     x = (torch.randn(rows, hidden, generator=g) * torch.exp2(torch.randint(-12, 9, (rows, hidden // 32, 1), generator=g)
