@@ -44,19 +44,17 @@ template <bool kMx>
 struct Shape {
   static constexpr int kThreads = kMx ? 512 : 384;
   // two accumulators of kMaxRows columns
-  static constexpr int kMaxRows = kMx ? 192 : 256;
+  static constexpr int kMaxRows = kMx ? 224 : 256;
   static constexpr int kBytesA = 128 * 128, kBytesB = kMaxRows / 2 * 128;
   static constexpr int kStage = kBytesA + kBytesB;
-  static constexpr int kStages = kMx ? 7 : 6;
+  static constexpr int kStages = 6;
   // 8-bit operands: scales in slots of four steps; a step's are 512 bytes for
   // the CTA's 128 rows of w and 1024 for up to 256 rows of x, and 12 columns
-  // of tensor memory, kept for kScaleRing steps (more than there are stages, so
-  // the step that used them before has finished)
+  // of tensor memory, reused after kScaleRing steps
   static constexpr int kSlots = kMx ? 3 : 0;
   static constexpr int kSlot = 4 * (512 + 1024);
-  static constexpr int kScaleColumns = 12, kScaleRing = 8;
+  static constexpr int kScaleColumns = 12, kScaleRing = 5;
   static_assert(2 * kMaxRows + (kMx ? kScaleRing * kScaleColumns : 0) <= 512, "tensor memory has 512 columns");
-  static_assert(kScaleRing > kStages, "a step's scale columns outlive its stage");
 };
 
 struct ProductArgs {
@@ -548,6 +546,9 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
     if (elect_one()) {
       int stage = 0, i = 0, sslot = 0, ring = 0;
       uint32_t phase = 0, sphase = 0;
+      int done = -S::kScaleRing;  // 8-bit: the step whose scale columns this one takes, counted over tiles,
+      int done_stage = 0;         // and the stage it was in
+      uint32_t done_phase = 0;
       bool ok = true;
       const uint64_t desc = tile_desc(sbase), sdesc = scale_desc(sbase + l.scales);
       for (int t = pair; t < ntiles && ok; t += pairs, ++i) {
@@ -568,6 +569,11 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
             const uint64_t sa = sdesc + (uint32_t)((sslot * S::kSlot + b * 512) >> 4),
                            sb = sdesc + (uint32_t)((sslot * S::kSlot + 2048 + b * 1024) >> 4);
             const uint32_t ta = tmem + 2 * S::kMaxRows + ring * S::kScaleColumns, tb = ta + 4;
+            if (done >= 0) {
+              if (!(ok = mbar_wait(empty + 8 * done_stage, done_phase, a.err))) break;
+              if (++done_stage == a.stages) done_stage = 0, done_phase ^= 1;
+            }
+            ++done;
             copy_scales(ta, sa);
             copy_scales(tb, sb);
             if (n > 128) copy_scales(tb + 4, sb + (512 >> 4));
