@@ -412,3 +412,88 @@ def test_counts_from_the_rank_buffers(L, dtype):
         L.llmoe_expert_product(recv, w, ya, None, n_in, n_out, code[dtype], 0, 0, bs)
         L.llmoe_expert_product(recv, w, yb, counts, n_in, n_out, code[dtype], 0, 0, L.geometry(T, R, E))
         assert torch.equal(ya, yb) and bool(ya.any())
+
+
+@pytest.mark.parametrize("rows,dtype", [("same", "bf16"), ("same", "fp16"), ("mx8", "bf16")])
+def test_moe_block(L, rows, dtype):
+    """The whole block against its definition, given the block's own choice of
+    experts (checked against the router's definition from its own logits)."""
+    from combine_routing_count_prefix_gb300.moe_block import MoEBlock
+
+    R, T, n, H, I, E, K = 2, 24, 19, 512, 160, 8, 3
+    t, g = TORCH[dtype], rnd(12)
+    norm_w = (1 + 0.1 * torch.randn(H, generator=g)).to(t)
+    router_w = (torch.randn(E, H, generator=g) * H ** -0.5).to(t)
+    gate_up = (torch.randn(E, 2 * I, H, generator=g) * H ** -0.5).to(t)
+    down = (torch.randn(E, H, I, generator=g) * I ** -0.5).to(t)
+    bias = torch.randint(-2, 3, (E,), generator=g).float() / 8
+    x = torch.randn(R, n, H, generator=g).to(t)
+    res = torch.randn(R, n, H, generator=g).to(t)
+    active = (torch.rand(R, n, generator=g) < 0.85).to(torch.uint8)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    m = MoEBlock(T, R, K, norm_w.cuda(), router_w.cuda(), gate_up.cuda(), down.cuda(), bias.cuda(), dtype, rows,
+                 scale=2.0, err=err)
+    residual, out = res.cuda(), torch.full((R, n, H), float("nan"), dtype=t, device="cuda")
+    m.forward(x.cuda(), residual, out, active.cuda())
+    first = out.clone()
+    h = (x.float() + res.float()).to(t)
+    assert torch.equal(residual.cpu(), h)
+    # again on the same buffers, without and within a CUDA graph: the same bits
+    residual.copy_(res.cuda())
+    m.forward(x.cuda(), residual, out, active.cuda())
+    assert torch.equal(out, first)
+    xs, acts = x.cuda(), active.cuda()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        m.forward(xs, residual, out, acts)
+    residual.copy_(res.cuda())
+    out.fill_(0)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, first) and int(err) == 0
+
+    tokens = R * n
+    v = ref.rmsnorm(wide(h).reshape(tokens, H), wide(norm_w), 1e-6)
+    xn = wide(m.xn)[:tokens]
+    close(xn, v, np.abs(v) * NORM_ERR, dtype)
+    logits = m.logits[:tokens].cpu()
+    want = xn @ wide(router_w).T
+    assert (np.abs(logits.double().numpy() - want) <= H * 2.0 ** -23 * (np.abs(xn) @ np.abs(wide(router_w)).T)).all()
+    idx, w, gap = ref.router(logits.numpy(), bias.numpy(), active.reshape(-1).numpy(), K, "sigmoid", True, 2.0)
+    assert gap > 1e-6
+    assert np.array_equal(m.topk_idx[:tokens].cpu().numpy(), idx)
+    # the experts on the rows that were dispatched, in 64 bits, each rounding of the path bounded
+    if rows == "mx8":
+        xe = ref.mx8_values(m.rows.cpu().numpy()[:tokens], H)
+        gu = ref.mx8_values(m.gate_up.cpu().numpy(), H)
+        dn = ref.mx8_values(m.down.cpu().numpy(), I)
+    else:
+        xe, gu, dn = xn, wide(gate_up), wide(down)
+    step = 2.0 ** -4 if rows == "mx8" else HALF_ULP[dtype]  # h's rounding, relative to its group's largest value
+    got = wide(first).reshape(tokens, H)
+    topk_w = m.topk_w[:tokens].cpu().double().numpy()
+    for i in range(tokens):
+        total, tol = np.zeros(H), np.zeros(H)
+        for k in range(K):
+            e = idx[i, k]
+            if e < 0:
+                continue
+            _, hv, he = ref.product(xe[i:i + 1], gu[e:e + 1], np.array([[1]]), 1, True)
+            hv, he = hv[0], he[0]
+            he = he + step * (np.repeat(np.abs(hv).reshape(-1, 32).max(1), 32) if rows == "mx8" else np.abs(hv)) + TINY[dtype]
+            y = dn[e] @ hv
+            ye = np.abs(dn[e]) @ he + I * 2.0 ** -23 * (np.abs(dn[e]) @ np.abs(hv))
+            ye += (np.abs(y) + ye) * HALF_ULP[dtype] + TINY[dtype]
+            total += topk_w[i, k] * y
+            tol += topk_w[i, k] * ye
+        tol += (np.abs(total) + tol) * (HALF_ULP[dtype] + K * 2.0 ** -23) + TINY[dtype]
+        assert (np.abs(got[i] - total) <= tol).all(), i
+
+
+def test_moe_block_refuses_too_many_tokens(L):
+    from combine_routing_count_prefix_gb300.moe_block import MoEBlock
+
+    z = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device="cuda")
+    m = MoEBlock(4, 2, 1, z(64), z(2, 64), z(2, 64, 64), z(2, 64, 32))
+    with pytest.raises(ValueError):
+        m.forward(z(2, 5, 64), z(2, 5, 64), z(2, 5, 64))
