@@ -80,18 +80,26 @@ struct ProductMaps {
   CUtensorMap w, x[kBoxes];
 };
 
-__device__ __forceinline__ int bucket_count(const ProductArgs& a, int e, int src) {
+// Received rows of the buckets (e, s), s = src, src + stride, ... below R, at
+// most N of them (0 for the others); all loads before any check.
+template <int N>
+__device__ __forceinline__ void bucket_counts(const ProductArgs& a, int e, int src, int stride, int (&rows)[N]) {
   const int64_t* p = a.counts != nullptr
-                         ? a.counts + (int64_t)e * a.R + src
+                         ? a.counts + (int64_t)e * a.R
                          : reinterpret_cast<const int64_t*>(a.base + (e / a.L) * a.rank_stride + a.sig_off) +
-                               ((int64_t)(e % a.L) * a.R + src);
-  const int64_t c = *p;
-  if (c < 0 || c > a.T) report(a.err, LLMOE_DEV_SLOT_RANGE);
-  return (int)max((int64_t)0, min(c, (int64_t)a.T));
+                               (int64_t)(e % a.L) * a.R;
+  int64_t c[N];
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < N; ++i) c[i] = src + i * stride < a.R ? p[src + i * stride] : 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    bad |= c[i] < 0 || c[i] > a.T;
+    rows[i] = (int)max((int64_t)0, min(c[i], (int64_t)a.T));
+  }
+  if (bad) report(a.err, LLMOE_DEV_SLOT_RANGE);
 }
-__device__ __forceinline__ int bucket_groups(const ProductArgs& a, int e, int src) {
-  return (bucket_count(a, e, src) + kGroup - 1) / kGroup;
-}
+__device__ __forceinline__ int groups_of(int rows) { return (rows + kGroup - 1) / kGroup; }
 
 // A planned tile; its rows are in the plan's row list.
 struct __align__(16) Tile {
@@ -132,25 +140,37 @@ __host__ __device__ inline SmemLayout smem_layout(int stages, int E) {
 }
 
 // ---------------------------------------------------------------------------
-// prologue: tiles before each expert
+// prologue: shares before each expert
 // ---------------------------------------------------------------------------
-// prefix[e] = tiles of the experts before e (prefix[E]: all tiles).
+// An expert's groups are cut into shares, the fewest of at most kMaxRows rows;
+// every share meets a.blocks feature blocks.  prefix[e] = shares of the experts
+// before e (prefix[E]: all).
 template <bool kMx>
-__device__ void count_tiles(const ProductArgs& a, int* prefix, int* part) {
-  constexpr int kThreads = Shape<kMx>::kThreads, kMost = Shape<kMx>::kMaxRows / kGroup;
+__device__ void count_shares(const ProductArgs& a, int* prefix, int* part) {
+  constexpr int kThreads = Shape<kMx>::kThreads, kMost = Shape<kMx>::kMaxRows / kGroup, kBatch = 8;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (a.R >= 32) {
+  if (a.R >= 32) {  // a warp per expert
     for (int e = warp; e < a.E; e += kThreads / 32) {
       int n = 0;
-      for (int s = lane; s < a.R; s += 32) n += bucket_groups(a, e, s);
+      for (int s = lane; s < a.R; s += 32 * kBatch) {
+        int c[kBatch];
+        bucket_counts(a, e, s, 32, c);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) n += groups_of(c[i]);
+      }
       n = __reduce_add_sync(0xffffffffu, n);
-      if (lane == 0) prefix[e] = (n + kMost - 1) / kMost * a.blocks;
+      if (lane == 0) prefix[e] = (n + kMost - 1) / kMost;
     }
   } else {
     for (int e = tid; e < a.E; e += kThreads) {
       int n = 0;
-      for (int s = 0; s < a.R; ++s) n += bucket_groups(a, e, s);
-      prefix[e] = (n + kMost - 1) / kMost * a.blocks;
+      for (int s = 0; s < a.R; s += kBatch) {
+        int c[kBatch];
+        bucket_counts(a, e, s, 1, c);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) n += groups_of(c[i]);
+      }
+      prefix[e] = (n + kMost - 1) / kMost;
     }
   }
   __syncthreads();
@@ -181,7 +201,7 @@ __device__ void count_tiles(const ProductArgs& a, int* prefix, int* part) {
 // plan: one warp turns a tile's number into its expert, features and rows
 // ---------------------------------------------------------------------------
 // One expert's buckets, 32 source ranks at a time: lane s holds rank s0 + s's
-// rows, and the groups of the ranks up to and with it.
+// rows, and the groups of the ranks from s0 up to and with it.
 struct Buckets {
   int expert, s0;
   int rows, incl;
@@ -191,8 +211,10 @@ __device__ __forceinline__ void load_buckets(const ProductArgs& a, int e, int s0
   const int lane = threadIdx.x & 31;
   b.expert = e;
   b.s0 = s0;
-  b.rows = s0 + lane < a.R ? bucket_count(a, e, s0 + lane) : 0;
-  b.incl = (b.rows + kGroup - 1) / kGroup;
+  int c[1];
+  bucket_counts(a, e, s0 + lane, 1, c);
+  b.rows = c[0];
+  b.incl = groups_of(b.rows);
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const int v = __shfl_up_sync(0xffffffffu, b.incl, d);
@@ -202,24 +224,30 @@ __device__ __forceinline__ void load_buckets(const ProductArgs& a, int e, int s0
 
 // Groups of expert e in order: source ranks ascending, slots ascending.  The
 // tile's share [g0, g1) goes to list, one entry per column: the row of x and y,
-// or -1 where there is none.
+// or -1 where there is none.  A lane takes a group: it finds the group's bucket
+// by a search over the lanes' sums.
 __device__ void plan_rows(const ProductArgs& a, int e, int g0, int g1, Buckets& b, int* list) {
   const int lane = threadIdx.x & 31;
   int before = 0;
   for (int s0 = 0; s0 < a.R && before < g1; s0 += 32) {
     load_buckets(a, e, s0, b);
-    const int end = before + b.incl, beg = end - (b.rows + kGroup - 1) / kGroup;
-    for (uint32_t left = __ballot_sync(0xffffffffu, max(beg, g0) < min(end, g1)); left; left &= left - 1) {
-      const int j = __ffs(left) - 1;
-      const int jbeg = __shfl_sync(0xffffffffu, beg, j), jend = __shfl_sync(0xffffffffu, end, j),
-                cnt = __shfl_sync(0xffffffffu, b.rows, j);
-      const int lo = max(jbeg, g0), hi = min(jend, g1), first = (e * a.R + s0 + j) * a.T;
-      for (int i = lo * kGroup + lane; i < hi * kGroup; i += 32) {
-        const int slot = i - jbeg * kGroup;
-        list[i - g0 * kGroup] = slot < cnt ? first + slot : -1;
+    const int end = before + __shfl_sync(0xffffffffu, b.incl, 31);
+    for (int first = max(g0, before); first < min(g1, end); first += 32) {
+      const int g = first + lane, target = g - before;
+      int s = 0;  // the first lane whose sum is above target
+#pragma unroll
+      for (int d = 16; d; d >>= 1)
+        if (__shfl_sync(0xffffffffu, b.incl, s + d - 1) <= target) s += d;
+      s = min(s, 31);
+      const int cnt = __shfl_sync(0xffffffffu, b.rows, s), incl = __shfl_sync(0xffffffffu, b.incl, s);
+      if (g < min(g1, end)) {
+        const int slot = (target - (incl - groups_of(cnt))) * kGroup, row = (e * a.R + s0 + s) * a.T + slot;
+        static_assert(kGroup == 4, "a group is one 16-byte store");
+        *reinterpret_cast<int4*>(list + (g - g0) * kGroup) =
+            make_int4(row, slot + 1 < cnt ? row + 1 : -1, slot + 2 < cnt ? row + 2 : -1, slot + 3 < cnt ? row + 3 : -1);
       }
     }
-    before += __shfl_sync(0xffffffffu, b.incl, 31);
+    before = end;
   }
   for (int i = (g1 - g0) * kGroup + lane; i < columns(g1 - g0); i += 32) list[i] = -1;
 }
@@ -246,26 +274,33 @@ __device__ void plan_tile(const ProductArgs& a, const int* prefix, int t, int ra
                           Box* boxes) {
   constexpr int kMaxRows = Shape<kMx>::kMaxRows;
   const int lane = threadIdx.x & 31;
-  int lo = 0, hi = a.E - 1;  // the largest e with prefix[e] <= t: it has tiles, for t < prefix[e + 1]
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (prefix[mid] <= t) lo = mid; else hi = mid - 1;
+  // the largest e with prefix[e] <= t / blocks (it has shares, for the next is
+  // above), 32 candidates at a time
+  const int nth = t / a.blocks;
+  int e = 0;
+  for (int span = a.E; span > 1;) {
+    const int step = (span + 31) / 32, at = e + lane * step;
+    const uint32_t below = __ballot_sync(0xffffffffu, lane * step < span && prefix[at] <= nth);
+    const int last = 31 - __clz(below);  // lane 0's is: prefix[e] <= nth
+    e += last * step;
+    span = min(step, span - last * step);
   }
-  const int e = lo, shares = (prefix[e + 1] - prefix[e]) / a.blocks;
-  const int local = t - prefix[e], share = local % shares;
+  const int shares = prefix[e + 1] - prefix[e], local = t - prefix[e] * a.blocks;
+  int block = local, share = 0;
+  if (shares > 1) {
+    block = local / shares;
+    share = local - block * shares;
+  }
   int total = 0;
-  if (a.R <= 32) {
-    load_buckets(a, e, 0, b);
-    total = __shfl_sync(0xffffffffu, b.incl, 31);
-  } else {
-    for (int s = lane; s < a.R; s += 32) total += bucket_groups(a, e, s);
-    total = __reduce_add_sync(0xffffffffu, total);
+  for (int s0 = 0; s0 < a.R; s0 += 32) {
+    load_buckets(a, e, s0, b);
+    total += __shfl_sync(0xffffffffu, b.incl, 31);
   }
   // shares of whole 32s of columns, as equal as that allows, the remainder
   // last: 1040 rows are 4 x 224 + 144 columns, 1056 as padded (five equal
   // shares would pad to 1120).  shares is the fewest that hold the total, so the
   // last is never empty.
-  const int per = columns((total + shares - 1) / shares) / kGroup;
+  const int per = shares == 1 ? total : columns((total + shares - 1) / shares) / kGroup;
   const int g0 = share * per, g1 = min(total, g0 + per);
   static_assert(kMaxRows % 32 == 0, "a share of at most kMaxRows rows pads to at most kMaxRows");
   plan_rows(a, e, g0, g1, b, list);
@@ -285,7 +320,7 @@ __device__ void plan_tile(const ProductArgs& a, const int* prefix, int t, int ra
       if (box >= 0) boxes[__popc(all & ((1u << lane) - 1))] = Box{lane * (kGroup * 128), row, box, 0};
     }
   }
-  if (lane == 0) *tile = Tile{e, local / shares, g1 - g0, count, bytes};
+  if (lane == 0) *tile = Tile{e, block, g1 - g0, count, bytes};
 }
 
 // ---------------------------------------------------------------------------
@@ -481,14 +516,14 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
   }
   if (warp == 3) tmem_alloc_pair(sbase + l.tmem, 512);
   wait_prior_grid();
-  count_tiles<kMx>(a, prefix, reinterpret_cast<int*>(smem + l.part));
+  count_shares<kMx>(a, prefix, reinterpret_cast<int*>(smem + l.part));
   tc_fence_before();
   __syncthreads();
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + l.tmem);
 
-  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, ntiles = prefix[a.E];
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, ntiles = prefix[a.E] * a.blocks;
 
   if (warp == 0 || warp == 3) {
     // ---- loads: one thread of each of two warps, on alternate steps ----------------
