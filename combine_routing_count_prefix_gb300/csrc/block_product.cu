@@ -269,14 +269,14 @@ __device__ __forceinline__ int plan_box(int row, int groups) {
   return p == 0 || p == len - (1 << size) ? size : -1;
 }
 
-template <bool kMx>
-__device__ void plan_tile(const ProductArgs& a, const int* prefix, int t, int rank, Buckets& b, Tile* tile, int* list,
-                          Box* boxes) {
-  constexpr int kMaxRows = Shape<kMx>::kMaxRows;
-  const int lane = threadIdx.x & 31;
+// Where tile t lies: expert, feature block, and which of the expert's shares.
+struct Place {
+  int expert, block, share, shares;
+};
+__device__ __forceinline__ Place find_tile(const ProductArgs& a, const int* prefix, int t) {
   // the largest e with prefix[e] <= t / blocks (it has shares, for the next is
   // above), 32 candidates at a time
-  const int nth = t / a.blocks;
+  const int lane = threadIdx.x & 31, nth = t / a.blocks;
   int e = 0;
   for (int span = a.E; span > 1;) {
     const int step = (span + 31) / 32, at = e + lane * step;
@@ -285,12 +285,22 @@ __device__ void plan_tile(const ProductArgs& a, const int* prefix, int t, int ra
     e += last * step;
     span = min(step, span - last * step);
   }
-  const int shares = prefix[e + 1] - prefix[e], local = t - prefix[e] * a.blocks;
-  int block = local, share = 0;
-  if (shares > 1) {
-    block = local / shares;
-    share = local - block * shares;
+  Place p{e, t - prefix[e] * a.blocks, 0, prefix[e + 1] - prefix[e]};
+  if (p.shares > 1) {
+    const int local = p.block;
+    p.block = local / p.shares;
+    p.share = local - p.block * p.shares;
   }
+  return p;
+}
+
+template <bool kMx>
+__device__ void plan_tile(const ProductArgs& a, const int* prefix, int t, int rank, Buckets& b, Tile* tile, int* list,
+                          Box* boxes) {
+  constexpr int kMaxRows = Shape<kMx>::kMaxRows;
+  const int lane = threadIdx.x & 31;
+  const Place place = find_tile(a, prefix, t);
+  const int e = place.expert, shares = place.shares, share = place.share;
   int total = 0;
   for (int s0 = 0; s0 < a.R; s0 += 32) {
     load_buckets(a, e, s0, b);
@@ -320,7 +330,7 @@ __device__ void plan_tile(const ProductArgs& a, const int* prefix, int t, int ra
       if (box >= 0) boxes[__popc(all & ((1u << lane) - 1))] = Box{lane * (kGroup * 128), row, box, 0};
     }
   }
-  if (lane == 0) *tile = Tile{e, block, g1 - g0, count, bytes};
+  if (lane == 0) *tile = Tile{e, place.block, g1 - g0, count, bytes};
 }
 
 // ---------------------------------------------------------------------------
@@ -527,16 +537,30 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
 
   if (warp == 0 || warp == 3) {
     // ---- loads: one thread of each of two warps, on alternate steps ----------------
+    const auto load_w = [&](uint32_t data, int k, int expert, int block, uint32_t bar) {
+      const int k0 = k * (kMx ? 128 : 64);
+      if constexpr (kSwiglu)
+        tma_tile5(data, &maps.w, k0, 0, 0, block * 16 + (int)rank * 8, expert, bar);
+      else
+        tma_tile3(data, &maps.w, k0, block * kTileFeatures + (int)rank * 128, expert, bar);
+    };
+    Place start{};
+    if (pair < ntiles) start = find_tile(a, prefix, pair);
     if (elect_one()) {
       int stage = warp == 3, i = 0;
       int turn = warp == 3;  // steps until this thread's next
       uint32_t phase = 0;
       bool ok = true;
+      // the first tile's weights fill the ring while its rows are planned
+      const int early = pair < ntiles ? min(a.steps, a.stages) : 0;
+      for (int k = turn; k < early; k += 2) {
+        if (leader) mbar_announce_tx(full + 8 * k, 2 * S::kBytesA);
+        load_w(sbase + k * S::kStage, k, start.expert, start.block, map_rank(full + 8 * k, 0));
+      }
       for (int t = pair; t < ntiles && ok; t += pairs, ++i) {
         const int slot = i % kPlanDepth;
         if (!(ok = mbar_wait(plan_full + 8 * slot, (i / kPlanDepth) & 1, a.err))) break;
         const Tile tile = tiles[slot];
-        const uint32_t bytes = 2 * S::kBytesA + tile.bytes;  // both CTAs', w and x
         // the first boxes stay in registers: read from shared memory at every
         // step, each load would wait for its box
         constexpr int kKept = 6;
@@ -548,11 +572,9 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
           if (!(ok = mbar_wait(empty + 8 * stage, phase ^ 1, a.err))) break;
           const uint32_t data = sbase + stage * S::kStage, to = data + S::kBytesA, bar = map_rank(full + 8 * stage, 0);
           const int k0 = k * (kMx ? 128 : 64);
-          if (leader) mbar_expect_tx(full + 8 * stage, bytes);
-          if constexpr (kSwiglu)
-            tma_tile5(data, &maps.w, k0, 0, 0, tile.block * 16 + (int)rank * 8, tile.expert, bar);
-          else
-            tma_tile3(data, &maps.w, k0, tile.block * kTileFeatures + (int)rank * 128, tile.expert, bar);
+          const bool has_w = i == 0 && k < early;
+          if (leader) mbar_expect_tx(full + 8 * stage, (has_w ? 0 : 2 * S::kBytesA) + tile.bytes);  // both CTAs'
+          if (!has_w) load_w(data, k, tile.expert, tile.block, bar);
 #pragma unroll
           for (int b = 0; b < kKept; ++b)
             if (b < tile.boxes) tma_rows(to + kept[b].offset, &maps.x[kept[b].size], k0, kept[b].row, bar);
@@ -917,6 +939,7 @@ int launch_product(ProductArgs& a, llmoe_stream_t stream) {
   ProductMaps maps;
   const cuuint32_t k_box = kMx ? 128 : 64;
   for (int b = 0; b < kBoxes; ++b) {
+    if (b > 0 && (uint64_t)kGroup << (b - 1) >= (uint64_t)a.R * a.T) break;  // a run is at most an expert's rows
     const cuuint64_t dims[2] = {(cuuint64_t)a.in, (cuuint64_t)a.E * a.R * a.T}, strides[1] = {a.x_row};
     const cuuint32_t box[2] = {k_box, (cuuint32_t)kGroup << b};
     if (!make_map(&maps.x[b], a.x, a.dtype, dims, strides, box, 2)) return LLMOE_ERR_CUDA;
