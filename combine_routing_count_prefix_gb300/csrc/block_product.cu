@@ -603,11 +603,11 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
     if (elect_one()) {
       int stage = 0, i = 0, sslot = 0, ring = 0;
       uint32_t phase = 0, sphase = 0;
-      int done = -S::kScaleRing;  // 8-bit: the step whose scale columns this one takes, counted over tiles,
-      int done_stage = 0;         // and the stage it was in
-      uint32_t done_phase = 0;
+      // 8-bit: steps whose products are known to be done, and the last one's stage and phase
+      int issued = 0, done = 0, done_stage = a.stages - 1;
+      uint32_t done_phase = 1;
       bool ok = true;
-      const uint64_t desc = tile_desc(sbase), sdesc = scale_desc(sbase + l.scales);
+      const uint32_t desc = tile_desc(sbase), sdesc = scale_desc(sbase + l.scales);  // they count 16 bytes
       for (int t = pair; t < ntiles && ok; t += pairs, ++i) {
         const int slot = i % kPlanDepth, buf = i & 1;
         if (!(ok = mbar_wait(plan_full + 8 * slot, (i / kPlanDepth) & 1, a.err))) break;
@@ -616,43 +616,62 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
         if (!(ok = mbar_wait(acc_empty + 8 * buf, ((i >> 1) & 1) ^ 1, a.err))) break;
         tc_fence_after();
         const uint32_t d = tmem + buf * S::kMaxRows, idesc = a.idesc | (uint32_t)(n >> 3) << 17;
-        for (int k = 0; k < a.steps; ++k) {
-          const bool last = k == a.steps - 1;
-          // descriptors count 16 bytes
-          const uint64_t da = desc + (uint32_t)(stage * (S::kStage >> 4)), db = da + (S::kBytesA >> 4);
-          if constexpr (kMx) {
-            const int b = k & 3;
-            if (b == 0 && !(ok = mbar_wait(scale_full + 8 * sslot, sphase, a.err))) break;
-            const uint64_t sa = sdesc + (uint32_t)((sslot * S::kSlot + b * 512) >> 4),
-                           sb = sdesc + (uint32_t)((sslot * S::kSlot + 2048 + b * 1024) >> 4);
-            const uint32_t ta = tmem + 2 * S::kMaxRows + ring * S::kScaleColumns, tb = ta + 4;
-            if (done >= 0) {
+        if constexpr (kMx) {
+          // two steps a turn: this thread's instructions, not the tensor core,
+          // bound the 8-bit product (496 cycles a step alone, of 422)
+          for (int k = 0; k < a.steps && ok; k += 2) {
+            const int m = k + 1 < a.steps ? 2 : 1;
+            const bool last = k + 2 >= a.steps;
+            if ((k & 2) == 0 && !(ok = mbar_wait(scale_full + 8 * sslot, sphase, a.err))) break;
+            issued += m;
+            if (issued - S::kScaleRing > done) {  // the columns' last users
+              done_stage += issued - S::kScaleRing - done;
+              done = issued - S::kScaleRing;
+              if (done_stage >= a.stages) done_stage -= a.stages, done_phase ^= 1;
               if (!(ok = mbar_wait(empty + 8 * done_stage, done_phase, a.err))) break;
-              if (++done_stage == a.stages) done_stage = 0, done_phase ^= 1;
             }
-            ++done;
-            copy_scales(ta, sa);
-            copy_scales(tb, sb);
-            if (n > 128) copy_scales(tb + 4, sb + (512 >> 4));
-            if (!(ok = mbar_wait(full + 8 * stage, phase, a.err))) break;
-            tc_fence_after();
+            const uint32_t sa = sdesc + (uint32_t)((sslot * S::kSlot + (k & 2) * 512) >> 4),
+                           sb = sdesc + (uint32_t)((sslot * S::kSlot + 2048 + (k & 2) * 1024) >> 4);
+            uint32_t ta[2];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)  // 32 bytes of K; scale j of each row's four
-              mma_mx8(d, da + 2 * j, db + 2 * j, idesc | (uint32_t)j << 4 | (uint32_t)j << 29, ta, tb, k > 0 || j > 0);
-            mma_commit_pair(empty + 8 * stage);
-            if (b == 3 || last) {
+            for (int u = 0; u < 2; ++u) {
+              ta[u] = tmem + 2 * S::kMaxRows + ring * S::kScaleColumns;
+              if (u < m) {
+                copy_scales(ta[u], sa + u * (512 >> 4));
+                copy_scales(ta[u] + 4, sb + u * (1024 >> 4));
+                if (n > 128) copy_scales(ta[u] + 8, sb + u * (1024 >> 4) + (512 >> 4));
+                if (++ring == S::kScaleRing) ring = 0;
+              }
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              if (u < m && ok) {
+                const uint32_t da = desc + (uint32_t)(stage * (S::kStage >> 4)), db = da + (S::kBytesA >> 4);
+                if (!(ok = mbar_wait(full + 8 * stage, phase, a.err))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int j = 0; j < 4; ++j)  // 32 bytes of K; scale j of each row's four
+                  mma_mx8(d, da + 2 * j, db + 2 * j, idesc | (uint32_t)j << 4 | (uint32_t)j << 29, ta[u], ta[u] + 4,
+                          k + u > 0 || j > 0);
+                mma_commit_pair(empty + 8 * stage);
+                if (++stage == a.stages) stage = 0, phase ^= 1;
+              }
+            }
+            if (((k & 2) != 0 || last) && ok) {
               mma_commit_pair(scale_empty + 8 * sslot);
               if (++sslot == S::kSlots) sslot = 0, sphase ^= 1;
             }
-            ring = (ring + 1) % S::kScaleRing;
-          } else {
+          }
+        } else {
+          for (int k = 0; k < a.steps; ++k) {
+            const uint32_t da = desc + (uint32_t)(stage * (S::kStage >> 4)), db = da + (S::kBytesA >> 4);
             if (!(ok = mbar_wait(full + 8 * stage, phase, a.err))) break;
             tc_fence_after();
 #pragma unroll
             for (int j = 0; j < 4; ++j) mma_16bit(d, da + 2 * j, db + 2 * j, idesc, k > 0 || j > 0);
             mma_commit_pair(empty + 8 * stage);
+            if (++stage == a.stages) stage = 0, phase ^= 1;
           }
-          if (++stage == a.stages) stage = 0, phase ^= 1;
         }
         if (ok) mma_commit_pair(acc_full + 8 * buf);
       }

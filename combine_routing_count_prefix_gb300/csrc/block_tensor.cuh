@@ -139,36 +139,40 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
 }
 
 // ---- products ------------------------------------------------------------------
-// Shared-memory descriptor of an operand tile stored K-major in rows of 128
-// bytes with the 128-byte swizzle: groups of 8 rows 1024 bytes apart.
-__device__ __forceinline__ uint64_t tile_desc(uint32_t addr) {
-  return (uint64_t)((addr & 0x3ffffu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
-         (uint64_t)2 << 61;
-}
-// Descriptor of 512 bytes of scales (32 rows of 16 bytes, not swizzled): groups
-// of 8 rows 128 bytes apart.
-__device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
-  return (uint64_t)((addr & 0x3ffffu) >> 4) | (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
-}
+// Shared-memory descriptors, in two words: the upper is a constant, the lower
+// holds the address.  An operand tile is stored K-major in rows of 128 bytes with
+// the 128-byte swizzle, groups of 8 rows 1024 bytes apart; 512 bytes of scales
+// are 32 rows of 16 bytes, not swizzled, groups of 8 rows 128 bytes apart.
+__device__ __forceinline__ uint32_t tile_desc(uint32_t addr) { return (addr & 0x3ffffu) >> 4 | 1u << 16; }
+__device__ __forceinline__ uint32_t scale_desc(uint32_t addr) { return (addr & 0x3ffffu) >> 4; }
+constexpr uint32_t kTileDescHigh = (1024 >> 4) | 1u << 14 | 2u << 29;
+constexpr uint32_t kScaleDescHigh = (128 >> 4) | 1u << 14;
+
 // D (+)= A B^T over 32 bytes of K, M = 256 over the pair.
-__device__ __forceinline__ void mma_16bit(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma_16bit(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)add), "n"(kTileDescHigh)
       : "memory");
 }
-__device__ __forceinline__ void mma_mx8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
+__device__ __forceinline__ void mma_mx8(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
                                         bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"((uint32_t)add)
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+      "mov.b64 a, {%1, %7};\n\tmov.b64 b, {%2, %7};\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], a, b, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(sa), "r"(sb), "r"((uint32_t)add), "n"(kTileDescHigh)
       : "memory");
 }
 // 512 bytes of scales from each CTA's shared memory to its tensor memory.
-__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+__device__ __forceinline__ void copy_scales(uint32_t tmem, uint32_t desc) {
+  asm volatile(
+      "{\n\t.reg .b64 s;\n\tmov.b64 s, {%1, %2};\n\t"
+      "tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], s;\n\t}" ::"r"(tmem),
+      "r"(desc), "n"(kScaleDescHigh)
+      : "memory");
 }
 // Arrives on the barrier at this offset of both CTAs when this thread's
 // products and copies so far are done.
