@@ -351,8 +351,9 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi, bool fp16) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-__device__ __forceinline__ uint8_t* y_row(const ProductArgs& a, int row) {
-  return a.y + (uint64_t)(uint32_t)row * a.y_row;
+// `at`, an address in row 0 of y, moved to `row`.
+__device__ __forceinline__ uint8_t* in_row(const ProductArgs& a, uint8_t* at, int row) {
+  return at + (uint64_t)(uint32_t)row * a.y_row;
 }
 
 // 32 columns (rows of y) of 32 features: lane l holds feature first + l.
@@ -361,10 +362,15 @@ __device__ __forceinline__ uint8_t* y_row(const ProductArgs& a, int row) {
 __device__ __forceinline__ void store_plain(const ProductArgs& a, const float (&v)[32], int first, const int* list) {
   const int lane = threadIdx.x & 31;
   if (a.out_dtype == LLMOE_DTYPE_FP32) {
+    if (first + lane >= a.out) return;
+    uint8_t* at = a.y + (uint64_t)(first + lane) * 4;
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      const int row = list[j];
-      if (row >= 0 && first + lane < a.out) reinterpret_cast<float*>(y_row(a, row))[first + lane] = v[j];
+    for (int j = 0; j < 32; j += 4) {
+      const int4 row = *reinterpret_cast<const int4*>(list + j);
+      if (row.x >= 0) *reinterpret_cast<float*>(in_row(a, at, row.x)) = v[j];
+      if (row.y >= 0) *reinterpret_cast<float*>(in_row(a, at, row.y)) = v[j + 1];
+      if (row.z >= 0) *reinterpret_cast<float*>(in_row(a, at, row.z)) = v[j + 2];
+      if (row.w >= 0) *reinterpret_cast<float*>(in_row(a, at, row.w)) = v[j + 3];
     }
     return;
   }
@@ -372,15 +378,21 @@ __device__ __forceinline__ void store_plain(const ProductArgs& a, const float (&
   // lanes the first column of a pair, odd lanes the second
   const bool odd = lane & 1, fp16 = a.out_dtype == LLMOE_DTYPE_FP16;
   const int feature = first + (lane & ~1);
+  const bool in = feature < a.out;
+  uint8_t* at = a.y + (uint64_t)feature * 2;
   int row[16];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) row[i] = feature < a.out ? list[2 * i + odd] : -1;
+  for (int i = 0; i < 16; i += 2) {
+    const int4 r = *reinterpret_cast<const int4*>(list + 2 * i);
+    row[i] = odd ? r.y : r.x;
+    row[i + 1] = odd ? r.w : r.z;
+  }
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     // both columns of this lane's feature in one word: it keeps one half
     const uint32_t mine = pack2(v[2 * i], v[2 * i + 1], fp16), got = __shfl_xor_sync(0xffffffffu, mine, 1);
-    const uint32_t u = odd ? __byte_perm(got, mine, 0x7632) : __byte_perm(mine, got, 0x5410);
-    if (row[i] >= 0) *reinterpret_cast<uint32_t*>(y_row(a, row[i]) + (uint32_t)feature * 2) = u;
+    const uint32_t u = __byte_perm(mine, got, odd ? 0x3276 : 0x5410);
+    if (in && row[i] >= 0) *reinterpret_cast<uint32_t*>(in_row(a, at, row[i])) = u;
   }
 }
 
@@ -446,13 +458,13 @@ __device__ __forceinline__ bool store_swiglu(const ProductArgs& a, const float (
       b = __byte_perm(b, got, lane & 1 ? 0x3715 : 0x6240);
       got = __shfl_xor_sync(0xffffffffu, b, 2);
       b = __byte_perm(b, got, lane & 2 ? 0x3276 : 0x5410);
-      if (row[g] >= 0) *reinterpret_cast<uint32_t*>(y_row(a, row[g]) + (uint32_t)(feature - q)) = b;
+      if (row[g] >= 0) *reinterpret_cast<uint32_t*>(in_row(a, a.y + (feature - q), row[g])) = b;
     }
     if (my_row >= 0) {
-      uint8_t* s = y_row(a, my_row) + a.out + first / 32;
+      uint8_t* s = in_row(a, a.y + a.out + first / 32, my_row);
       *s = (uint8_t)mine;
       if (first + 32 == a.out)
-        for (uint8_t* end = y_row(a, my_row) + a.y_row; ++s < end;) *s = 0;
+        for (uint8_t* end = in_row(a, a.y + a.y_row, my_row); ++s < end;) *s = 0;
     }
     return true;
   }
@@ -460,7 +472,7 @@ __device__ __forceinline__ bool store_swiglu(const ProductArgs& a, const float (
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const int row = list[2 * i + up];
-      if (row >= 0 && feature < a.out) reinterpret_cast<float*>(y_row(a, row))[feature] = h[i];
+      if (row >= 0 && feature < a.out) *reinterpret_cast<float*>(in_row(a, a.y + (uint64_t)feature * 4, row)) = h[i];
     }
     return true;
   }
@@ -472,8 +484,8 @@ __device__ __forceinline__ bool store_swiglu(const ProductArgs& a, const float (
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const uint32_t mine = pack2(h[2 * i], h[2 * i + 1], fp16), got = __shfl_xor_sync(0xffffffffu, mine, 1);
-    const uint32_t u = odd ? __byte_perm(got, mine, 0x7632) : __byte_perm(mine, got, 0x5410);
-    if (row[i] >= 0) *reinterpret_cast<uint32_t*>(y_row(a, row[i]) + (uint32_t)even_feature * 2) = u;
+    const uint32_t u = __byte_perm(mine, got, odd ? 0x3276 : 0x5410);
+    if (row[i] >= 0) *reinterpret_cast<uint32_t*>(in_row(a, a.y + (uint64_t)even_feature * 2, row[i])) = u;
   }
   return true;
 }
