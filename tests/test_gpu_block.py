@@ -227,6 +227,19 @@ def test_router_masked_experts(L, scoring):
         assert np.allclose(gw, w, rtol=64 * 2.0 ** -23, atol=0)
 
 
+@pytest.mark.parametrize("E", [256, 100, 257])
+def test_router_logits_not_16_byte_aligned(L, E):
+    rows, K = 70, 8
+    flat = torch.randint(-24, 25, (rows * E + 1,), generator=rnd(E)).float() / 8
+    at = flat.cuda()[1:]
+    idx = torch.empty(rows, K, dtype=torch.int64, device="cuda")
+    w = torch.empty(rows, K, device="cuda")
+    L.llmoe_topk_router(at, None, None, idx, w, rows, E, K, L.LLMOE_DTYPE_FP32, L.LLMOE_SCORE_SOFTMAX, 0, 1.0)
+    want, ww, _ = ref.router(flat[1:].reshape(rows, E).numpy(), None, None, K, "softmax", False, 1.0)
+    assert np.array_equal(idx.cpu().numpy(), want)
+    assert (np.abs(w.cpu().double().numpy() - ww) <= ww * (E / 32 + K + 32) * 2.0 ** -23).all()
+
+
 def test_router_no_rows(L):
     L.llmoe_topk_router(None, None, None, None, None, 0, 8, 2, L.LLMOE_DTYPE_FP32, 0, 0, 1.0)
     torch.cuda.synchronize()
@@ -365,6 +378,47 @@ def test_product_is_reproducible_and_captures(L, dtype):
     assert torch.equal(ys[0], ys[1]) and torch.equal(ys[0], ys[2])
 
 
+@pytest.mark.parametrize("dtype,out_dtype", [("bf16", "bf16"), ("mx8", "bf16"), ("mx8", "mx8")])
+def test_product_nan_stays_in_its_row_and_feature(L, dtype, out_dtype):
+    R, T, E, n_in, n_out = 1, 40, 2, 256, 128
+    counts = torch.tensor([[40], [7]], dtype=torch.int64, device="cuda")
+    swiglu = out_dtype == "mx8"
+    x, _ = make_rows(L, E * R * T, n_in, dtype, 1)
+    w, _ = make_rows(L, E * n_out * (1 + swiglu), n_in, dtype, 2, 0.1)
+    code = L.ROW_DTYPE_CODES
+    rb = L.llmoe_row_bytes(n_out, code[out_dtype])
+
+    def run():
+        y = torch.zeros(E * R * T, rb, dtype=torch.uint8, device="cuda")
+        L.llmoe_expert_product(x, w, y, counts, n_in, n_out, code[dtype], code[out_dtype], int(swiglu), L.geometry(T, R, E))
+        return y.cpu()
+
+    clean = run()
+    if dtype == "mx8":
+        x[5, n_in + 3] = 255  # the NaN scale of one group
+        w[n_out * (1 + swiglu) + 9, n_in] = 255  # feature (or gate) 9 of expert 1
+    else:
+        x[5, 100] = float("nan")
+        w[n_out + 9, 0] = float("inf")
+    got = run()
+    same = np.ones(E * T, bool)
+    same[5] = False
+    same[T:T + 7] = False
+    assert torch.equal(got[torch.from_numpy(same)], clean[torch.from_numpy(same)])
+    if out_dtype == "mx8":
+        assert (got[5, n_out:n_out + n_out // 32] == 255).all()  # every group holds a NaN
+        hit = got[T:T + 7]
+        assert (hit[:, n_out] == 255).all()  # the group of feature 9, and no other
+        assert torch.equal(hit[:, 32:n_out], clean[T:T + 7, 32:n_out])
+        assert torch.equal(hit[:, n_out + 1:], clean[T:T + 7, n_out + 1:])
+    else:
+        v, c = got.view(torch.bfloat16), clean.view(torch.bfloat16)
+        assert v[5].isnan().all()
+        others = [f for f in range(n_out) if f != 9]
+        assert torch.equal(v[T:T + 7][:, others], c[T:T + 7][:, others])
+        assert not v[T:T + 7, 9].isfinite().any()
+
+
 @pytest.mark.parametrize("bad", [-3, 18])
 def test_product_bad_count_is_reported_and_clamped(L, bad):
     R, T, E = 1, 17, 2
@@ -382,6 +436,89 @@ def test_product_bad_count_is_reported_and_clamped(L, bad):
     rest = np.ones(len(y), bool)
     rest[at] = False
     assert not wide(y)[rest].any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "mx8"])
+def test_product_most_experts(L, dtype):
+    R, T, E = 1, 1, 8192
+    c = (np.random.RandomState(3).rand(E, 1) < 0.3).astype(np.int64)
+    check_product(L, R, T, E, 32, 32, dtype, "bf16", dtype == "mx8", c)
+
+
+@pytest.mark.parametrize("n_in,n_out", [(4096, 64), (64, 4096)])
+def test_product_offsets_past_32_bits(L, n_in, n_out):
+    """x or y larger than 4 GiB, rows received at the very end of it."""
+    R, T, E = 1, 80000, 8
+    rows = E * R * T
+    counts = np.array([[2], [0], [0], [0], [0], [0], [0], [T]], np.int64)
+    counts[3] = 5
+    used = np.concatenate([np.arange(2), np.arange(3 * T, 3 * T + 5), np.arange(rows - 3, rows)])
+    g = rnd(5)
+    x = torch.zeros(rows, n_in, dtype=torch.bfloat16, device="cuda")
+    xv = torch.randn(len(used), n_in, generator=g).bfloat16()
+    x[torch.from_numpy(used).cuda()] = xv.cuda()
+    w = (torch.randn(E, n_out, n_in, generator=g) * n_in ** -0.5).bfloat16()
+    y = torch.zeros(rows, n_out, dtype=torch.bfloat16, device="cuda")
+    L.llmoe_expert_product(x, w.cuda(), y, torch.from_numpy(counts).cuda(), n_in, n_out, 0, 0, 0, L.geometry(T, R, E))
+    got = wide(y[torch.from_numpy(used).cuda()])
+    for i, r in enumerate(used):
+        a, b = wide(xv)[i], wide(w)[r // T]
+        close(got[i], b @ a, n_in * 2.0 ** -23 * (np.abs(b) @ np.abs(a)), "bf16")
+    assert not bool(y[2:3 * T].any()) and not bool(y[3 * T + 5:7 * T].any())
+    del x, y
+    torch.cuda.empty_cache()
+
+
+def test_norm_offsets_past_32_bits(L):
+    rows, hidden = 300000, 7168  # 4.3 GB
+    x = torch.ones(rows, hidden, dtype=torch.bfloat16, device="cuda")
+    last = torch.randn(3, hidden, generator=rnd(2)).bfloat16()
+    x[-3:] = last.cuda()
+    w = torch.ones(hidden, dtype=torch.bfloat16, device="cuda")
+    L.llmoe_add_rmsnorm(x, None, w, 0.0, None, x, rows, hidden, 0, 0)
+    v = ref.rmsnorm(wide(last), np.ones(hidden), 0.0)
+    close(wide(x[-3:]), v, np.abs(v) * NORM_ERR, "bf16")
+    assert bool((x[:-3] == 1).all())
+    del x
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "mx8"])
+def test_product_of_tensors_16_bytes_off(L, dtype):
+    """Every pointer 16-byte aligned and no more."""
+    R, T, E, n_in, n_out = 2, 11, 4, 160, 96
+    counts = some_counts(E, R, T, "ragged", 8)
+    x, xv = make_rows(L, E * R * T, n_in, dtype, 1)
+    w, wv = make_rows(L, E * n_out, n_in, dtype, 2, 0.1)
+    shift = lambda t: torch.cat([torch.zeros(16, dtype=torch.uint8, device="cuda"), t.reshape(-1).view(torch.uint8)])[16:]
+    y = torch.zeros(16 + E * R * T * n_out * 2, dtype=torch.uint8, device="cuda")[16:]
+    L.llmoe_expert_product(shift(x), shift(w), y, torch.from_numpy(counts).cuda(), n_in, n_out,
+                           L.ROW_DTYPE_CODES[dtype], 0, 0, L.geometry(T, R, E))
+    at, v, err = ref.product(xv, wv.reshape(E, n_out, n_in), counts, T, False)
+    close(wide(y.view(torch.bfloat16).reshape(-1, n_out))[at], v, err, "bf16")
+
+
+def test_products_on_two_streams_at_once(L):
+    """Two calls in flight, each with every SM in its grid."""
+    R, T, E, n = 2, 200, 8, 512
+    c = torch.from_numpy(some_counts(E, R, T, "ragged", 6)).cuda()
+    bs = L.geometry(T, R, E)
+    sets = []
+    for dtype in ("bf16", "mx8"):
+        x, _ = make_rows(L, E * R * T, n, dtype, 3)
+        w, _ = make_rows(L, E * n, n, dtype, 4, 0.05)
+        ys = [torch.zeros(E * R * T, n, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        sets.append((x, w, ys, L.ROW_DTYPE_CODES[dtype], torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for x, w, ys, code, _ in sets:
+        L.llmoe_expert_product(x, w, ys[0], c, n, n, code, 0, 0, bs)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for x, w, ys, code, s in sets:
+            L.llmoe_expert_product(x, w, ys[1], c, n, n, code, 0, 0, bs, s)
+    torch.cuda.synchronize()
+    for _, _, ys, _, _ in sets:
+        assert torch.equal(ys[0], ys[1]) and bool(ys[0].any())
 
 
 # ---------------------------------------------------------------------------
