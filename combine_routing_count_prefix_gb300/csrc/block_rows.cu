@@ -5,11 +5,12 @@
 // residual, h = T(x + residual), the sum of squares over the CTA in fp32, then
 // v = h * r * weight from the registers and 16-byte (MX8: 8-byte) stores.
 // Every byte is read and written once, so HBM bandwidth bounds a large call
-// (8192 rows of 7168 bf16 with a residual to MX8: 63.5 us, 6.5 TB/s, 97% of the
-// copy rate), launch and load latency a small one (one row 2.4 us).  A few
-// large CTAs per SM stay for all rows and prefetch their next row into L2:
-// 152 rows 3.3 us against 4.3 with twice the quads per thread and a CTA per
-// row, 2048 rows 19.3 against 19.9, 8192 63.5 against 65.4.  Sums are packed
+// (8192 rows of 7168 bf16 with a residual to MX8: 62.9 us, 6.6 TB/s, 98% of the
+// copy rate), launch and load latency a small one (one row 2.3 us, 1024 rows
+// 10.9).  A few large CTAs per SM stay for all rows and load the next row into
+// the registers that the sum has just freed: 1024 rows 10.9 us against 12.6 with
+// the next row prefetched into L2, and 12.7 with a CTA per row.  Two quads a
+// thread rather than four: 152 rows 3.1 us against 4.3.  Sums are packed
 // additions of T and the fp32 arithmetic is on pairs.
 #include "block_common.cuh"
 
@@ -111,27 +112,24 @@ __global__ void __launch_bounds__(1024) rows_kernel(RowsArgs a) {
   release_next_grid();
   wait_prior_grid();
   const int tid = threadIdx.x, nthr = blockDim.x;
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    const uint4* x = a.x + row * a.nq;
-    uint4 h[Q], res[Q];
+  uint4 x[Q], res[Q];  // the next row to be normed
+  const auto load = [&](int64_t row) {
 #pragma unroll
     for (int i = 0; i < Q; ++i) {
       const int j = tid + i * nthr;
-      h[i] = j < a.nq ? x[j] : make_uint4(0, 0, 0, 0);
+      x[i] = j < a.nq ? a.x[row * a.nq + j] : make_uint4(0, 0, 0, 0);
       if (kNorm && a.residual != nullptr) res[i] = j < a.nq ? a.residual[row * a.nq + j] : make_uint4(0, 0, 0, 0);
     }
-    // the next row's lines start on their way to L2
-    if (const int64_t next = row + gridDim.x; next < a.rows) {
-      for (int o = tid * 8; o < a.nq; o += nthr * 8) {
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.x + next * a.nq + o));
-        if (kNorm && a.residual != nullptr) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.residual + next * a.nq + o));
-      }
-    }
-    Pair r2 = 0;
-    if constexpr (kNorm) {
-      Pair sum = 0;  // of squares
+  };
+  int64_t row = blockIdx.x;
+  if (row < a.rows) load(row);
+  for (; row < a.rows; row += gridDim.x) {
+    uint4 h[Q];
+    Pair sum = 0;  // of squares
 #pragma unroll
-      for (int i = 0; i < Q; ++i) {
+    for (int i = 0; i < Q; ++i) {
+      h[i] = x[i];
+      if constexpr (kNorm) {
         const int j = tid + i * nthr;
         if (a.residual != nullptr) h[i] = add_quad<DT>(h[i], res[i]);  // the norm is of the rounded sum
         if (a.residual_out != nullptr && j < a.nq) a.residual_out[row * a.nq + j] = h[i];
@@ -140,6 +138,12 @@ __global__ void __launch_bounds__(1024) rows_kernel(RowsArgs a) {
 #pragma unroll
         for (int k = 0; k < P; ++k) sum = fma2(v[k], v[k], sum);
       }
+    }
+    // its registers are free: the next row is on its way while this one's sum
+    // crosses the CTA and its output is written
+    if (row + gridDim.x < a.rows) load(row + gridDim.x);
+    Pair r2 = 0;
+    if constexpr (kNorm) {
       const float2 s = unpair(sum);
       const float r = 1.0f / sqrtf(block_sum(s.x + s.y, part) * a.inv_n + a.eps);
       r2 = pair(r, r);
@@ -205,8 +209,7 @@ template <int DT, bool MX, bool kNorm>
 int launch_rows(const RowsArgs& a, llmoe_stream_t stream) {
   // two quads per thread where a CTA has threads enough; as many CTAs as the
   // registers (64 a thread) hold
-  int threads = 128;
-  while (threads < 1024 && threads * 2 < a.nq) threads *= 2;
+  const int threads = std::min(1024, std::max(128, (a.nq / 2 + 31) / 32 * 32));
   const unsigned grid = (unsigned)std::min<int64_t>(a.rows, (int64_t)num_sms() * (1024 / threads));
   const int q = (a.nq + threads - 1) / threads;
   if (q <= 1) return launch_block(rows_kernel<DT, MX, 1, kNorm>, grid, threads, 0, stream, a);
