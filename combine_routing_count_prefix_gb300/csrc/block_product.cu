@@ -549,26 +549,11 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
 
   if (warp == 0 || warp == 3) {
     // ---- loads: one thread of each of two warps, on alternate steps ----------------
-    const auto load_w = [&](uint32_t data, int k, int expert, int block, uint32_t bar) {
-      const int k0 = k * (kMx ? 128 : 64);
-      if constexpr (kSwiglu)
-        tma_tile5(data, &maps.w, k0, 0, 0, block * 16 + (int)rank * 8, expert, bar);
-      else
-        tma_tile3(data, &maps.w, k0, block * kTileFeatures + (int)rank * 128, expert, bar);
-    };
-    Place start{};
-    if (pair < ntiles) start = find_tile(a, prefix, pair);
     if (elect_one()) {
       int stage = warp == 3, i = 0;
       int turn = warp == 3;  // steps until this thread's next
       uint32_t phase = 0;
       bool ok = true;
-      // the first tile's weights fill the ring while its rows are planned
-      const int early = pair < ntiles ? min(a.steps, a.stages) : 0;
-      for (int k = turn; k < early; k += 2) {
-        if (leader) mbar_announce_tx(full + 8 * k, 2 * S::kBytesA);
-        load_w(sbase + k * S::kStage, k, start.expert, start.block, map_rank(full + 8 * k, 0));
-      }
       for (int t = pair; t < ntiles && ok; t += pairs, ++i) {
         const int slot = i % kPlanDepth;
         if (!(ok = mbar_wait(plan_full + 8 * slot, (i / kPlanDepth) & 1, a.err))) break;
@@ -584,9 +569,11 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
           if (!(ok = mbar_wait(empty + 8 * stage, phase ^ 1, a.err))) break;
           const uint32_t data = sbase + stage * S::kStage, to = data + S::kBytesA, bar = map_rank(full + 8 * stage, 0);
           const int k0 = k * (kMx ? 128 : 64);
-          const bool has_w = i == 0 && k < early;
-          if (leader) mbar_expect_tx(full + 8 * stage, (has_w ? 0 : 2 * S::kBytesA) + tile.bytes);  // both CTAs'
-          if (!has_w) load_w(data, k, tile.expert, tile.block, bar);
+          if (leader) mbar_expect_tx(full + 8 * stage, 2 * S::kBytesA + tile.bytes);  // both CTAs', w and x
+          if constexpr (kSwiglu)
+            tma_tile5(data, &maps.w, k0, 0, 0, tile.block * 16 + (int)rank * 8, tile.expert, bar);
+          else
+            tma_tile3(data, &maps.w, k0, tile.block * kTileFeatures + (int)rank * 128, tile.expert, bar);
 #pragma unroll
           for (int b = 0; b < kKept; ++b)
             if (b < tile.boxes) tma_rows(to + kept[b].offset, &maps.x[kept[b].size], k0, kept[b].row, bar);

@@ -484,6 +484,36 @@ def test_norm_offsets_past_32_bits(L):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "mx8"])
+def test_product_many_calls(L, dtype):
+    """Calls with cold caches, warm ones and after other kernels: the same bits
+    every time and no wait that expires."""
+    R, T, E, K, n_in, n_out = 1, 128, 256, 8, 2048, 512
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    bs = L.geometry(T, R, E, err=err)
+    code = L.ROW_DTYPE_CODES
+    g = rnd(31)
+    x, _ = make_rows(L, E * R * T // 64, n_in, dtype, 1)
+    x = x.repeat(64, 1)
+    w, _ = make_rows(L, 64 * 2 * n_out, n_in, dtype, 2, 0.05)
+    w = w.repeat(4, 1)
+    flush = torch.empty(64 << 20, dtype=torch.float32, device="cuda")
+    for _ in range(12):
+        counts = torch.zeros(E, R, dtype=torch.int64)
+        counts[torch.randperm(E, generator=g)[:K]] = 1
+        c = counts.cuda()
+        first = None
+        for call in range(40):
+            y = torch.zeros(E * R * T, n_out, dtype=torch.bfloat16, device="cuda")
+            if call % 4 == 1:
+                flush.add_(1)
+            L.llmoe_expert_product(x, w, y, c, n_in, n_out, code[dtype], 0, L.LLMOE_PRODUCT_SWIGLU, bs)
+            first = y if first is None else first
+            assert torch.equal(first, y)
+        assert int(err) == 0
+        assert int(first.any(1).sum()) == K
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "mx8"])
 def test_product_of_tensors_16_bytes_off(L, dtype):
     """Every pointer 16-byte aligned and no more."""
     R, T, E, n_in, n_out = 2, 11, 4, 160, 96
