@@ -497,7 +497,7 @@ def test_product_many_calls(L, dtype):
     w, _ = make_rows(L, 64 * 2 * n_out, n_in, dtype, 2, 0.05)
     w = w.repeat(4, 1)
     flush = torch.empty(64 << 20, dtype=torch.float32, device="cuda")
-    for _ in range(12):
+    for _ in range(6):
         counts = torch.zeros(E, R, dtype=torch.int64)
         counts[torch.randperm(E, generator=g)[:K]] = 1
         c = counts.cuda()
