@@ -455,7 +455,7 @@ __device__ __forceinline__ bool store_swiglu(const ProductArgs& a, const float (
     amax[warp * 32 + up * 16 + at] = m[0];
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
-    if (!mbar_wait(bar, parity, a.err)) return false;
+    if (!mbar_wait_warp(bar, parity, a.err)) return false;
     uint32_t mine = 0;  // the scale code of column 2 at + up
     uint32_t code[16];
 #pragma unroll
@@ -702,7 +702,7 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
     Buckets buckets{-1, 0, 0, 0};
     for (int t = pair; t < ntiles; t += pairs, ++i) {
       const int slot = i % kPlanDepth;
-      if (!mbar_wait(plan_empty + 8 * slot, ((i / kPlanDepth) & 1) ^ 1, a.err)) break;
+      if (!mbar_wait_warp(plan_empty + 8 * slot, ((i / kPlanDepth) & 1) ^ 1, a.err)) break;
       plan_tile<kMx>(a, prefix, t, (int)rank, buckets, tiles + slot, rows + slot * S::kMaxRows, boxes + 32 * slot);
       __syncwarp();
       if (lane == 0) mbar_arrive(plan_full + 8 * slot);
@@ -715,12 +715,12 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
     int i = 0, flip = 0;
     for (int t = pair; t < ntiles; t += pairs, ++i) {
       const int slot = i % kPlanDepth, buf = i & 1;
-      if (!mbar_wait(plan_full + 8 * slot, (i / kPlanDepth) & 1, a.err)) break;
+      if (!mbar_wait_warp(plan_full + 8 * slot, (i / kPlanDepth) & 1, a.err)) break;
       const Tile tile = tiles[slot];
       const int* list = rows + slot * S::kMaxRows;
       const int first = kSwiglu ? tile.block * 128 + (int)rank * 64 + w * 16
                                 : tile.block * kTileFeatures + (int)rank * 128 + w * 32;
-      if (!mbar_wait(acc_full + 8 * buf, (i >> 1) & 1, a.err)) break;
+      if (!mbar_wait_warp(acc_full + 8 * buf, (i >> 1) & 1, a.err)) break;
       tc_fence_after();
       const uint32_t acc = tmem + ((uint32_t)(32 * w) << 16) + buf * S::kMaxRows;
       bool ok = true;
@@ -758,7 +758,7 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
     bool ok = true;
     for (int t = pair; t < ntiles && ok; t += pairs, ++i) {
       const int slot = i % kPlanDepth;
-      if (!(ok = mbar_wait(plan_full + 8 * slot, (i / kPlanDepth) & 1, a.err))) break;
+      if (!(ok = mbar_wait_warp(plan_full + 8 * slot, (i / kPlanDepth) & 1, a.err))) break;
       const Tile tile = tiles[slot];
       const int n = columns(tile.groups), m = 32 * q + lane;
       const int f = min(kSwiglu ? (m >> 3 & 1) * a.out + tile.block * 128 + (int)rank * 64 + (m >> 4) * 8 + (m & 7)
@@ -786,7 +786,7 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
         for (int u = 0; u < kAhead; ++u) {
           const int c = c0 + u;
           if (c >= chunks || !ok) break;
-          if (!(ok = mbar_wait(scale_empty + 8 * sslot, sphase ^ 1, a.err))) break;
+          if (!(ok = mbar_wait_warp(scale_empty + 8 * sslot, sphase ^ 1, a.err))) break;
           uint8_t* dst = smem + l.scales + sslot * S::kSlot + lane * 16 + q * 4;
 #pragma unroll
           for (int b = 0; b < 4; ++b) {
@@ -813,7 +813,7 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
       }
     }
     for (int s = 0; s < S::kSlots && ok; ++s) {  // as the ring
-      ok = mbar_wait(scale_empty + 8 * sslot, sphase ^ 1, a.err);
+      ok = mbar_wait_warp(scale_empty + 8 * sslot, sphase ^ 1, a.err);
       if (++sslot == S::kSlots) sslot = 0, sphase ^= 1;
     }
   }

@@ -85,7 +85,8 @@ class MoEBlock:
         self.recv_src = torch.empty(received, dtype=torch.int32, device=dev)
         self.h = torch.empty(received, llmoe.llmoe_row_bytes(self.I, self.row_code), dtype=torch.uint8, device=dev)
         self.y = torch.empty(received, self.H, dtype=t, device=dev)
-        self.token_counts = {}
+        # the router product's one count, for every number of tokens a call may have
+        self.token_counts = torch.arange(self.T + 1, dtype=torch.int64, device=dev) * self.R
 
     def forward(self, x: torch.Tensor, residual: torch.Tensor, out: torch.Tensor,
                 active: torch.Tensor | None = None) -> torch.Tensor:
@@ -97,15 +98,13 @@ class MoEBlock:
             raise ValueError(f"x holds {R} ranks of {n} tokens, the block {self.R} of at most {self.T}")
         tokens = R * n
         L, code, row_code = llmoe, self.code, self.row_code
-        if n not in self.token_counts:
-            self.token_counts[n] = torch.tensor([[tokens]], dtype=torch.int64, device=x.device)
         if row_code == code:
             L.llmoe_add_rmsnorm(x, residual, self.norm_weight, self.eps, residual, self.xn, tokens, H, code, code)
         else:
             L.llmoe_add_rmsnorm(x, residual, self.norm_weight, self.eps, residual, self.rows, tokens, H, code, row_code)
             L.llmoe_add_rmsnorm(residual, None, self.norm_weight, self.eps, None, self.xn, tokens, H, code, code)
         # a dense product is one expert that every token was sent to
-        L.llmoe_expert_product(self.xn, self.router_weight, self.logits, self.token_counts[n], H, E, code,
+        L.llmoe_expert_product(self.xn, self.router_weight, self.logits, self.token_counts[n:n + 1], H, E, code,
                                L.LLMOE_DTYPE_FP32, 0, L.geometry(max(1, R * self.T), 1, 1, self.err))
         L.llmoe_topk_router(self.logits, self.router_bias, active, self.topk_idx, self.topk_w, tokens, E, self.K,
                             L.LLMOE_DTYPE_FP32, self.scoring, L.LLMOE_ROUTER_RENORM, self.scale)
