@@ -134,6 +134,11 @@ __device__ __forceinline__ void trace_phase(int base, int p) {
 // complete and flush before its first global memory access (a no-op when
 // launched without the attribute).  With LLMOE_FLAG_INPUTS_READY, dispatch
 // and combine read their routing inputs before that wait.
+// A pointer that a kernel loads through is not __restrict__: to the compiler
+// the wait cannot change memory that only such an argument names, and it moves
+// loads from it to before the wait, where a router's topk_idx, written by the
+// kernel before, may not be there yet.  (A kernel that only stores through
+// one keeps it: what it stores comes from loads behind the wait.)
 __device__ __forceinline__ void wait_prior_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void release_next_grid() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
@@ -173,7 +178,7 @@ constexpr int kPrefetch = 8;  // prefix ids a thread has in flight per pass
 __device__ __forceinline__ void sync_all() { __syncthreads(); }
 
 template <void (*Sync)() = sync_all>
-__device__ void route_hist(const Geometry& g, const int64_t* __restrict__ idx, int src, int t0, int t1,
+__device__ void route_hist(const Geometry& g, const int64_t* idx, int src, int t0, int t1,
                            const RouteSmem& s, int tid, int nthr) {
   const int K = g.K, E = g.E;
   const int64_t* src_idx = idx + (int64_t)src * g.T * K;
@@ -267,7 +272,7 @@ __device__ __forceinline__ void put_signal(const Geometry& g, int64_t* word, int
 // = rows expert e returns to src), and the count CTAs together zero the other
 // set's words when LLMOE_FLAG_CLEAN_OTHER_SET asks for it.  They move no rows,
 // so no data CTA carries the counts after its rows.
-__device__ void count_source(const Geometry& g, const int64_t* __restrict__ idx, int src, const RouteSmem& s,
+__device__ void count_source(const Geometry& g, const int64_t* idx, int src, const RouteSmem& s,
                              bool early, bool dispatch_words) {
   release_next_grid();
   if (!early) wait_prior_grid();
@@ -482,8 +487,8 @@ __device__ __forceinline__ void consumers_sync() {
 // llmoe_unpack makes from the messages: the CTA holds the row and knows the
 // slot, so it stores the row as it is (aligned) beside the message.
 template <bool kRows>
-__global__ void __launch_bounds__(kDspThreads, 8) dispatch_kernel(Geometry g, const void* __restrict__ x,
-                                                               const int64_t* __restrict__ idx,
+__global__ void __launch_bounds__(kDspThreads, 8) dispatch_kernel(Geometry g, const void* x,
+                                                               const int64_t* idx,
                                                                void* __restrict__ recv_x,
                                                                int32_t* __restrict__ recv_src) {
   extern __shared__ __align__(128) unsigned char smem[];
@@ -706,9 +711,9 @@ constexpr int kKBatch = 8;  // most expert-row loads a lane has in flight
 // quads (512 B) of one output row per unit: up to kKBatch expert rows are
 // loaded (16 B per lane each) before they are accumulated, in ascending k.
 template <int DT, int KB>  // KB: expert-row loads in flight per lane, the top-k rounded up to 2, 4 or 8
-__global__ void __launch_bounds__(kCmbThreads) combine_kernel(Geometry g, const void* __restrict__ y,
-                                                              const int64_t* __restrict__ idx,
-                                                              const float* __restrict__ topk_w,
+__global__ void __launch_bounds__(kCmbThreads) combine_kernel(Geometry g, const void* y,
+                                                              const int64_t* idx,
+                                                              const float* topk_w,
                                                               void* __restrict__ out) {
   extern __shared__ __align__(128) unsigned char smem[];
   const RouteSmem s = carve_route(smem, g);
@@ -861,8 +866,8 @@ __device__ __forceinline__ uint4 unshift_words(const uint4& a, const uint4& b, i
 // combine_recv[e][t] (row e * T_max + t of its receive region).  One warp
 // moves 32 quads of one entry's row per unit; rank src's flag words are
 // written by the CTA of its last token block.
-__global__ void __launch_bounds__(kThreads, 4) combine_put_kernel(Geometry g, const void* __restrict__ y,
-                                                                  const int64_t* __restrict__ idx) {
+__global__ void __launch_bounds__(kThreads, 4) combine_put_kernel(Geometry g, const void* y,
+                                                                  const int64_t* idx) {
   extern __shared__ __align__(128) unsigned char smem[];
   const RouteSmem s = carve_route(smem, g);
   const int TBK = g.TB * g.K;
@@ -991,8 +996,8 @@ struct RedMeta {
 };
 
 template <int DT>
-__global__ void __launch_bounds__(kRedThreads) combine_reduce_ring_kernel(Geometry g, const int64_t* __restrict__ idx,
-                                                                          const float* __restrict__ topk_w,
+__global__ void __launch_bounds__(kRedThreads) combine_reduce_ring_kernel(Geometry g, const int64_t* idx,
+                                                                          const float* topk_w,
                                                                           void* __restrict__ out) {
   extern __shared__ __align__(128) unsigned char smem[];
   const int K = g.K;
@@ -1132,8 +1137,8 @@ constexpr int kReduceBatch = LLMOE_REDUCE_KBATCH;  // messages whose loads a war
 // then load that token's expert id and weight (one memory round trip), and
 // every unit of the token reuses them from registers.
 template <int DT>
-__global__ void __launch_bounds__(kThreads, 4) combine_reduce_kernel(Geometry g, const int64_t* __restrict__ idx,
-                                                                     const float* __restrict__ topk_w,
+__global__ void __launch_bounds__(kThreads, 4) combine_reduce_kernel(Geometry g, const int64_t* idx,
+                                                                     const float* topk_w,
                                                                      void* __restrict__ out) {
   release_next_grid();
   wait_prior_grid();
@@ -1637,7 +1642,7 @@ __global__ void __launch_bounds__(kThreads, 3) dispatch_signaled_kernel(Geometry
   }
 }
 
-__global__ void __launch_bounds__(kThreads) route_kernel(Geometry g, const int64_t* __restrict__ idx,
+__global__ void __launch_bounds__(kThreads) route_kernel(Geometry g, const int64_t* idx,
                                                          int32_t* __restrict__ slot_out,
                                                          int64_t* __restrict__ counts) {
   extern __shared__ __align__(128) unsigned char smem[];

@@ -122,6 +122,8 @@ LLMOE_API int llmoe_topk_router(const void* logits, const float* bias, const uin
  *           FP32, and MX8 with LLMOE_PRODUCT_SWIGLU.
  *   bs      geometry: num_max_tokens, num_ranks, num_experts, and err; with
  *           counts NULL also base, rank_stride, hidden, dtype and set.
+ * Every wait inside the kernel is bounded (about a second); one that expires
+ * leaves its rows unwritten and validate mode reports LLMOE_DEV_TIMEOUT.
  * x, w, y 16-byte aligned; llmoe_row_bytes(in_features, dtype) and
  * llmoe_row_bytes(out_features, out_dtype) not 0; out_features a multiple of
  * 8 with LLMOE_PRODUCT_SWIGLU; E * R * T < 2^31. */

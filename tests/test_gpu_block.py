@@ -664,3 +664,85 @@ def test_moe_block_refuses_too_many_tokens(L):
     m = MoEBlock(4, 2, 1, z(64), z(2, 64), z(2, 64, 64), z(2, 64, 32))
     with pytest.raises(ValueError):
         m.forward(z(2, 5, 64), z(2, 5, 64), z(2, 5, 64))
+
+
+@pytest.mark.parametrize("call", ["route", "dispatch", "dispatch_unpack", "combine", "combine_staged"])
+def test_router_queued_before(L, call):
+    """A call queued right behind the router that writes its topk_idx and
+    topk_w, all launched while the device is still busy, reads what the router
+    wrote: the same bytes as with a synchronize between the two."""
+    R, T, H, E, K = 4, 48, 512, 32, 4
+    logits = torch.randn(R * T, E, generator=rnd(77)).cuda()
+    x = torch.randn(R, T, H, generator=rnd(78)).to(torch.bfloat16).cuda()
+    y = torch.randn(E, R, T, H, generator=rnd(79)).to(torch.bfloat16).cuda()
+    idx = torch.empty(R, T, K, dtype=torch.int64, device="cuda")
+    w = torch.empty(R, T, K, dtype=torch.float32, device="cuda")
+
+    def run(between):
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        rb = L.RankBuffers(T, H, R, E, fill=0)
+        s = 1 if call.startswith("combine") else 0
+        bs = rb.buf_set(s, K, err=err)
+        recv_x = torch.zeros(E, R, T, H, dtype=torch.bfloat16, device="cuda")
+        recv_src = torch.zeros(E, R, T, dtype=torch.int32, device="cuda")
+        out = torch.zeros(R, T, H, dtype=torch.bfloat16, device="cuda")
+        slot = torch.zeros(R, T, K, dtype=torch.int32, device="cuda")
+        counts = torch.zeros(E, R, dtype=torch.int64, device="cuda")
+        idx.fill_(-1)
+        w.fill_(0)
+        torch.cuda.synchronize()
+        torch.cuda._sleep(4_000_000)
+        L.llmoe_topk_router(logits, None, None, idx, w, R * T, E, K, L.LLMOE_DTYPE_FP32, L.LLMOE_SCORE_SOFTMAX, 0, 1.0)
+        between()
+        if call == "route":
+            L.llmoe_route(idx, slot, counts, bs)
+        elif call == "dispatch":
+            L.llmoe_dispatch(x, idx, bs)
+        elif call == "dispatch_unpack":
+            L.llmoe_dispatch_unpack(x, idx, recv_x, recv_src, bs)
+        elif call == "combine":
+            L.llmoe_combine(y, idx, w, out, bs)
+        else:
+            L.llmoe_combine_staged(y, idx, w, out, bs)
+        torch.cuda.synchronize()
+        assert int(err) == 0
+        return rb.storage, recv_x, recv_src, out, slot, counts
+
+    want = run(torch.cuda.synchronize)
+    for _ in range(3):
+        for got, ref_ in zip(run(lambda: None), want):
+            assert torch.equal(got, ref_)
+
+
+@pytest.mark.parametrize("rows", ["same", "mx8"])
+def test_moe_block_queued(L, rows):
+    """A block's calls all queued while the device is still busy, over buffers
+    that held something else: the bits of a call on an idle device."""
+    from combine_routing_count_prefix_gb300.moe_block import MoEBlock
+
+    R, T, n, H, I, E, K = 4, 64, 37, 1536, 768, 32, 4
+    g = rnd(91)
+    new = lambda *s: (torch.randn(*s, generator=g) * s[-1] ** -0.5).to(torch.bfloat16).cuda()
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    m = MoEBlock(T, R, K, torch.ones(H, dtype=torch.bfloat16, device="cuda"), new(E, H), new(E, 2 * I, H), new(E, H, I),
+                 None, "bf16", rows, err=err)
+    x, res0 = H ** 0.5 * new(R, n, H), new(R, n, H)
+    out, outs = torch.empty_like(x), []
+    res = res0.clone()
+    for busy in (False, True, True):
+        res.copy_(res0)
+        out.zero_()
+        m.topk_idx.fill_(-1)
+        m.topk_w.zero_()
+        m.logits.zero_()
+        m.recv_x.zero_()
+        m.recv_src.zero_()
+        torch.cuda.synchronize()
+        if busy:
+            torch.cuda._sleep(8_000_000)
+        m.forward(x, res, out)
+        torch.cuda.synchronize()
+        assert int(err) == 0
+        outs.append(out.clone())
+    assert torch.isfinite(outs[0]).all() and (outs[0] != 0).any()
+    assert torch.equal(outs[1], outs[0]) and torch.equal(outs[2], outs[0])
