@@ -79,6 +79,14 @@ inline uint64_t row_bytes(int64_t n, int dtype) {
 // ---------------------------------------------------------------------------
 // device side
 // ---------------------------------------------------------------------------
+// A kernel here lets the next one on the stream start (release_next_grid) only
+// after its own wait: whatever starts behind it then finds everything before
+// it complete, among it a router's topk_idx and topk_w for a combine that
+// reads them before its wait (LLMOE_FLAG_INPUTS_READY).  Releasing before the
+// wait measured the same on every call (one-token norm 5.8 us, router 6.3,
+// smallest product 7.3), large norm 64.4 against 64.2 us.  And no pointer that
+// a kernel loads through is __restrict__: the compiler would be free to load
+// through it before the wait.
 __device__ __forceinline__ void wait_prior_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void release_next_grid() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

@@ -535,7 +535,6 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
                  acc_empty = acc_full + 16, plan_full = acc_empty + 16, plan_empty = plan_full + 8 * kPlanDepth,
                  halves = plan_empty + 8 * kPlanDepth, scale_full = halves + 32, scale_empty = scale_full + 32;
 
-  release_next_grid();
   if (threadIdx.x == 0) {
     tma_prefetch_map(&maps.w);
     for (int s = 0; s < a.stages; ++s) {
@@ -559,6 +558,7 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
   }
   if (warp == 3) tmem_alloc_pair(sbase + l.tmem, 512);
   wait_prior_grid();
+  release_next_grid();
   count_shares<kMx>(a, prefix, reinterpret_cast<int*>(smem + l.part));
   tc_fence_before();
   __syncthreads();

@@ -112,8 +112,8 @@ template <int W, int V, bool kVec>
 __global__ void __launch_bounds__(256, W > 1 || V > 8 ? 2 : 5) router_kernel(RouterArgs a) {
   __shared__ uint32_t part[W];
   __shared__ uint2 gathered[W == 1 ? 8 : 1][32];
-  release_next_grid();
   wait_prior_grid();
+  release_next_grid();
   const Group<W> group{part};
   const int lane = W == 1 ? threadIdx.x & 31 : threadIdx.x;
   const int64_t first = W == 1 ? ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5 : blockIdx.x;

@@ -109,8 +109,8 @@ __global__ void __launch_bounds__(1024) rows_kernel(RowsArgs a) {
   constexpr int V = Quad<DT>::kValues, P = V / 2;
   constexpr int kLanes = 32 / V;  // adjacent lanes that hold one group of 32
   __shared__ float part[32];
-  release_next_grid();
   wait_prior_grid();
+  release_next_grid();
   const int tid = threadIdx.x, nthr = blockDim.x;
   uint4 x[Q], res[Q];  // the next row to be normed
   const auto load = [&](int64_t row) {

@@ -89,6 +89,10 @@ LLMOE_API int llmoe_add_rmsnorm(const void* x, const void* residual, const void*
  * An expert whose logit or key is NaN or -infinity cannot be chosen and has
  * score 0; where fewer than num_topk can, the remaining entries are -1 with
  * weight 0.  Softmax: logits of +infinity share the whole weight.
+ * LLMOE_FLAG_INPUTS_READY on the dispatch or combine that takes them needs
+ * another call of this header between the router and that call (the experts'
+ * products, for a combine): what starts behind such a call finds all before
+ * it complete, where the calls of llmoe.h may start while it is at work.
  * 1 <= num_topk <= min(num_experts, LLMOE_MAX_TOPK), num_experts <=
  * LLMOE_MAX_EXPERTS.  rows may be 0. */
 LLMOE_API int llmoe_topk_router(const void* logits, const float* bias, const uint8_t* active, int64_t* topk_idx,

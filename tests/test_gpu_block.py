@@ -746,3 +746,47 @@ def test_moe_block_queued(L, rows):
         outs.append(out.clone())
     assert torch.isfinite(outs[0]).all() and (outs[0] != 0).any()
     assert torch.equal(outs[1], outs[0]) and torch.equal(outs[2], outs[0])
+
+
+@pytest.mark.parametrize("between", ["pack", "norm", "product"])
+def test_router_before_an_early_combine(L, between):
+    """LLMOE_FLAG_INPUTS_READY on a combine with one other call between the
+    router and it, all queued while the device is busy: the combine may read
+    topk_idx and topk_w before its wait, and they are there."""
+    R, T, H, E, K = 1, 1, 512, 8192, 8
+    logits = torch.randn(1, E, generator=rnd(81)).cuda()
+    y = torch.randn(E, R, T, H, generator=rnd(82)).to(torch.bfloat16).cuda()
+    z = torch.randn(32, 64, generator=rnd(83)).to(torch.bfloat16).cuda()
+    w1, counts = torch.ones(64, dtype=torch.bfloat16, device="cuda"), torch.ones(1, dtype=torch.int64, device="cuda")
+    packed = torch.empty(32, 80, dtype=torch.uint8, device="cuda")
+    zz, prod = torch.empty_like(z), torch.empty(1, 32, dtype=torch.bfloat16, device="cuda")
+    idx = torch.empty(R, T, K, dtype=torch.int64, device="cuda")
+    w = torch.empty(R, T, K, dtype=torch.float32, device="cuda")
+    out = torch.empty(R, T, H, dtype=torch.bfloat16, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    rb = L.RankBuffers(T, H, R, E, fill=0)
+    one = L.geometry(1, 1, 1, err)
+    outs = []
+    for sync in (True, False, False, False):
+        idx.fill_(-1)
+        w.zero_()
+        out.zero_()
+        rb.storage.zero_()
+        torch.cuda.synchronize()
+        torch.cuda._sleep(4_000_000)
+        L.llmoe_topk_router(logits, None, None, idx, w, 1, E, K, L.LLMOE_DTYPE_FP32, L.LLMOE_SCORE_SOFTMAX, 0, 1.0)
+        if between == "pack":
+            L.llmoe_pack_mx8(z, packed, 32, 64, L.LLMOE_DTYPE_BF16)
+        elif between == "norm":
+            L.llmoe_add_rmsnorm(z, None, w1, 1e-6, None, zz, 32, 64, L.LLMOE_DTYPE_BF16, L.LLMOE_DTYPE_BF16)
+        else:
+            L.llmoe_expert_product(z[:1], z, prod, counts, 64, 32, L.LLMOE_DTYPE_BF16, L.LLMOE_DTYPE_BF16, 0, one)
+        if sync:
+            torch.cuda.synchronize()
+        L.llmoe_combine(y, idx, w, out, rb.buf_set(1, K, err=err, flags=L.LLMOE_FLAG_INPUTS_READY))
+        torch.cuda.synchronize()
+        assert int(err) == 0
+        outs.append(out.clone())
+    assert (outs[0] != 0).any()
+    for o in outs[1:]:
+        assert torch.equal(o, outs[0])
