@@ -84,9 +84,10 @@ inline uint64_t row_bytes(int64_t n, int dtype) {
 // it complete, among it a router's topk_idx and topk_w for a combine that
 // reads them before its wait (LLMOE_FLAG_INPUTS_READY).  Releasing before the
 // wait measured the same on every call (one-token norm 5.8 us, router 6.3,
-// smallest product 7.3), large norm 64.4 against 64.2 us.  And no pointer that
-// a kernel loads through is __restrict__: the compiler would be free to load
-// through it before the wait.
+// smallest product 7.3), large norm 64.4 against 64.2 us.  And no load is
+// through a __restrict__ pointer or __ldg: the compiler would be free to move
+// it before the wait, and a read-only load must not meet memory that is still
+// written while the kernel starts.  Plain loads measured the same.
 __device__ __forceinline__ void wait_prior_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void release_next_grid() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

@@ -779,7 +779,7 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
 #pragma unroll
         for (int j = 0; j < 3; ++j) {
           ahead[u][j] = make_uint4(0, 0, 0, 0);
-          if (have[j] && u < chunks) ahead[u][j] = __ldg(src[j] + u);
+          if (have[j] && u < chunks) ahead[u][j] = src[j][u];
         }
       for (int c0 = 0; c0 < chunks && ok; c0 += kAhead) {
 #pragma unroll
@@ -808,7 +808,7 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
           if (++sslot == S::kSlots) sslot = 0, sphase ^= 1;
 #pragma unroll
           for (int j = 0; j < 3; ++j)
-            if (have[j] && c + kAhead < chunks) ahead[u][j] = __ldg(src[j] + c + kAhead);
+            if (have[j] && c + kAhead < chunks) ahead[u][j] = src[j][c + kAhead];
         }
       }
     }

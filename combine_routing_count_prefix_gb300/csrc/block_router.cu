@@ -102,7 +102,7 @@ __device__ __forceinline__ float unorder(uint32_t b) {
 }
 __device__ __forceinline__ uint32_t exact_key(const RouterArgs& a, int e, float l) {
   float k = a.softmax ? l : sigmoid_score(l);
-  if (a.bias != nullptr) k += __ldg(a.bias + e);
+  if (a.bias != nullptr) k += a.bias[e];
   return order(l, k);
 }
 
@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(256, W > 1 || V > 8 ? 2 : 5) router_kernel(Rou
       for (int i = 0; i < V; ++i) {
         near[i] = a.softmax ? l[i] : __fdividef(1.0f, 1.0f + __expf(-l[i]));
         const int e = expert_of<W, kVec>(lane, i);
-        if (a.bias != nullptr && e < a.E) near[i] += __ldg(a.bias + e);
+        if (a.bias != nullptr && e < a.E) near[i] += a.bias[e];
         if (!(l[i] > -INFINITY)) near[i] = -INFINITY;
         left = fmaxf(left, near[i]);
       }

@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(1024) rows_kernel(RowsArgs a) {
       quad_pairs<DT>(h[i], v);
       if constexpr (kNorm) {
         Pair w[P];
-        quad_pairs<DT>(j < a.nq ? __ldg(a.weight + j) : make_uint4(0, 0, 0, 0), w);
+        quad_pairs<DT>(j < a.nq ? a.weight[j] : make_uint4(0, 0, 0, 0), w);
 #pragma unroll
         for (int k = 0; k < P; ++k) v[k] = mul2(mul2(v[k], r2), w[k]);
       }

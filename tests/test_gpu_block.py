@@ -790,3 +790,31 @@ def test_router_before_an_early_combine(L, between):
     assert (outs[0] != 0).any()
     for o in outs[1:]:
         assert torch.equal(o, outs[0])
+
+
+@pytest.mark.parametrize("rows", ["same", "mx8"])
+def test_moe_block_changing_inputs(L, rows):
+    """Two inputs in turn through one block's buffers, all queued: each has the
+    bits of a call on an idle device, so no step reads what the other left."""
+    from combine_routing_count_prefix_gb300.moe_block import MoEBlock
+
+    R, T, H, I, E, K = 2, 32, 512, 128, 8, 2
+    g = rnd(95)
+    new = lambda *s: (torch.randn(*s, generator=g) * s[-1] ** -0.5).to(torch.bfloat16).cuda()
+    m = MoEBlock(T, R, K, torch.ones(H, dtype=torch.bfloat16, device="cuda"), new(E, H), new(E, 2 * I, H), new(E, H, I),
+                 None, "bf16", rows)
+    xs = [new(R, T, H), 8 * new(R, T, H)]
+    res, outs = [torch.zeros_like(x) for x in xs], [torch.empty_like(x) for x in xs]
+    want = []
+    for x, r, o in zip(xs, res, outs):
+        m.forward(x, r, o)
+        torch.cuda.synchronize()
+        want.append(o.clone())
+    assert not torch.equal(want[0], want[1])
+    for _ in range(5):
+        torch.cuda._sleep(4_000_000)
+        for _ in range(8):
+            for x, r, o in zip(xs, res, outs):
+                r.zero_()
+                m.forward(x, r, o)
+        assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
