@@ -73,7 +73,7 @@ LLMOE_API int llmoe_add_rmsnorm(const void* x, const void* residual, const void*
 
 /* llmoe_topk_router scoring */
 #define LLMOE_SCORE_SIGMOID 0 /* score = 1 / (1 + exp(-l)), key = score + bias */
-#define LLMOE_SCORE_SOFTMAX 1 /* score = softmax(l) over the row's experts, key = l + bias */
+#define LLMOE_SCORE_SOFTMAX 1 /* score = softmax(l) over the row's experts that can be chosen, key = l + bias */
 /* llmoe_topk_router flags */
 #define LLMOE_ROUTER_RENORM 1u /* divide the chosen scores by their sum */
 
@@ -88,7 +88,8 @@ LLMOE_API int llmoe_add_rmsnorm(const void* x, const void* residual, const void*
  *   topk_w    device fp32 [rows][num_topk] out, as llmoe_combine takes it.
  * An expert whose logit or key is NaN or -infinity cannot be chosen and has
  * score 0; where fewer than num_topk can, the remaining entries are -1 with
- * weight 0.  Softmax: logits of +infinity share the whole weight.
+ * weight 0.  Softmax: such experts are not in its sum; logits of +infinity share
+ * the whole weight.
  * LLMOE_FLAG_INPUTS_READY on the dispatch or combine that takes them needs
  * another call of this header between the router and that call (the experts'
  * products, for a combine): what starts behind such a call finds all before
