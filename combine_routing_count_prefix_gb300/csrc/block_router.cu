@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(256, W > 1 || V > 8 ? 2 : 5) router_kernel(Rou
       }
     }
     float top = -INFINITY, total = 0.0f;
-    if constexpr (kSoftmax) {
+    if (kSoftmax && !a.renorm) {
 #pragma unroll
       for (int i = 0; i < V; ++i) top = fmaxf(top, l[i]);
       top = group.max_f(top);
@@ -241,21 +241,26 @@ __global__ void __launch_bounds__(256, W > 1 || V > 8 ? 2 : 5) router_kernel(Rou
       }
     }
     if (W > 1 && lane >= 32) continue;
-    float score = 0.0f;
-    if (mine >= 0) {
-      const float v = load_logit(a, row * a.E + mine);
-      score = kSoftmax ? softmax_score(v, top) / total : sigmoid_score(v);
+    const float v = mine >= 0 ? load_logit(a, row * a.E + mine) : -INFINITY;
+    if (kSoftmax && a.renorm) {
+      // what is renormalised is a softmax of the chosen alone: relative to the
+      // largest of them, which the row's largest may be above by more than an
+      // fp32 score can be small
+      top = v;
+#pragma unroll
+      for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
     }
-    float m = a.scale;
+    float score = 0.0f;
+    if (mine >= 0) score = !kSoftmax ? sigmoid_score(v) : a.renorm ? softmax_score(v, top) : softmax_score(v, top) / total;
     if (a.renorm) {
       float sum = score;
 #pragma unroll
       for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-      m = sum > 0.0f ? a.scale / sum : 0.0f;
+      score = sum > 0.0f ? score / sum : 0.0f;  // before the scale: scale / sum may be above fp32's largest
     }
     if (lane < a.K) {
       a.topk_idx[row * a.K + lane] = mine;
-      a.topk_w[row * a.K + lane] = score * m;
+      a.topk_w[row * a.K + lane] = score * a.scale;
     }
   }
 }

@@ -79,8 +79,10 @@ LLMOE_API int llmoe_add_rmsnorm(const void* x, const void* residual, const void*
 
 /* Router: each row's num_topk experts of largest key, in descending order of
  * key, equal keys by ascending expert; their weights are scale * score (with
- * LLMOE_ROUTER_RENORM, scale * score / the sum of the row's chosen scores; 0
- * where that sum is 0).  Scores, keys and sums are fp32.
+ * LLMOE_ROUTER_RENORM, scale * (score / the sum of the row's chosen scores); 0
+ * where that sum is 0).  Scores, keys and sums are fp32: a sigmoid below 2^-128
+ * is 0.  A renormalised softmax is taken over the chosen alone, which is the
+ * same, so that an unchosen expert far above them does not make their scores 0.
  *   logits    device T [rows][num_experts]; T per dtype (BF16, FP16, FP32).
  *   bias      device fp32 [num_experts], or NULL.
  *   active    device uint8 [rows], or NULL: rows with 0 choose nothing.

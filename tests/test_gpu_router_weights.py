@@ -113,3 +113,30 @@ def test_softmax_rows_without_a_choice(L, E):
     for renorm in (False, True):
         gi, gw = run(L, logits, bias, 2, L.LLMOE_SCORE_SOFTMAX, renorm, 1.0)
         assert (gi == -1).all() and (gw == 0).all()
+
+
+@pytest.mark.parametrize("lead", [60.0, 95.0, 120.0, 1e4])
+@pytest.mark.parametrize("E", EXPERTS)
+def test_renormalised_softmax_below_a_leading_expert(L, E, lead):
+    """An expert whose logit leads by far but whose finite bias keeps it from
+    being chosen: the chosen scores are too small for fp32, their shares are not."""
+    logits = eighths(4, E, 3 * E)
+    bias = torch.zeros(E)
+    bias[2] = -1e6
+    logits[:, 2] = lead
+    check(L, logits, bias, 3, True)
+    check(L, logits, None, 3, True)  # and chosen
+
+
+@pytest.mark.parametrize("K", [1, 2, 4])
+@pytest.mark.parametrize("E", EXPERTS)
+def test_renormalised_sigmoid_of_least_scores(L, E, K):
+    """Equal scores of about 5e-39 (subnormal): every weight is scale / K
+    exactly, where scale / sum is above fp32's largest value."""
+    logits = torch.full((5, E), -88.0)
+    gi, gw = run(L, logits, None, K, L.LLMOE_SCORE_SIGMOID, True, 2.5)
+    assert (gi == np.arange(K)).all()
+    assert (gw == 2.5 / K).all()
+    # a sum of zero gives zeros
+    gi, gw = run(L, torch.full((5, E), -200.0), None, K, L.LLMOE_SCORE_SIGMOID, True, 2.5)
+    assert (gi == np.arange(K)).all() and (gw == 0).all()
