@@ -302,6 +302,14 @@ extern "C" int llmoe_topk_router(const void* logits, const float* bias, const ui
   if (logits == nullptr || topk_idx == nullptr || topk_w == nullptr || !aligned(logits, es) || !aligned(bias, 4) ||
       !aligned(topk_idx, 8) || !aligned(topk_w, 4))
     return LLMOE_ERR_INVALID_ARGUMENT;
+  // rows are read and written by many CTAs in no order: no output may be an input
+  const uint64_t n = (uint64_t)rows, idx_bytes = n * num_topk * 8, w_bytes = n * num_topk * 4;
+  const auto meets = [&](const void* in, uint64_t bytes) {
+    return in != nullptr && (overlap(topk_idx, idx_bytes, in, bytes) || overlap(topk_w, w_bytes, in, bytes));
+  };
+  if (meets(logits, n * num_experts * es) || meets(bias, (uint64_t)num_experts * 4) || meets(active, n) ||
+      overlap(topk_idx, idx_bytes, topk_w, w_bytes))
+    return LLMOE_ERR_INVALID_ARGUMENT;
   const RouterArgs a{logits,      bias,     active, topk_idx, topk_w, rows, num_experts, num_topk,
                      dtype, (flags & LLMOE_ROUTER_RENORM) != 0, scale};
   const bool vec = dtype == LLMOE_DTYPE_FP32 && num_experts % 4 == 0 && aligned(logits, 16);

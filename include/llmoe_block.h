@@ -96,6 +96,7 @@ LLMOE_API int llmoe_add_rmsnorm(const void* x, const void* residual, const void*
  * another call of this header between the router and that call (the experts'
  * products, for a combine): what starts behind such a call finds all before
  * it complete, where the calls of llmoe.h may start while it is at work.
+ * topk_idx and topk_w must overlap neither each other nor an input.
  * 1 <= num_topk <= min(num_experts, LLMOE_MAX_TOPK), num_experts <=
  * LLMOE_MAX_EXPERTS.  rows may be 0. */
 LLMOE_API int llmoe_topk_router(const void* logits, const float* bias, const uint8_t* active, int64_t* topk_idx,

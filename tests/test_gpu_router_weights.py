@@ -140,3 +140,19 @@ def test_renormalised_sigmoid_of_least_scores(L, E, K):
     # a sum of zero gives zeros
     gi, gw = run(L, torch.full((5, E), -200.0), None, K, L.LLMOE_SCORE_SIGMOID, True, 2.5)
     assert (gi == np.arange(K)).all() and (gw == 0).all()
+
+
+def test_inputs_and_outputs_side_by_side(L):
+    """One allocation holds logits, bias, active, topk_idx and topk_w, each right
+    behind the one before: no overlap, so no refusal."""
+    rows, E, K = 8, 40, 3
+    sizes = [rows * E * 4, E * 4, rows, rows * K * 8, rows * K * 4]
+    flat = torch.zeros(sum(sizes), dtype=torch.uint8, device="cuda")
+    logits, bias, active, idx, w = flat.split(sizes)
+    want = eighths(rows, E, 5)
+    logits.view(torch.float32).copy_(want.reshape(-1).cuda())
+    active.fill_(1)
+    L.llmoe_topk_router(logits.view(torch.float32), bias.view(torch.float32), active, idx.view(torch.int64),
+                        w.view(torch.float32), rows, E, K, L.LLMOE_DTYPE_FP32, L.LLMOE_SCORE_SOFTMAX, 0, 1.0)
+    ri, _ = softmax_router(want.numpy(), None, K, False, 1.0)
+    assert np.array_equal(idx.view(torch.int64).cpu().numpy().reshape(rows, K), ri)
