@@ -926,23 +926,25 @@ bool make_map(CUtensorMap* m, const void* base, int dtype, const cuuint64_t* dim
 constexpr size_t kMaxSmem = 232448;  // 227 KB
 
 // Opts the kernel in to its shared memory and asks how many pairs can be
-// resident, once per device and shared-memory size.
+// resident, once per device.  Asked with the most shared memory: whatever a call
+// uses is more than half of an SM's, so there is one CTA on an SM in any case.
 template <bool kMx, bool kSwiglu>
-int resident_pairs(size_t smem) {
+int resident_pairs() {
+  static_assert((Shape<kMx>::kStages - 1) * Shape<kMx>::kStage > kMaxSmem / 2, "one CTA per SM");
   constexpr int kMaxDevices = 64;
-  static std::atomic<uint64_t> cache[kMaxDevices];  // bytes << 32 | pairs
+  static std::atomic<int> cache[kMaxDevices];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 0;
   if (dev < kMaxDevices) {
-    const uint64_t c = cache[dev].load(std::memory_order_relaxed);
-    if (c >> 32 == smem) return (int)(uint32_t)c;
+    const int c = cache[dev].load(std::memory_order_relaxed);
+    if (c > 0) return c;
   }
   const auto kernel = product_kernel<kMx, kSwiglu>;
   int n = 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * num_sms());
   cfg.blockDim = dim3(Shape<kMx>::kThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = kMaxSmem;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
@@ -955,7 +957,7 @@ int resident_pairs(size_t smem) {
     cudaGetLastError();
     return 0;
   }
-  if (dev < kMaxDevices) cache[dev].store((uint64_t)smem << 32 | (uint32_t)n, std::memory_order_relaxed);
+  if (dev < kMaxDevices) cache[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 
@@ -995,7 +997,7 @@ int launch_product(ProductArgs& a, llmoe_stream_t stream) {
     const cuuint32_t box[3] = {k_box, 128, 1};
     if (!make_map(&maps.w, a.w, a.dtype, dims, strides, box, 3)) return LLMOE_ERR_CUDA;
   }
-  const int pairs = resident_pairs<kMx, kSwiglu>(smem);
+  const int pairs = resident_pairs<kMx, kSwiglu>();
   if (pairs < 1) return LLMOE_ERR_CUDA;
 
   cudaLaunchConfig_t cfg = {};
