@@ -138,7 +138,11 @@ __device__ __forceinline__ void trace_phase(int base, int p) {
 // the wait cannot change memory that only such an argument names, and it moves
 // loads from it to before the wait, where a router's topk_idx, written by the
 // kernel before, may not be there yet.  (A kernel that only stores through
-// one keeps it: what it stores comes from loads behind the wait.)
+// one keeps it: what it stores comes from loads behind the wait.)  Nor does it
+// load through the read-only path (__ldg, ld.global.nc): that wants memory that
+// nothing writes while the kernel runs, and the kernel before may still be
+// writing y, x or messages when this one starts.  dispatch_signaled_kernel, a
+// cooperative launch that starts after all before it, is the exception to both.
 __device__ __forceinline__ void wait_prior_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void release_next_grid() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
@@ -299,14 +303,16 @@ __device__ __forceinline__ uint4 shift_words(const uint4& prev, const uint4& cur
   }
 }
 
-// 16-byte read-only load that does not allocate in L1: for rows read exactly
-// once (expert outputs in the combine and the staged put), where L1 lines
-// would only add allocation work to every miss.
+// 16-byte load that does not allocate in L1: for rows read exactly once (expert
+// outputs in the combine and the staged put), where L1 lines would only add
+// allocation work to every miss.  Volatile, so that it stays behind the wait;
+// as a read-only load that the compiler may move it measured the same (round
+// 48.3 us on DS-V3, staged combine 71.8).
 __device__ __forceinline__ uint4 ld_stream16(const uint4* p) {
   uint4 r;
-  asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-      : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-      : "l"(p));
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p));
   return r;
 }
 
@@ -950,13 +956,13 @@ __global__ void __launch_bounds__(kThreads, 4) combine_put_kernel(Geometry g, co
 // whole warp, so the branch does not diverge.
 __device__ __forceinline__ uint4 ld_payload_quad(const uint8_t* pay, int phase, int j) {
   const uint8_t* p = pay + 16 * (size_t)j;
-  if (phase == 0) return __ldg(reinterpret_cast<const uint4*>(p));
+  if (phase == 0) return *reinterpret_cast<const uint4*>(p);
   if (phase == 2) {
-    const uint2 lo = __ldg(reinterpret_cast<const uint2*>(p)), hi = __ldg(reinterpret_cast<const uint2*>(p + 8));
+    const uint2 lo = *reinterpret_cast<const uint2*>(p), hi = *reinterpret_cast<const uint2*>(p + 8);
     return make_uint4(lo.x, lo.y, hi.x, hi.y);
   }
   const uint32_t* w = reinterpret_cast<const uint32_t*>(p);
-  return make_uint4(__ldg(w), __ldg(w + 1), __ldg(w + 2), __ldg(w + 3));
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // Reduce through a shared-memory ring (combine_reduce_ring_kernel), for grids
