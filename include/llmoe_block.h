@@ -113,6 +113,8 @@ LLMOE_API int llmoe_topk_router(const void* logits, const float* bias, const uin
  *   y[r][:] = x[r][:] w[e]^T       summed in fp32, rounded once to out_dtype;
  * with LLMOE_PRODUCT_SWIGLU w[e] is [gate; up], 2 * out_features rows, and
  *   y[r][:] = silu(x[r] gate^T) * (x[r] up^T),  silu(a) = a / (1 + exp(-a)), in fp32.
+ * (Where y is of 16 or 8 bits, exp and the quotient are the hardware's: within
+ * 4 + |a| / 2 units of the last fp32 place, which y's rounding covers.)
  * Other rows of y are not written.  Unreceived rows of x, whatever they hold,
  * do not touch the result.
  *   x       device rows of dtype [E * R * T], in_features values each.
