@@ -209,7 +209,7 @@ template <int DT, bool MX, bool kNorm>
 int launch_rows(const RowsArgs& a, llmoe_stream_t stream) {
   // two quads per thread where a CTA has threads enough; as many CTAs as the
   // registers (64 a thread) hold
-  const int threads = std::min(1024, std::max(128, (a.nq / 2 + 31) / 32 * 32));
+  const int threads = std::min(1024, std::max(128, ((a.nq + 1) / 2 + 31) / 32 * 32));
   const unsigned grid = (unsigned)std::min<int64_t>(a.rows, (int64_t)num_sms() * (1024 / threads));
   const int q = (a.nq + threads - 1) / threads;
   if (q <= 1) return launch_block(rows_kernel<DT, MX, 1, kNorm>, grid, threads, 0, stream, a);
