@@ -214,8 +214,10 @@ int launch_rows(const RowsArgs& a, llmoe_stream_t stream) {
   const int q = (a.nq + threads - 1) / threads;
   if (q <= 1) return launch_block(rows_kernel<DT, MX, 1, kNorm>, grid, threads, 0, stream, a);
   if (q <= 2) return launch_block(rows_kernel<DT, MX, 2, kNorm>, grid, threads, 0, stream, a);
-  if (q <= 4) return launch_block(rows_kernel<DT, MX, 4, kNorm>, grid, threads, 0, stream, a);
-  return launch_block(rows_kernel<DT, MX, 8, kNorm>, grid, threads, 0, stream, a);
+  if constexpr (DT == LLMOE_DTYPE_FP32)  // 16-bit rows have at most four quads for each of 1024 threads
+    if (q > 4) return launch_block(rows_kernel<DT, MX, 8, kNorm>, grid, threads, 0, stream, a);
+  static_assert(LLMOE_MAX_ROW_VALUES <= 4 * 1024 * 8, "16-bit rows past four quads a thread");
+  return launch_block(rows_kernel<DT, MX, 4, kNorm>, grid, threads, 0, stream, a);
 }
 
 template <bool MX, bool kNorm>
