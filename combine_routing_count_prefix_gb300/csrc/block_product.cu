@@ -54,7 +54,7 @@
 namespace {
 
 constexpr int kPlanDepth = 4;       // planned tiles in flight
-constexpr int kMaxStages = 8;
+constexpr int kStages = 6;          // of the ring at most; fewer where thousands of experts take their room
 constexpr int kTileFeatures = 256;  // rows of w per tile: 128 in each CTA
 constexpr int kGroup = 4;           // rows of x taken together
 constexpr int kBoxes = 6;           // x loads of 1, 2, .. 32 groups
@@ -68,7 +68,6 @@ struct Shape {
   static constexpr int kMaxRows = kMx ? 224 : 256;
   static constexpr int kBytesA = 128 * 128, kBytesB = kMaxRows / 2 * 128;
   static constexpr int kStage = kBytesA + kBytesB;
-  static constexpr int kStages = 6;
   // 8-bit operands: scales in slots of four steps; a step's are 512 bytes for
   // the CTA's 128 rows of w and 1024 for up to 256 rows of x, and 12 columns
   // of tensor memory, reused after kScaleRing steps
@@ -152,7 +151,7 @@ __host__ __device__ inline SmemLayout smem_layout(int stages, int E) {
   l.rows = at, at += kPlanDepth * S::kMaxRows * 4;
   l.tiles = at, at += kPlanDepth * (uint32_t)sizeof(Tile);
   l.amax = at, at += 2 * 8 * 32 * 4;
-  l.bars = at, at += (2 * kMaxStages + 4 + 2 * kPlanDepth + 4 + 2 * 4) * 8;
+  l.bars = at, at += (2 * kStages + 4 + 2 * kPlanDepth + 4 + 2 * 4) * 8;
   l.tmem = at, at += 16;
   l.part = at, at += 64;
   l.prefix = at, at += (E + 1) * 4;
@@ -538,7 +537,7 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
   Box* boxes = reinterpret_cast<Box*>(smem + l.boxes);
   Tile* tiles = reinterpret_cast<Tile*>(smem + l.tiles);
   int* prefix = reinterpret_cast<int*>(smem + l.prefix);
-  const uint32_t full = sbase + l.bars, empty = full + 8 * kMaxStages, acc_full = empty + 8 * kMaxStages,
+  const uint32_t full = sbase + l.bars, empty = full + 8 * kStages, acc_full = empty + 8 * kStages,
                  acc_empty = acc_full + 16, plan_full = acc_empty + 16, plan_empty = plan_full + 8 * kPlanDepth,
                  halves = plan_empty + 8 * kPlanDepth, scale_full = halves + 32, scale_empty = scale_full + 32;
 
@@ -937,7 +936,7 @@ constexpr size_t kMaxSmem = 232448;  // 227 KB
 // uses is more than half of an SM's, so there is one CTA on an SM in any case.
 template <bool kMx, bool kSwiglu>
 int resident_pairs() {
-  static_assert((Shape<kMx>::kStages - 1) * Shape<kMx>::kStage > kMaxSmem / 2, "one CTA per SM");
+  static_assert((kStages - 1) * Shape<kMx>::kStage > kMaxSmem / 2, "one CTA per SM");
   constexpr int kMaxDevices = 64;
   static std::atomic<int> cache[kMaxDevices];
   int dev = 0;
@@ -977,7 +976,7 @@ int launch_product(ProductArgs& a, llmoe_stream_t stream) {
   const uint64_t groups = (uint64_t)((a.T + kGroup - 1) / kGroup) * a.R, share = S::kMaxRows / kGroup;
   const uint64_t most = (groups + share - 1) / share * a.E * a.blocks;
   if (most > INT32_MAX) return LLMOE_ERR_INVALID_ARGUMENT;
-  a.stages = S::kStages;
+  a.stages = kStages;
   while (smem_layout<kMx>(a.stages, a.E).total > kMaxSmem) --a.stages;
   const size_t smem = smem_layout<kMx>(a.stages, a.E).total;
   // both operands 16-bit or both e4m3 (0), fp32 sums, M = 256; 8-bit: e8m0 scales
