@@ -32,14 +32,15 @@
 // What bounds it, and what was measured on a GB300 (6.69 TB/s copy rate, 1.90
 // PFLOP/s cuBLAS bf16 in a burst, 1.73 in a loop under the power cap):
 // - few rows per expert: the weights' bytes.  256 experts x ~32 rows, 7168 ->
-//   2 x 2048: 2.20-2.26 ms bf16 (6.7-6.9 TB/s), 1.14-1.19 ms MX8.  The ring
-//   is what covers HBM's latency: MX8 with seven stages, not six, took 2% less.
-// - many rows: the tensor cores, then power.  16 experts x ~1024 rows: 532-550
-//   us in a burst (1.75-1.81 PFLOP/s), 620-645 us steadily.  A row costs its
+//   2 x 2048: 2.19-2.26 ms bf16 (6.7-6.9 TB/s), 1.14-1.19 ms MX8.  The ring is
+//   what covers HBM's latency: MX8 tiles of 192 rows, which leave room for a
+//   seventh stage, took 2% less here and 5% more with many rows.
+// - many rows: the tensor cores, then power.  16 experts x ~1024 rows: 527-555
+//   us in a burst (1.73-1.82 PFLOP/s), 620-655 us steadily.  A row costs its
 //   columns padded to 4 per bucket and 32 per share.  MX8 (2048 -> 7168): 182-188
 //   us in a burst (2.6 PFLOP/s), 212-218 steadily; there the epilogue and the
 //   scale copies of a tile of 16 steps take what the tensor cores leave.
-// - one row: eight experts' weights, 77-79 us of 70; 6 us are launch, plan, the
+// - one row: eight experts' weights, 76-79 us of 70; 6 us are launch, plan, the
 //   first load's latency and the last tile's stores.
 // What the structure bought, in microseconds (dense bf16 / decode bf16 / decode
 // MX8): rows by four-row gathers and one load warp 2311 / 3433 / 3547; boxes of

@@ -12,8 +12,9 @@
 // (K = 8 of 256: about ten do), and for that keys from the hardware's
 // exponential and reciprocal are enough, with a margin for their error.  Those
 // few go one to a lane, which computes their fp32 keys as defined, and the
-// rounds run over them.  8192 tokens of 256 experts: 8.6 us with exact keys for
-// all, 7.7 with this.
+// rounds run over them.  8192 tokens of 256 experts, sigmoid: 8.6 us with exact
+// keys for all, 7.7 with this; 7.3 with a kernel for each scoring (a softmax 7.2
+// renormalised, 7.8 not), one token 3.0.  About 710 instructions a token.
 #include <float.h>
 
 #include "block_common.cuh"

@@ -5,13 +5,15 @@
 // residual, h = T(x + residual), the sum of squares over the CTA in fp32, then
 // v = h * r * weight from the registers and 16-byte (MX8: 8-byte) stores.
 // Every byte is read and written once, so HBM bandwidth bounds a large call
-// (8192 rows of 7168 bf16 with a residual to MX8: 62.9 us, 6.6 TB/s, 98% of the
-// copy rate), launch and load latency a small one (one row 2.3 us, 1024 rows
-// 10.9).  A few large CTAs per SM stay for all rows and load the next row into
-// the registers that the sum has just freed: 1024 rows 10.9 us against 12.6 with
+// (8192 rows of 7168 bf16 with a residual to MX8: 63.2 us, 6.5 TB/s, 98% of the
+// copy rate; to bf16 75.5 us, 93%), launch and load latency a small one (one row
+// 2.2 us, 1024 rows 11.0).  A few large CTAs per SM stay for all rows and load the
+// next row into the registers that the sum has just freed: 1024 rows 11.0 us against 12.6 with
 // the next row prefetched into L2, and 12.7 with a CTA per row.  Two quads a
-// thread rather than four: 152 rows 3.1 us against 4.3.  Sums are packed
-// additions of T and the fp32 arithmetic is on pairs.
+// thread rather than four: 152 rows 3.1 us against 4.3.  Rows of more than 2048
+// quads take four or, fp32, eight a thread, which spill under 64 registers: 32768
+// bf16 values 92% of the copy rate, 16384 fp32 95%, 32768 fp32 57% (to MX8 76, 89
+// and 29%).  Sums are packed additions of T and the fp32 arithmetic is on pairs.
 #include "block_common.cuh"
 
 namespace {

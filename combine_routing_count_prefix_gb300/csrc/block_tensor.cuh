@@ -1,5 +1,5 @@
 // block_tensor.cuh -- the sm_103a instructions block_product.cu is written in:
-// mbarriers across a CTA pair, TMA tile and gather loads, tcgen05 products with
+// mbarriers across a CTA pair, TMA tile loads, tcgen05 products with
 // tensor-memory accumulators.  Thin wrappers, one instruction each.
 #pragma once
 #include <cuda.h>
