@@ -15,9 +15,10 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
-SRCS = [os.path.join(CSRC, f) for f in ("llmoe.cu", "block_rows.cu", "block_router.cu", "block_product.cu")]
+SRCS = [os.path.join(CSRC, f) for f in ("llmoe.cu", "block_rows.cu", "block_weights.cu", "block_router.cu",
+                                          "block_group_router.cu", "block_product.cu", "block_scaled.cu")]
 HDRS = [os.path.join(ROOT, "include", "llmoe.h"), os.path.join(ROOT, "include", "llmoe_block.h"),
-        os.path.join(CSRC, "block_common.cuh"), os.path.join(CSRC, "block_tensor.cuh")]
+        *(os.path.join(CSRC, f) for f in ("block_common.cuh", "block_tensor.cuh", "block_plan.cuh", "block_router.cuh"))]
 OUT_DIR = os.path.join(PKG, "_build")
 SO = os.path.join(OUT_DIR, "libllmoe.so")
 # the phase-trace build (-DLLMOE_PHASE_TRACE=1): the same library with per-CTA

@@ -1,5 +1,5 @@
 // block_common.cuh -- what the translation units of llmoe_block.h share: host
-// checks and launch, 16-byte rows as fp32 values, MX8 encoding.
+// checks and launch, 16-byte rows as fp32 values, MX8 and FP8B encoding.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -72,6 +72,8 @@ inline uint64_t row_bytes(int64_t n, int dtype) {
     case LLMOE_DTYPE_FP16: return n % 8 == 0 ? (uint64_t)n * 2 : 0;
     case LLMOE_DTYPE_FP32: return n % 4 == 0 ? (uint64_t)n * 4 : 0;
     case LLMOE_DTYPE_MX8: return n % 32 == 0 ? (uint64_t)n + (uint64_t)(n / 32 + 15) / 16 * 16 : 0;
+    case LLMOE_DTYPE_FP8B:
+      return n % 16 == 0 ? (uint64_t)n + ((uint64_t)(n + LLMOE_FP8B_BLOCK - 1) / LLMOE_FP8B_BLOCK * 4 + 15) / 16 * 16 : 0;
     default: return 0;
   }
 }
@@ -155,7 +157,14 @@ __device__ __forceinline__ uint32_t scale_code(uint32_t amax) {
 __device__ __forceinline__ float scale_inverse(uint32_t code) {
   return code == 255 ? __uint_as_float(0x7fffffffu) : __uint_as_float((254u - code) << 23);
 }
-// Two quotients as e4m3 (nearest even; none exceeds 448), a in the low byte.
+// The FP8B scale of a block whose largest magnitude is amax (NaN where the block
+// holds one): NaN where it is not finite; the codes are of v * (1 / scale).  The
+// least scale is a normal float with a finite inverse.
+__device__ __forceinline__ float block_scale(float amax) {
+  if (!(amax < INFINITY)) return __uint_as_float(0x7fffffffu);
+  return fmaxf(__fdiv_rn(amax, 448.0f), 0x1p-126f);
+}
+// Two quotients as e4m3 (nearest even; none rounds to more than 448), a in the low byte.
 __device__ __forceinline__ uint32_t pack_e4m3x2(float a, float b) {
   return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }

@@ -50,15 +50,9 @@
 // epilogue sets 656 / 2272 / 1285; no cluster release in the scale warps (2600
 // cycles each) 651 / 2265 / 1177; loads by two warps, the epilogue as below 620
 // / 2197 / 1136.
-#include "block_tensor.cuh"
+#include "block_plan.cuh"
 
 namespace {
-
-constexpr int kPlanDepth = 4;       // planned tiles in flight
-constexpr int kStages = 6;          // of the ring at most; fewer where thousands of experts take their room
-constexpr int kTileFeatures = 256;  // rows of w per tile: 128 in each CTA
-constexpr int kGroup = 4;           // rows of x taken together
-constexpr int kBoxes = 6;           // x loads of 1, 2, .. 32 groups
 
 // Per operand type: the most rows per tile and the ring stage's layout (128
 // bytes of K: 64 values of 16 bits or 128 of 8 bits).
@@ -77,66 +71,6 @@ struct Shape {
   static constexpr int kScaleColumns = 12, kScaleRing = 5;
   static_assert(2 * kMaxRows + (kMx ? kScaleRing * kScaleColumns : 0) <= 512, "tensor memory has 512 columns");
 };
-
-struct ProductArgs {
-  const uint8_t* x;
-  const uint8_t* w;
-  uint8_t* y;
-  const int64_t* counts;  // [E][R], or null: the signal words
-  const uint8_t* base;    // rank buffers' signal words: base + (e / L) * rank_stride + sig_off
-  uint64_t rank_stride, sig_off;
-  int32_t* err;
-  int T, R, E, L;
-  int in, out, n;  // n: rows of w per expert
-  uint64_t x_row;  // bytes of a row
-  uint32_t y_row;
-  int dtype, out_dtype;
-  int blocks;   // feature tiles per expert
-  int steps;    // 128-byte steps of K
-  int stages;   // of the ring
-  uint32_t idesc;  // instruction descriptor without N and scale ids
-};
-
-struct ProductMaps {
-  CUtensorMap w, x[kBoxes];
-};
-
-// Received rows of the buckets (e, s), s = src, src + stride, ... below R, at
-// most N of them (0 for the others); all loads before any check.
-template <int N>
-__device__ __forceinline__ void bucket_counts(const ProductArgs& a, int e, int src, int stride, int (&rows)[N]) {
-  const int64_t* p = a.counts != nullptr
-                         ? a.counts + (int64_t)e * a.R
-                         : reinterpret_cast<const int64_t*>(a.base + (e / a.L) * a.rank_stride + a.sig_off) +
-                               (int64_t)(e % a.L) * a.R;
-  int64_t c[N];
-  bool bad = false;
-#pragma unroll
-  for (int i = 0; i < N; ++i) c[i] = src + i * stride < a.R ? p[src + i * stride] : 0;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    bad |= c[i] < 0 || c[i] > a.T;
-    rows[i] = (int)max((int64_t)0, min(c[i], (int64_t)a.T));
-  }
-  if (bad) report(a.err, LLMOE_DEV_SLOT_RANGE);
-}
-__device__ __forceinline__ int groups_of(int rows) { return (rows + kGroup - 1) / kGroup; }
-
-// A planned tile; its rows are in the plan's row list.
-struct __align__(16) Tile {
-  int expert, block, groups;
-  int boxes;  // loads of x rows in this CTA
-  int bytes;  // that the loads of x rows of both CTAs bring
-};
-
-// One load of consecutive x rows: offset in the stage's rows, first row, and
-// the power of two of its groups.
-struct __align__(16) Box {
-  int offset, row, size, unused;
-};
-
-// Columns of a tile's product: a CTA pair's N is a multiple of 32.
-__device__ __forceinline__ int columns(int groups) { return (groups * kGroup + 31) / 32 * 32; }
 
 // Byte offsets in dynamic shared memory, from its first 1024-byte boundary.
 struct SmemLayout {
@@ -161,227 +95,8 @@ __host__ __device__ inline SmemLayout smem_layout(int stages, int E) {
 }
 
 // ---------------------------------------------------------------------------
-// prologue: shares before each expert
-// ---------------------------------------------------------------------------
-// An expert's groups are cut into shares, the fewest of at most kMaxRows rows;
-// every share meets a.blocks feature blocks.  prefix[e] = shares of the experts
-// before e (prefix[E]: all).
-template <bool kMx>
-__device__ void count_shares(const ProductArgs& a, int* prefix, int* part) {
-  constexpr int kThreads = Shape<kMx>::kThreads, kMost = Shape<kMx>::kMaxRows / kGroup, kBatch = 8;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (a.R >= 32) {  // a warp per expert
-    for (int e = warp; e < a.E; e += kThreads / 32) {
-      int n = 0;
-      for (int s = lane; s < a.R; s += 32 * kBatch) {
-        int c[kBatch];
-        bucket_counts(a, e, s, 32, c);
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) n += groups_of(c[i]);
-      }
-      n = __reduce_add_sync(0xffffffffu, n);
-      if (lane == 0) prefix[e] = (n + kMost - 1) / kMost;
-    }
-  } else {
-    for (int e = tid; e < a.E; e += kThreads) {
-      int n = 0;
-      for (int s = 0; s < a.R; s += kBatch) {
-        int c[kBatch];
-        bucket_counts(a, e, s, 1, c);
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) n += groups_of(c[i]);
-      }
-      prefix[e] = (n + kMost - 1) / kMost;
-    }
-  }
-  __syncthreads();
-  // exclusive scan: a contiguous segment per thread, the segments' sums across the CTA
-  const int seg = (a.E + kThreads - 1) / kThreads, lo = min(a.E, tid * seg), hi = min(a.E, lo + seg);
-  int sum = 0;
-  for (int e = lo; e < hi; ++e) sum += prefix[e];
-  int incl = sum;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl += v;
-  }
-  if (lane == 31) part[warp] = incl;
-  __syncthreads();
-  int run = incl - sum;
-  for (int w = 0; w < warp; ++w) run += part[w];
-  for (int e = lo; e < hi; ++e) {
-    const int t = prefix[e];
-    prefix[e] = run;
-    run += t;
-  }
-  if (tid == kThreads - 1) prefix[a.E] = run;  // the last segments are empty or end at E
-  __syncthreads();
-}
-
-// ---------------------------------------------------------------------------
-// plan: one warp turns a tile's number into its expert, features and rows
-// ---------------------------------------------------------------------------
-// One expert's buckets, 32 source ranks at a time: lane s holds rank s0 + s's
-// rows, and the groups of the ranks from s0 up to and with it.
-struct Buckets {
-  int expert, s0;
-  int rows, incl;
-};
-__device__ __forceinline__ void load_buckets(const ProductArgs& a, int e, int s0, Buckets& b) {
-  if (b.expert == e && b.s0 == s0) return;  // the previous tile's
-  const int lane = threadIdx.x & 31;
-  b.expert = e;
-  b.s0 = s0;
-  int c[1];
-  bucket_counts(a, e, s0 + lane, 1, c);
-  b.rows = c[0];
-  b.incl = groups_of(b.rows);
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, b.incl, d);
-    if (lane >= d) b.incl += v;
-  }
-}
-
-// Groups of expert e in order: source ranks ascending, slots ascending.  The
-// tile's share [g0, g1) goes to list, one entry per column: the row of x and y,
-// or -1 where there is none.  A lane takes a group: it finds the group's bucket
-// by a search over the lanes' sums.
-__device__ void plan_rows(const ProductArgs& a, int e, int g0, int g1, Buckets& b, int* list) {
-  const int lane = threadIdx.x & 31;
-  int before = 0;
-  for (int s0 = 0; s0 < a.R && before < g1; s0 += 32) {
-    load_buckets(a, e, s0, b);
-    const int end = before + __shfl_sync(0xffffffffu, b.incl, 31);
-    for (int first = max(g0, before); first < min(g1, end); first += 32) {
-      const int g = first + lane, target = g - before;
-      int s = 0;  // the first lane whose sum is above target
-#pragma unroll
-      for (int d = 16; d; d >>= 1)
-        if (__shfl_sync(0xffffffffu, b.incl, s + d - 1) <= target) s += d;
-      s = min(s, 31);
-      const int cnt = __shfl_sync(0xffffffffu, b.rows, s), incl = __shfl_sync(0xffffffffu, b.incl, s);
-      if (g < min(g1, end)) {
-        const int slot = (target - (incl - groups_of(cnt))) * kGroup, row = (e * a.R + s0 + s) * a.T + slot;
-        static_assert(kGroup == 4, "a group is one 16-byte store");
-        *reinterpret_cast<int4*>(list + (g - g0) * kGroup) =
-            make_int4(row, slot + 1 < cnt ? row + 1 : -1, slot + 2 < cnt ? row + 2 : -1, slot + 3 < cnt ? row + 3 : -1);
-      }
-    }
-    before = end;
-  }
-  for (int i = (g1 - g0) * kGroup + lane; i < columns(g1 - g0); i += 32) list[i] = -1;
-}
-
-// The box that starts at this lane's group, as the power of two of its groups,
-// or -1: a CTA's share of a tile is `groups` groups, lane g's starting at row
-// `row`.  A run of consecutive rows is one box, or two of the same size that
-// overlap where its length is no power of two (the rows in both are written
-// twice, with the same values): loads are bound by their number.
-__device__ __forceinline__ int plan_box(int row, int groups) {
-  const int lane = threadIdx.x & 31;
-  const int prev = __shfl_up_sync(0xffffffffu, row, 1);
-  const uint32_t heads = __ballot_sync(0xffffffffu, lane < groups && (lane == 0 || row != prev + kGroup));
-  if (lane >= groups) return -1;
-  const int head = 31 - __clz(heads & (0xffffffffu >> (31 - lane)));
-  const uint32_t later = lane == 31 ? 0 : heads >> (lane + 1);
-  const int len = (later ? lane + __ffs(later) : groups) - head, p = lane - head;
-  const int size = 31 - __clz(len);
-  return p == 0 || p == len - (1 << size) ? size : -1;
-}
-
-// Where tile t lies: expert, feature block, and which of the expert's shares.
-struct Place {
-  int expert, block, share, shares;
-};
-__device__ __forceinline__ Place find_tile(const ProductArgs& a, const int* prefix, int t) {
-  // the largest e with prefix[e] <= t / blocks (it has shares, for the next is
-  // above), 32 candidates at a time
-  const int lane = threadIdx.x & 31, nth = t / a.blocks;
-  int e = 0;
-  for (int span = a.E; span > 1;) {
-    const int step = (span + 31) / 32, at = e + lane * step;
-    const uint32_t below = __ballot_sync(0xffffffffu, lane * step < span && prefix[at] <= nth);
-    const int last = 31 - __clz(below);  // lane 0's is: prefix[e] <= nth
-    e += last * step;
-    span = min(step, span - last * step);
-  }
-  Place p{e, t - prefix[e] * a.blocks, 0, prefix[e + 1] - prefix[e]};
-  if (p.shares > 1) {
-    const int local = p.block;
-    p.block = local / p.shares;
-    p.share = local - p.block * p.shares;
-  }
-  return p;
-}
-
-template <bool kMx>
-__device__ void plan_tile(const ProductArgs& a, const int* prefix, int t, int rank, Buckets& b, Tile* tile, int* list,
-                          Box* boxes) {
-  constexpr int kMaxRows = Shape<kMx>::kMaxRows;
-  const int lane = threadIdx.x & 31;
-  const Place place = find_tile(a, prefix, t);
-  const int e = place.expert, shares = place.shares, share = place.share;
-  int total = 0;
-  for (int s0 = 0; s0 < a.R; s0 += 32) {
-    load_buckets(a, e, s0, b);
-    total += __shfl_sync(0xffffffffu, b.incl, 31);
-  }
-  // shares of whole 32s of columns, as equal as that allows, the remainder
-  // last: 1040 rows are 4 x 224 + 144 columns, 1056 as padded (five equal
-  // shares would pad to 1120).  shares is the fewest that hold the total, so the
-  // last is never empty.
-  const int per = shares == 1 ? total : columns((total + shares - 1) / shares) / kGroup;
-  const int g0 = share * per, g1 = min(total, g0 + per);
-  static_assert(kMaxRows % 32 == 0, "a share of at most kMaxRows rows pads to at most kMaxRows");
-  plan_rows(a, e, g0, g1, b, list);
-  __syncwarp();
-  // the loads of each CTA's half of the columns
-  const int half = columns(g1 - g0) / 2;
-  int bytes = 0, count = 0;
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    const int mine = max(0, min(g1 - g0 - r * (half / kGroup), half / kGroup));
-    const int row = lane < mine ? list[r * half + lane * kGroup] : 0;
-    const int box = plan_box(row, mine);
-    const uint32_t all = __ballot_sync(0xffffffffu, box >= 0);
-    bytes += __reduce_add_sync(0xffffffffu, box >= 0 ? kGroup * 128 << box : 0);
-    if (r == rank) {
-      count = __popc(all);
-      if (box >= 0) boxes[__popc(all & ((1u << lane) - 1))] = Box{lane * (kGroup * 128), row, box, 0};
-    }
-  }
-  if (lane == 0) *tile = Tile{e, place.block, g1 - g0, count, bytes};
-}
-
-// ---------------------------------------------------------------------------
 // epilogue
 // ---------------------------------------------------------------------------
-// v / (1 + exp(-v)) in fp32, for fp32 outputs, which show its bits (4096 rows of
-// 1024 -> 2 x 2048: 38 us against 33 with near_silu, one token 80.3 against 78.1).
-__device__ __forceinline__ float silu(float v) { return v / (1.0f + expf(-v)); }
-// The same with the hardware's exponential and division, for outputs of 16 or 8
-// bits: each within a few units of the last fp32 place (the exponential's also
-// grow by |v| halves of one: 30 units at v = -75, a 64th of half an fp16 unit); a
-// denominator above 2^126 gives 0 for what is below 2^-118.  silu() for those too
-// took one token from 78.9 to 81.1 us.
-__device__ __forceinline__ float near_silu(float v) { return __fdividef(v, 1.0f + __expf(-v)); }
-
-// Two values as BF16 or FP16, the first in the low half.
-__device__ __forceinline__ uint32_t pack2(float lo, float hi, bool fp16) {
-  if (fp16) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// `at`, an address in row 0 of y, moved to `row`.
-__device__ __forceinline__ uint8_t* in_row(const ProductArgs& a, uint8_t* at, int row) {
-  return at + (uint64_t)(uint32_t)row * a.y_row;
-}
-
 // 32 columns (rows of y) of 32 features: lane l holds feature first + l.
 // list: the columns' rows, -1 where nothing is stored (read before the stores,
 // which the compiler cannot tell from writes to it).
@@ -566,7 +281,7 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
   if (warp == 3) tmem_alloc_pair(sbase + l.tmem, 512);
   wait_prior_grid();
   release_next_grid();
-  count_shares<kMx>(a, prefix, reinterpret_cast<int*>(smem + l.part));
+  count_shares<S::kMaxRows, S::kThreads>(a, prefix, reinterpret_cast<int*>(smem + l.part));
   tc_fence_before();
   __syncthreads();
   cluster_sync();
@@ -710,7 +425,7 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
     for (int t = pair; t < ntiles; t += pairs, ++i) {
       const int slot = i % kPlanDepth;
       if (!mbar_wait_warp(plan_empty + 8 * slot, ((i / kPlanDepth) & 1) ^ 1, a.err)) break;
-      plan_tile<kMx>(a, prefix, t, (int)rank, buckets, tiles + slot, rows + slot * S::kMaxRows, boxes + 32 * slot);
+      plan_tile<S::kMaxRows>(a, prefix, t, (int)rank, buckets, tiles + slot, rows + slot * S::kMaxRows, boxes + 32 * slot);
       __syncwarp();
       if (lane == 0) mbar_arrive(plan_full + 8 * slot);
     }
@@ -838,134 +553,26 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
 // Checks a product's arguments and fills its geometry.
 int product_args(const void* x, const void* w, void* y, const int64_t* counts, int in, int out, int dtype,
                  int out_dtype, uint32_t flags, const llmoe_buf_set_t* bs, ProductArgs* a) {
-  if (bs == nullptr || (flags & ~LLMOE_PRODUCT_SWIGLU) != 0) return LLMOE_ERR_INVALID_ARGUMENT;
+  if ((flags & ~LLMOE_PRODUCT_SWIGLU) != 0 || !product_buckets(counts, bs, a)) return LLMOE_ERR_INVALID_ARGUMENT;
   const bool swiglu = (flags & LLMOE_PRODUCT_SWIGLU) != 0;
-  const int T = bs->num_max_tokens, R = bs->num_ranks, E = bs->num_experts;
-  if (T < 1 || R < 1 || E < R || E % R != 0 || E > LLMOE_MAX_EXPERTS || !aligned(bs->err, 4))
-    return LLMOE_ERR_INVALID_ARGUMENT;
-  if ((uint64_t)E * R > INT32_MAX || (uint64_t)E * R * T > INT32_MAX) return LLMOE_ERR_INVALID_ARGUMENT;
   switch (dtype) {
     case LLMOE_DTYPE_BF16:
     case LLMOE_DTYPE_FP16:
       if (out_dtype != dtype && out_dtype != LLMOE_DTYPE_FP32) return LLMOE_ERR_INVALID_ARGUMENT;
       break;
     case LLMOE_DTYPE_MX8:
-      if (out_dtype == LLMOE_DTYPE_MX8 && !swiglu) return LLMOE_ERR_INVALID_ARGUMENT;
+      if ((out_dtype == LLMOE_DTYPE_MX8 && !swiglu) || out_dtype == LLMOE_DTYPE_FP8B) return LLMOE_ERR_INVALID_ARGUMENT;
       break;
     default: return LLMOE_ERR_INVALID_ARGUMENT;
   }
-  const uint64_t xr = row_bytes(in, dtype), yr = row_bytes(out, out_dtype);
-  if (xr == 0 || yr == 0 || yr > INT32_MAX || out > INT32_MAX / 2 || (swiglu && out % 8 != 0)) return LLMOE_ERR_INVALID_ARGUMENT;
-  if (x == nullptr || w == nullptr || y == nullptr || !aligned(x, 16) || !aligned(w, 16) || !aligned(y, 16) ||
-      !aligned(counts, 8))
+  const uint64_t xr = row_bytes(in, dtype);
+  if (!product_rows(x, y, in, out, dtype, out_dtype, swiglu, a) || w == nullptr || !aligned(w, 16) ||
+      xr > kMostBytes / ((uint64_t)a->n * a->E))
     return LLMOE_ERR_INVALID_ARGUMENT;
-  const uint64_t rows = (uint64_t)E * R * T, n = (uint64_t)out * (swiglu ? 2 : 1);
-  const uint64_t limit = (uint64_t)INT64_MAX / 2;
-  if (xr > limit / rows || yr > limit / rows || xr > limit / (n * E)) return LLMOE_ERR_INVALID_ARGUMENT;
-  if (overlap(y, rows * yr, x, rows * xr) || overlap(y, rows * yr, w, n * E * xr)) return LLMOE_ERR_INVALID_ARGUMENT;
-  *a = ProductArgs{};
-  if (counts == nullptr) {
-    const size_t total = llmoe_layout_bytes_dtype(T, bs->hidden, R, E, bs->dtype);
-    uint64_t sig = 0;
-    if (total == 0 || bs->base == nullptr || !aligned(bs->base, 16) || bs->rank_stride % 16 != 0 ||
-        bs->rank_stride < total || bs->rank_stride > limit / R ||
-        llmoe_layout_offsets_dtype(T, bs->hidden, R, E, bs->dtype, bs->set, nullptr, nullptr, &sig) != LLMOE_SUCCESS ||
-        sig % 8 != 0)
-      return LLMOE_ERR_INVALID_ARGUMENT;
-    a->base = static_cast<const uint8_t*>(bs->base);
-    a->rank_stride = bs->rank_stride;
-    a->sig_off = sig;
-  }
-  a->x = static_cast<const uint8_t*>(x);
+  const uint64_t rows = (uint64_t)a->E * a->R * a->T;
+  if (overlap(y, rows * a->y_row, w, (uint64_t)a->n * a->E * xr)) return LLMOE_ERR_INVALID_ARGUMENT;
   a->w = static_cast<const uint8_t*>(w);
-  a->y = static_cast<uint8_t*>(y);
-  a->counts = counts;
-  a->err = bs->err;
-  a->T = T;
-  a->R = R;
-  a->E = E;
-  a->L = E / R;
-  a->in = in;
-  a->out = out;
-  a->n = (int)n;
-  a->x_row = xr;
-  a->y_row = (uint32_t)yr;
-  a->dtype = dtype;
-  a->out_dtype = out_dtype;
   return LLMOE_SUCCESS;
-}
-
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// The driver's tensor-map encoder, looked up once (the library does not link libcuda).
-EncodeTiled encode_tiled() {
-  static std::atomic<EncodeTiled> cache{nullptr};
-  EncodeTiled f = cache.load(std::memory_order_acquire);
-  if (f != nullptr) return f;
-  void* p = nullptr;
-  cudaDriverEntryPointQueryResult found;
-  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
-      found != cudaDriverEntryPointSuccess) {
-    cudaGetLastError();
-    return nullptr;
-  }
-  f = reinterpret_cast<EncodeTiled>(p);
-  cache.store(f, std::memory_order_release);
-  return f;
-}
-
-// Rows of 128-byte steps along K, 128-byte swizzle; `dims` beyond the row.
-bool make_map(CUtensorMap* m, const void* base, int dtype, const cuuint64_t* dims, const cuuint64_t* strides,
-              const cuuint32_t* box, int rank) {
-  const EncodeTiled encode = encode_tiled();
-  if (encode == nullptr) return false;
-  const CUtensorMapDataType type = dtype == LLMOE_DTYPE_BF16   ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                   : dtype == LLMOE_DTYPE_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
-                                                               : CU_TENSOR_MAP_DATA_TYPE_UINT8;
-  const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
-  return encode(m, type, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, ones,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-constexpr size_t kMaxSmem = 232448;  // 227 KB
-
-// Opts the kernel in to its shared memory and asks how many pairs can be
-// resident, once per device.  Asked with the most shared memory: whatever a call
-// uses is more than half of an SM's, so there is one CTA on an SM in any case.
-template <bool kMx, bool kSwiglu>
-int resident_pairs() {
-  static_assert((kStages - 1) * Shape<kMx>::kStage > kMaxSmem / 2, "one CTA per SM");
-  constexpr int kMaxDevices = 64;
-  static std::atomic<int> cache[kMaxDevices];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 0;
-  if (dev < kMaxDevices) {
-    const int c = cache[dev].load(std::memory_order_relaxed);
-    if (c > 0) return c;
-  }
-  const auto kernel = product_kernel<kMx, kSwiglu>;
-  int n = 0;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * num_sms());
-  cfg.blockDim = dim3(Shape<kMx>::kThreads);
-  cfg.dynamicSmemBytes = kMaxSmem;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem) != cudaSuccess ||
-      cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
-    cudaGetLastError();
-    return 0;
-  }
-  if (dev < kMaxDevices) cache[dev].store(n, std::memory_order_relaxed);
-  return n;
 }
 
 template <bool kMx, bool kSwiglu>
@@ -1004,7 +611,8 @@ int launch_product(ProductArgs& a, llmoe_stream_t stream) {
     const cuuint32_t box[3] = {k_box, 128, 1};
     if (!make_map(&maps.w, a.w, a.dtype, dims, strides, box, 3)) return LLMOE_ERR_CUDA;
   }
-  const int pairs = resident_pairs<kMx, kSwiglu>();
+  static_assert((kStages - 1) * S::kStage > kMaxSmem / 2, "one CTA per SM");
+  const int pairs = resident_pairs<product_kernel<kMx, kSwiglu>>(S::kThreads);
   if (pairs < 1) return LLMOE_ERR_CUDA;
 
   cudaLaunchConfig_t cfg = {};

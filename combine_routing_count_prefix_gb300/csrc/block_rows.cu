@@ -1,4 +1,4 @@
-// block_rows.cu -- llmoe_add_rmsnorm, llmoe_pack_mx8 and llmoe_row_bytes
+// block_rows.cu -- llmoe_add_rmsnorm, llmoe_pack_mx8, llmoe_pack_fp8b and llmoe_row_bytes
 // (include/llmoe_block.h).
 //
 // One CTA holds one row at a time in registers: 16-byte loads of x and
@@ -21,7 +21,7 @@ namespace {
 struct RowsArgs {
   const uint4* x;
   const uint4* residual;  // or null
-  const uint4* weight;    // null for llmoe_pack_mx8
+  const uint4* weight;    // null for llmoe_pack_mx8 and llmoe_pack_fp8b
   uint4* residual_out;    // or null
   uint8_t* out;
   int64_t rows;
@@ -104,12 +104,13 @@ __device__ __forceinline__ float block_sum(float v, float* part) {
   return v;
 }
 
-// DT: T of x, residual, weight; MX: MX8 output rows; Q: quads per thread;
-// kNorm: false for llmoe_pack_mx8.
-template <int DT, bool MX, int Q, bool kNorm>
+// DT: T of x, residual, weight; OUT: DT, or MX8 or FP8B output rows; Q: quads
+// per thread; kNorm: false for llmoe_pack_mx8 and llmoe_pack_fp8b.
+template <int DT, int OUT, int Q, bool kNorm>
 __global__ void __launch_bounds__(1024) rows_kernel(RowsArgs a) {
   constexpr int V = Quad<DT>::kValues, P = V / 2;
-  constexpr int kLanes = 32 / V;  // adjacent lanes that hold one group of 32
+  constexpr bool MX = OUT == LLMOE_DTYPE_MX8, k8Bit = MX || OUT == LLMOE_DTYPE_FP8B;
+  constexpr int kLanes = (MX ? 32 : LLMOE_FP8B_BLOCK) / V;  // adjacent lanes that hold one scale's values
   __shared__ float part[32];
   wait_prior_grid();
   release_next_grid();
@@ -163,7 +164,7 @@ __global__ void __launch_bounds__(1024) rows_kernel(RowsArgs a) {
 #pragma unroll
         for (int k = 0; k < P; ++k) v[k] = mul2(mul2(v[k], r2), w[k]);
       }
-      if constexpr (MX) {
+      if constexpr (k8Bit) {
         float most = 0.0f;
 #pragma unroll
         for (int k = 0; k < P; ++k) {
@@ -172,8 +173,9 @@ __global__ void __launch_bounds__(1024) rows_kernel(RowsArgs a) {
         }
 #pragma unroll
         for (int d = 1; d < kLanes; d <<= 1) most = max_magnitude(most, __shfl_xor_sync(0xffffffffu, most, d));
-        const uint32_t code = scale_code(__float_as_uint(most));
-        const float inv = scale_inverse(code);
+        // the scale, as an e8m0 code or a float, and its inverse
+        const uint32_t scale = MX ? scale_code(__float_as_uint(most)) : __float_as_uint(block_scale(most));
+        const float inv = MX ? scale_inverse(scale) : __frcp_rn(__uint_as_float(scale));
         const Pair inv2 = pair(inv, inv);
         if (j < a.nq) {
           uint32_t b[P];
@@ -187,7 +189,12 @@ __global__ void __launch_bounds__(1024) rows_kernel(RowsArgs a) {
                 make_uint2(__byte_perm(b[0], b[1], 0x5410), __byte_perm(b[2], b[3], 0x5410));
           else
             *reinterpret_cast<uint32_t*>(out + (size_t)j * 4) = __byte_perm(b[0], b[1], 0x5410);
-          if (j % kLanes == 0) out[a.hidden + j / kLanes] = (uint8_t)code;
+          if (j % kLanes == 0) {
+            if constexpr (MX)
+              out[a.hidden + j / kLanes] = (uint8_t)scale;
+            else
+              reinterpret_cast<uint32_t*>(out + a.hidden)[j / kLanes] = scale;
+          }
         }
       } else if (j < a.nq) {
         float f[V];
@@ -200,36 +207,39 @@ __global__ void __launch_bounds__(1024) rows_kernel(RowsArgs a) {
         reinterpret_cast<uint4*>(out)[j] = pack_quad<DT>(f);
       }
     }
-    if constexpr (MX) {  // zeros up to the row's 16-byte end
-      const int used = a.hidden + a.hidden / 32;
+    if constexpr (k8Bit) {  // zeros up to the row's 16-byte end
+      const int used = a.hidden + (MX ? a.hidden / 32 : (a.hidden + LLMOE_FP8B_BLOCK - 1) / LLMOE_FP8B_BLOCK * 4);
       if (tid < (int)a.out_stride - used) out[used + tid] = 0;
     }
   }
 }
 
-template <int DT, bool MX, bool kNorm>
+template <int DT, int OUT, bool kNorm>
 int launch_rows(const RowsArgs& a, llmoe_stream_t stream) {
   // two quads per thread where a CTA has threads enough; as many CTAs as the
   // registers (64 a thread) hold
   const int threads = std::min(1024, std::max(128, ((a.nq + 1) / 2 + 31) / 32 * 32));
   const unsigned grid = (unsigned)std::min<int64_t>(a.rows, (int64_t)num_sms() * (1024 / threads));
   const int q = (a.nq + threads - 1) / threads;
-  if (q <= 1) return launch_block(rows_kernel<DT, MX, 1, kNorm>, grid, threads, 0, stream, a);
-  if (q <= 2) return launch_block(rows_kernel<DT, MX, 2, kNorm>, grid, threads, 0, stream, a);
+  if (q <= 1) return launch_block(rows_kernel<DT, OUT, 1, kNorm>, grid, threads, 0, stream, a);
+  if (q <= 2) return launch_block(rows_kernel<DT, OUT, 2, kNorm>, grid, threads, 0, stream, a);
   if constexpr (DT == LLMOE_DTYPE_FP32)  // 16-bit rows have at most four quads for each of 1024 threads
-    if (q > 4) return launch_block(rows_kernel<DT, MX, 8, kNorm>, grid, threads, 0, stream, a);
+    if (q > 4) return launch_block(rows_kernel<DT, OUT, 8, kNorm>, grid, threads, 0, stream, a);
   static_assert(LLMOE_MAX_ROW_VALUES <= 4 * 1024 * 8, "16-bit rows past four quads a thread");
-  return launch_block(rows_kernel<DT, MX, 4, kNorm>, grid, threads, 0, stream, a);
+  return launch_block(rows_kernel<DT, OUT, 4, kNorm>, grid, threads, 0, stream, a);
 }
 
-template <bool MX, bool kNorm>
+// OUT: MX8 or FP8B rows, or (BF16) rows of the input's type.
+template <int OUT, bool kNorm>
 int launch_rows_dtype(const RowsArgs& a, int dtype, llmoe_stream_t stream) {
+  constexpr bool k8Bit = OUT == LLMOE_DTYPE_MX8 || OUT == LLMOE_DTYPE_FP8B;
   switch (dtype) {
-    case LLMOE_DTYPE_FP16: return launch_rows<LLMOE_DTYPE_FP16, MX, kNorm>(a, stream);
-    case LLMOE_DTYPE_FP32: return launch_rows<LLMOE_DTYPE_FP32, MX, kNorm>(a, stream);
-    default: return launch_rows<LLMOE_DTYPE_BF16, MX, kNorm>(a, stream);
+    case LLMOE_DTYPE_FP16: return launch_rows<LLMOE_DTYPE_FP16, k8Bit ? OUT : LLMOE_DTYPE_FP16, kNorm>(a, stream);
+    case LLMOE_DTYPE_FP32: return launch_rows<LLMOE_DTYPE_FP32, k8Bit ? OUT : LLMOE_DTYPE_FP32, kNorm>(a, stream);
+    default: return launch_rows<LLMOE_DTYPE_BF16, k8Bit ? OUT : LLMOE_DTYPE_BF16, kNorm>(a, stream);
   }
 }
+
 
 // Fills the geometry of a call on `rows` rows of `hidden` values; false where
 // the arguments are not valid.
@@ -249,6 +259,15 @@ bool rows_geometry(const void* x, const void* out, int64_t rows, int hidden, int
   return true;
 }
 
+template <int OUT>
+int pack_rows(const void* x, void* out, int64_t rows, int hidden, int dtype, llmoe_stream_t stream) {
+  RowsArgs a;
+  if (!rows_geometry(x, out, rows, hidden, dtype, OUT, &a)) return LLMOE_ERR_INVALID_ARGUMENT;
+  if (rows == 0) return LLMOE_SUCCESS;
+  if (overlap(x, (uint64_t)rows * a.nq * 16, out, (uint64_t)rows * a.out_stride)) return LLMOE_ERR_INVALID_ARGUMENT;
+  return launch_rows_dtype<OUT, false>(a, dtype, stream);
+}
+
 }  // namespace
 
 extern "C" {
@@ -256,17 +275,17 @@ extern "C" {
 size_t llmoe_row_bytes(int n, int dtype) { return (size_t)row_bytes(n, dtype); }
 
 int llmoe_pack_mx8(const void* x, void* out, int64_t rows, int hidden, int dtype, llmoe_stream_t stream) {
-  RowsArgs a;
-  if (!rows_geometry(x, out, rows, hidden, dtype, LLMOE_DTYPE_MX8, &a)) return LLMOE_ERR_INVALID_ARGUMENT;
-  if (rows == 0) return LLMOE_SUCCESS;
-  if (overlap(x, (uint64_t)rows * a.nq * 16, out, (uint64_t)rows * a.out_stride)) return LLMOE_ERR_INVALID_ARGUMENT;
-  return launch_rows_dtype<true, false>(a, dtype, stream);
+  return pack_rows<LLMOE_DTYPE_MX8>(x, out, rows, hidden, dtype, stream);
+}
+
+int llmoe_pack_fp8b(const void* x, void* out, int64_t rows, int hidden, int dtype, llmoe_stream_t stream) {
+  return pack_rows<LLMOE_DTYPE_FP8B>(x, out, rows, hidden, dtype, stream);
 }
 
 int llmoe_add_rmsnorm(const void* x, const void* residual, const void* weight, float eps, void* residual_out,
                       void* out, int64_t rows, int hidden, int dtype, int out_dtype, llmoe_stream_t stream) {
   RowsArgs a;
-  if ((out_dtype != dtype && out_dtype != LLMOE_DTYPE_MX8) || !(eps >= 0.0f) ||
+  if ((out_dtype != dtype && out_dtype != LLMOE_DTYPE_MX8 && out_dtype != LLMOE_DTYPE_FP8B) || !(eps >= 0.0f) ||
       !rows_geometry(x, out, rows, hidden, dtype, out_dtype, &a))
     return LLMOE_ERR_INVALID_ARGUMENT;
   if (rows == 0) return LLMOE_SUCCESS;
@@ -289,8 +308,11 @@ int llmoe_add_rmsnorm(const void* x, const void* residual, const void* weight, f
   a.residual_out = static_cast<uint4*>(residual_out);
   a.eps = eps;
   a.inv_n = 1.0f / (float)hidden;
-  return out_dtype == LLMOE_DTYPE_MX8 ? launch_rows_dtype<true, true>(a, dtype, stream)
-                                      : launch_rows_dtype<false, true>(a, dtype, stream);
+  switch (out_dtype) {
+    case LLMOE_DTYPE_MX8: return launch_rows_dtype<LLMOE_DTYPE_MX8, true>(a, dtype, stream);
+    case LLMOE_DTYPE_FP8B: return launch_rows_dtype<LLMOE_DTYPE_FP8B, true>(a, dtype, stream);
+    default: return launch_rows_dtype<LLMOE_DTYPE_BF16, true>(a, dtype, stream);
+  }
 }
 
 }  // extern "C"

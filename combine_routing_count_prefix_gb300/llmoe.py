@@ -52,15 +52,20 @@ EXPORTS = ("llmoe_layout_bytes", "llmoe_layout_bytes_dtype", "llmoe_layout_offse
            "llmoe_signal_workspace_bytes", "llmoe_dispatch_signaled", "llmoe_dispatch_signaled_static", "llmoe_clean",
            "llmoe_get_error",
            "llmoe_status_string",
-           "llmoe_row_bytes", "llmoe_pack_mx8", "llmoe_add_rmsnorm", "llmoe_topk_router", "llmoe_expert_product")
+           "llmoe_row_bytes", "llmoe_pack_mx8", "llmoe_add_rmsnorm", "llmoe_topk_router", "llmoe_expert_product",
+           "llmoe_pack_fp8b", "llmoe_pack_fp8b_weights", "llmoe_group_router", "llmoe_expert_product_fp8b")
 
 LLMOE_DTYPE_BF16, LLMOE_DTYPE_FP16, LLMOE_DTYPE_FP32 = 0, 1, 2
 DTYPE_CODES = {"bf16": LLMOE_DTYPE_BF16, "fp16": LLMOE_DTYPE_FP16, "fp32": LLMOE_DTYPE_FP32}
 LLMOE_DTYPE_MX8 = 3  # 8-bit rows with scales: a row type of the block operators, not a payload type
-ROW_DTYPE_CODES = {**DTYPE_CODES, "mx8": LLMOE_DTYPE_MX8}
+LLMOE_DTYPE_FP8B = 5  # 8-bit rows with a scale for each block of 128, the same
+LLMOE_FP8B_BLOCK = 128
+ROW_DTYPE_CODES = {**DTYPE_CODES, "mx8": LLMOE_DTYPE_MX8, "fp8b": LLMOE_DTYPE_FP8B}
 LLMOE_MAX_ROW_VALUES = 32768
 LLMOE_SCORE_SIGMOID, LLMOE_SCORE_SOFTMAX = 0, 1
 LLMOE_ROUTER_RENORM = 1
+LLMOE_ROUTER_GROUP_TOP2 = 2
+LLMOE_MAX_GROUPS = 256
 LLMOE_PRODUCT_SWIGLU = 1
 DTYPE_BYTES = {LLMOE_DTYPE_BF16: 2, LLMOE_DTYPE_FP16: 2, LLMOE_DTYPE_FP32: 4}
 
@@ -128,6 +133,14 @@ _lib.llmoe_topk_router.argtypes = [_P, _P, _P, _P, _P, _L, _I, _I, _I, _I, _U, _
 _lib.llmoe_topk_router.restype = _I
 _lib.llmoe_expert_product.argtypes = [_P, _P, _P, _P, _I, _I, _I, _I, _U, _BS, _P]
 _lib.llmoe_expert_product.restype = _I
+_lib.llmoe_pack_fp8b.argtypes = [_P, _P, _L, _I, _I, _P]
+_lib.llmoe_pack_fp8b.restype = _I
+_lib.llmoe_pack_fp8b_weights.argtypes = [_P, _P, _P, _L, _I, _I, _I, _P]
+_lib.llmoe_pack_fp8b_weights.restype = _I
+_lib.llmoe_group_router.argtypes = [_P, _P, _P, _P, _P, _L, _I, _I, _I, _I, _I, _I, _U, _F, _P]
+_lib.llmoe_group_router.restype = _I
+_lib.llmoe_expert_product_fp8b.argtypes = [_P, _P, _P, _P, _P, _I, _I, _I, _U, _BS, _P]
+_lib.llmoe_expert_product_fp8b.restype = _I
 _lib.llmoe_status_string.argtypes = [_I]
 _lib.llmoe_status_string.restype = ctypes.c_char_p
 
@@ -151,6 +164,7 @@ _DTYPES = {
     "f32": (torch.float32,),
     "u8": (torch.uint8, torch.bool),
     "rows": (torch.bfloat16, torch.float16, torch.int16, torch.uint16, torch.float32, torch.uint8),
+    "codes": (torch.uint8, torch.float8_e4m3fn),
 }
 
 
@@ -308,6 +322,32 @@ def llmoe_expert_product(x, w, y, counts, in_features: int, out_features: int, d
     _check(_lib.llmoe_expert_product(_addr(x, "rows"), _addr(w, "rows"), _addr(y, "rows"), _addr(counts, "i64"),
                                      in_features, out_features, dtype, out_dtype, flags, ctypes.byref(bs),
                                      _stream(stream)), "llmoe_expert_product")
+
+
+def llmoe_pack_fp8b(x, out, rows: int, hidden: int, dtype: int, stream=None) -> None:
+    _check(_lib.llmoe_pack_fp8b(_addr(x, "payload"), _addr(out, "rows"), rows, hidden, dtype, _stream(stream)),
+           "llmoe_pack_fp8b")
+
+
+def llmoe_pack_fp8b_weights(w, codes, scales, matrices: int, rows: int, cols: int, dtype: int, stream=None) -> None:
+    _check(_lib.llmoe_pack_fp8b_weights(_addr(w, "payload"), _addr(codes, "codes"), _addr(scales, "f32"), matrices,
+                                        rows, cols, dtype, _stream(stream)), "llmoe_pack_fp8b_weights")
+
+
+def llmoe_group_router(logits, bias, active, topk_idx, topk_w, rows: int, num_experts: int, num_topk: int,
+                       num_groups: int, kept_groups: int, dtype: int, scoring: int, flags: int, scale: float,
+                       stream=None) -> None:
+    _check(_lib.llmoe_group_router(_addr(logits, "payload"), _addr(bias, "f32"), _addr(active, "u8"),
+                                   _addr(topk_idx, "i64"), _addr(topk_w, "f32"), rows, num_experts, num_topk,
+                                   num_groups, kept_groups, dtype, scoring, flags, scale, _stream(stream)),
+           "llmoe_group_router")
+
+
+def llmoe_expert_product_fp8b(x, w, w_scale, y, counts, in_features: int, out_features: int, out_dtype: int,
+                              flags: int, bs: llmoe_buf_set_t, stream=None) -> None:
+    _check(_lib.llmoe_expert_product_fp8b(_addr(x, "rows"), _addr(w, "codes"), _addr(w_scale, "f32"), _addr(y, "rows"),
+                                          _addr(counts, "i64"), in_features, out_features, out_dtype, flags,
+                                          ctypes.byref(bs), _stream(stream)), "llmoe_expert_product_fp8b")
 
 
 def geometry(num_max_tokens: int, num_ranks: int, num_experts: int, err=None) -> llmoe_buf_set_t:
