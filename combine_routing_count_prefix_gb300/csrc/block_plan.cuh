@@ -265,6 +265,68 @@ __device__ void plan_tile(const ProductArgs& a, const int* prefix, int t, int ra
 }
 
 // ---------------------------------------------------------------------------
+// loads
+// ---------------------------------------------------------------------------
+// Barriers of the ring and of the plans, as shared-memory addresses.
+struct RingBars {
+  uint32_t full, empty, plan_full, plan_empty;
+};
+
+// One thread of each of two warps, on alternate steps: one box of w and those of
+// x's rows per 128 bytes of K.
+template <int kStage, int kBytesA, int kStepValues, bool kSwiglu>
+__device__ __forceinline__ void load_tiles(const ProductArgs& a, const ProductMaps& maps, uint32_t sbase,
+                                           const RingBars& bars, const Tile* tiles, const Box* boxes, bool second,
+                                           uint32_t rank, int pair, int pairs, int ntiles) {
+  int stage = second, i = 0;
+  int turn = second;  // steps until this thread's next
+  uint32_t phase = 0;
+  bool ok = true;
+  for (int t = pair; t < ntiles && ok; t += pairs, ++i) {
+    const int slot = i % kPlanDepth;
+    if (!(ok = mbar_wait(bars.plan_full + 8 * slot, (i / kPlanDepth) & 1, a.err))) break;
+    const Tile tile = tiles[slot];
+    // the first boxes stay in registers: read from shared memory at every
+    // step, each load would wait for its box
+    constexpr int kKept = 6;
+    Box kept[kKept];
+#pragma unroll
+    for (int b = 0; b < kKept; ++b) kept[b] = b < tile.boxes ? boxes[32 * slot + b] : Box{};
+    int k = turn;
+    for (; k < a.steps; k += 2) {
+      if (!(ok = mbar_wait(bars.empty + 8 * stage, phase ^ 1, a.err))) break;
+      const uint32_t data = sbase + stage * kStage, to = data + kBytesA, bar = map_rank(bars.full + 8 * stage, 0);
+      const int k0 = k * kStepValues;
+      if (rank == 0) mbar_expect_tx(bars.full + 8 * stage, 2 * kBytesA + tile.bytes);  // both CTAs', w and x
+      if constexpr (kSwiglu)
+        tma_tile5(data, &maps.w, k0, 0, 0, tile.block * 16 + (int)rank * 8, tile.expert, bar);
+      else
+        tma_tile3(data, &maps.w, k0, tile.block * kTileFeatures + (int)rank * 128, tile.expert, bar);
+#pragma unroll
+      for (int b = 0; b < kKept; ++b)
+        if (b < tile.boxes) tma_rows(to + kept[b].offset, &maps.x[kept[b].size], k0, kept[b].row, bar);
+      for (int b = kKept; b < tile.boxes; b += 4) {
+        Box q[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) q[u] = b + u < tile.boxes ? boxes[32 * slot + b + u] : Box{};
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (b + u < tile.boxes) tma_rows(to + q[u].offset, &maps.x[q[u].size], k0, q[u].row, bar);
+      }
+      if ((stage += 2) >= a.stages) stage -= a.stages, phase ^= 1;
+    }
+    turn = k - a.steps;
+    mbar_arrive(bars.plan_empty + 8 * slot);
+  }
+  // the ring drains: no product reads shared memory, and no arrival is under
+  // way to this CTA, once every stage has been handed back
+  for (int n = turn; n < a.stages && ok; n += 2) {
+    ok = mbar_wait(bars.empty + 8 * stage, phase ^ 1, a.err);
+    if ((stage += 2) >= a.stages) stage -= a.stages, phase ^= 1;
+  }
+}
+
+// ---------------------------------------------------------------------------
 // epilogue
 // ---------------------------------------------------------------------------
 // v / (1 + exp(-v)) in fp32, for fp32 outputs, which show its bits (4096 rows of

@@ -288,58 +288,13 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + l.tmem);
 
+  const RingBars bars{full, empty, plan_full, plan_empty};
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, ntiles = prefix[a.E] * a.blocks;
 
   if (warp == 0 || warp == 3) {
-    // ---- loads: one thread of each of two warps, on alternate steps ----------------
-    if (elect_one()) {
-      int stage = warp == 3, i = 0;
-      int turn = warp == 3;  // steps until this thread's next
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int t = pair; t < ntiles && ok; t += pairs, ++i) {
-        const int slot = i % kPlanDepth;
-        if (!(ok = mbar_wait(plan_full + 8 * slot, (i / kPlanDepth) & 1, a.err))) break;
-        const Tile tile = tiles[slot];
-        // the first boxes stay in registers: read from shared memory at every
-        // step, each load would wait for its box
-        constexpr int kKept = 6;
-        Box kept[kKept];
-#pragma unroll
-        for (int b = 0; b < kKept; ++b) kept[b] = b < tile.boxes ? boxes[32 * slot + b] : Box{};
-        int k = turn;
-        for (; k < a.steps; k += 2) {
-          if (!(ok = mbar_wait(empty + 8 * stage, phase ^ 1, a.err))) break;
-          const uint32_t data = sbase + stage * S::kStage, to = data + S::kBytesA, bar = map_rank(full + 8 * stage, 0);
-          const int k0 = k * (kMx ? 128 : 64);
-          if (leader) mbar_expect_tx(full + 8 * stage, 2 * S::kBytesA + tile.bytes);  // both CTAs', w and x
-          if constexpr (kSwiglu)
-            tma_tile5(data, &maps.w, k0, 0, 0, tile.block * 16 + (int)rank * 8, tile.expert, bar);
-          else
-            tma_tile3(data, &maps.w, k0, tile.block * kTileFeatures + (int)rank * 128, tile.expert, bar);
-#pragma unroll
-          for (int b = 0; b < kKept; ++b)
-            if (b < tile.boxes) tma_rows(to + kept[b].offset, &maps.x[kept[b].size], k0, kept[b].row, bar);
-          for (int b = kKept; b < tile.boxes; b += 4) {
-            Box q[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) q[u] = b + u < tile.boxes ? boxes[32 * slot + b + u] : Box{};
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-              if (b + u < tile.boxes) tma_rows(to + q[u].offset, &maps.x[q[u].size], k0, q[u].row, bar);
-          }
-          if ((stage += 2) >= a.stages) stage -= a.stages, phase ^= 1;
-        }
-        turn = k - a.steps;
-        mbar_arrive(plan_empty + 8 * slot);
-      }
-      // the ring drains: no product reads shared memory, and no arrival is under
-      // way to this CTA, once every stage has been handed back
-      for (int n = turn; n < a.stages && ok; n += 2) {
-        ok = mbar_wait(empty + 8 * stage, phase ^ 1, a.err);
-        if ((stage += 2) >= a.stages) stage -= a.stages, phase ^= 1;
-      }
-    }
+    if (elect_one())
+      load_tiles<S::kStage, S::kBytesA, kMx ? 128 : 64, kSwiglu>(a, maps, sbase, bars, tiles, boxes, warp == 3, rank, pair,
+                                                                 pairs, ntiles);
   } else if (warp == 1 && leader) {
     // ---- products: one thread -----------------------------------------------------
     if (elect_one()) {

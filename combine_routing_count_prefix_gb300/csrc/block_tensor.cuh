@@ -1,4 +1,4 @@
-// block_tensor.cuh -- the sm_103a instructions block_product.cu is written in:
+// block_tensor.cuh -- the sm_103a instructions the expert products are written in:
 // mbarriers across a CTA pair, TMA tile loads, tcgen05 products with
 // tensor-memory accumulators.  Thin wrappers, one instruction each.
 #pragma once
@@ -53,6 +53,11 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
 // fence_async_shared has made visible to it.
 __device__ __forceinline__ void mbar_arrive_peer(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// The same with what this thread wrote to the cluster's shared memory before it,
+// for a peer's thread that waits on the barrier.
+__device__ __forceinline__ void mbar_arrive_peer_release(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   uint32_t done;
@@ -139,6 +144,54 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// 32 columns of this warp's 32 lanes in four lanes at a time: with q = lane % 4 and
+// l = lane / 4, v[half][j][r] is lane 16 half + 8 (r / 2) + l, column 8 j + 2 q +
+// r % 2.  A thread holds pairs of neighbouring columns, and each column's value
+// for four lanes.
+__device__ __forceinline__ void tmem_load_pairs(uint32_t addr, uint32_t (&v)[2][4][4]) {
+#define LLMOE_REGS(h)                                                                                               \
+  "=r"(v[h][0][0]), "=r"(v[h][0][1]), "=r"(v[h][0][2]), "=r"(v[h][0][3]), "=r"(v[h][1][0]), "=r"(v[h][1][1]),        \
+      "=r"(v[h][1][2]), "=r"(v[h][1][3]), "=r"(v[h][2][0]), "=r"(v[h][2][1]), "=r"(v[h][2][2]), "=r"(v[h][2][3]),    \
+      "=r"(v[h][3][0]), "=r"(v[h][3][1]), "=r"(v[h][3][2]), "=r"(v[h][3][3])
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32"
+      " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%32];\n\t"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32"
+      " {%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%33];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : LLMOE_REGS(0), LLMOE_REGS(1)
+      : "r"(addr), "r"(addr + (16u << 16))
+      : "memory");
+#undef LLMOE_REGS
+}
+
+// Four 8 x 8 matrices of 16-bit values to shared memory, turned: this thread's
+// word of a matrix holds row lane / 4, columns 2 (lane % 4) and the next, and
+// lane 8 m + c gives the address where matrix m's column c goes, 16 bytes.
+__device__ __forceinline__ void store_turned(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared::cta.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+               "r"(c), "r"(d)
+               : "memory");
+}
+__device__ __forceinline__ uint4 shared_load16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared::cta.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void shared_store_peer(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// Registers of this warpgroup's threads from here on.
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // ---- products ------------------------------------------------------------------
 // Shared-memory descriptors, in two words: the upper is a constant, the lower
 // holds the address.  An operand tile is stored K-major in rows of 128 bytes with
@@ -155,6 +208,15 @@ __device__ __forceinline__ void mma_16bit(uint32_t d, uint32_t a, uint32_t b, ui
       "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\t"
       "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
       "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)add), "n"(kTileDescHigh)
+      : "memory");
+}
+// The same with e4m3 operands.
+__device__ __forceinline__ void mma_8bit(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %3, p;\n\t}" ::"r"(d),
       "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)add), "n"(kTileDescHigh)
       : "memory");
 }
