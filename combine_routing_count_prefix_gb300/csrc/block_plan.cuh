@@ -226,7 +226,7 @@ __device__ __forceinline__ Place find_tile(const ProductArgs& a, const int* pref
   return p;
 }
 
-template <int kMaxRows>
+template <int kMaxRows, bool kEven>
 __device__ void plan_tile(const ProductArgs& a, const int* prefix, int t, int rank, Buckets& b, Tile* tile, int* list,
                           Box* boxes) {
   const int lane = threadIdx.x & 31;
@@ -241,7 +241,8 @@ __device__ void plan_tile(const ProductArgs& a, const int* prefix, int t, int ra
   // last: 1040 rows are 4 x 224 + 144 columns, 1056 as padded (five equal
   // shares would pad to 1120).  shares is the fewest that hold the total, so the
   // last is never empty.
-  const int per = shares == 1 ? total : columns((total + shares - 1) / shares) / kGroup;
+  // (Not kEven: full shares and what is left.)
+  const int per = shares == 1 ? total : kEven ? columns((total + shares - 1) / shares) / kGroup : kMaxRows / kGroup;
   const int g0 = share * per, g1 = min(total, g0 + per);
   static_assert(kMaxRows % 32 == 0, "a share of at most kMaxRows rows pads to at most kMaxRows");
   plan_rows(a, e, g0, g1, b, list);
@@ -352,6 +353,136 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi, bool fp16) {
 // `at`, an address in row 0 of y, moved to `row`.
 __device__ __forceinline__ uint8_t* in_row(const ProductArgs& a, uint8_t* at, int row) {
   return at + (uint64_t)(uint32_t)row * a.y_row;
+}
+
+// 32 columns (rows of y) of 32 features: lane l holds feature first + l.
+// list: the columns' rows, -1 where nothing is stored (read before the stores,
+// which the compiler cannot tell from writes to it).
+__device__ __forceinline__ void store_plain(const ProductArgs& a, const float (&v)[32], int first, const int* list) {
+  const int lane = threadIdx.x & 31;
+  if (a.out_dtype == LLMOE_DTYPE_FP32) {
+    if (first + lane >= a.out) return;
+    uint8_t* at = a.y + (uint64_t)(first + lane) * 4;
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+      const int4 row = *reinterpret_cast<const int4*>(list + j);
+      if (row.x >= 0) *reinterpret_cast<float*>(in_row(a, at, row.x)) = v[j];
+      if (row.y >= 0) *reinterpret_cast<float*>(in_row(a, at, row.y)) = v[j + 1];
+      if (row.z >= 0) *reinterpret_cast<float*>(in_row(a, at, row.z)) = v[j + 2];
+      if (row.w >= 0) *reinterpret_cast<float*>(in_row(a, at, row.w)) = v[j + 3];
+    }
+    return;
+  }
+  // neighbours swap so that a lane holds two features of one column: even
+  // lanes the first column of a pair, odd lanes the second
+  const bool odd = lane & 1, fp16 = a.out_dtype == LLMOE_DTYPE_FP16;
+  const int feature = first + (lane & ~1);
+  const bool in = feature < a.out;
+  uint8_t* at = a.y + (uint64_t)feature * 2;
+  int row[16];
+#pragma unroll
+  for (int i = 0; i < 16; i += 2) {
+    const int4 r = *reinterpret_cast<const int4*>(list + 2 * i);
+    row[i] = odd ? r.y : r.x;
+    row[i + 1] = odd ? r.w : r.z;
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    // both columns of this lane's feature in one word: it keeps one half
+    const uint32_t mine = pack2(v[2 * i], v[2 * i + 1], fp16), got = __shfl_xor_sync(0xffffffffu, mine, 1);
+    const uint32_t u = __byte_perm(mine, got, odd ? 0x3276 : 0x5410);
+    if (in && row[i] >= 0) *reinterpret_cast<uint32_t*>(in_row(a, at, row[i])) = u;
+  }
+}
+
+// SwiGLU: 32 columns of 16 gate and 16 up features, eight of each in turn: lane l
+// holds gate (l & 8 == 0) or up of output feature first + l / 16 * 8 + l % 8.
+__device__ __forceinline__ int swiglu_feature(int first) {
+  const int lane = threadIdx.x & 31;
+  return first + (lane >> 4) * 8 + (lane & 7);
+}
+// Gate and up lanes swap, so that gate lanes end with h of even columns and up
+// lanes of odd ones: h[i] is column 2 i + up's.
+__device__ __forceinline__ void swiglu_columns(const float (&v)[32], float (&h)[16]) {
+  const bool up = threadIdx.x >> 3 & 1;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float got = __shfl_xor_sync(0xffffffffu, up ? v[2 * i] : v[2 * i + 1], 8);
+    h[i] = up ? near_silu(got) * v[2 * i + 1] : near_silu(v[2 * i]) * got;
+  }
+}
+
+// To rows of fp32, bf16 or fp16.
+__device__ __forceinline__ void store_swiglu_values(const ProductArgs& a, const float (&v)[32], int first,
+                                                    const int* list) {
+  const int lane = threadIdx.x & 31, up = lane >> 3 & 1, feature = swiglu_feature(first);
+  if (a.out_dtype == LLMOE_DTYPE_FP32) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float got = __shfl_xor_sync(0xffffffffu, up ? v[2 * i] : v[2 * i + 1], 8);
+      const float h = silu(up ? got : v[2 * i]) * (up ? v[2 * i + 1] : got);
+      const int row = list[2 * i + up];
+      if (row >= 0 && feature < a.out) *reinterpret_cast<float*>(in_row(a, a.y + (uint64_t)feature * 4, row)) = h;
+    }
+    return;
+  }
+  float h[16];
+  swiglu_columns(v, h);
+  const bool odd = lane & 1, fp16 = a.out_dtype == LLMOE_DTYPE_FP16;
+  const int even_feature = feature & ~1;
+  int row[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) row[i] = even_feature < a.out ? list[4 * i + 2 * odd + up] : -1;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t mine = pack2(h[2 * i], h[2 * i + 1], fp16), got = __shfl_xor_sync(0xffffffffu, mine, 1);
+    const uint32_t u = __byte_perm(mine, got, odd ? 0x3276 : 0x5410);
+    if (row[i] >= 0) *reinterpret_cast<uint32_t*>(in_row(a, a.y + (uint64_t)even_feature * 2, row[i])) = u;
+  }
+}
+
+// The largest magnitude of each column of the warp's 16 features: lanes of the
+// same columns halve the columns they keep at each of four exchanges, so that
+// lane at = 0..15 of them ends with column 2 at + up's.
+__device__ __forceinline__ uint32_t largest_of_columns(const float (&h)[16], int& at) {
+  const int lane = threadIdx.x & 31;
+  uint32_t m[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) m[i] = magnitude(h[i]);
+  at = 0;
+#pragma unroll
+  for (int step = 0; step < 4; ++step) {
+    const int d = step == 3 ? 16 : 1 << step, keep = 8 >> step;  // lane bits 0, 1, 2, 4
+    const bool high = lane & d;
+#pragma unroll
+    for (int i = 0; i < keep; ++i) {
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? m[i] : m[i + keep], d);
+      m[i] = max(high ? m[i + keep] : m[i], got);
+    }
+    at += high ? keep : 0;
+  }
+  return m[0];
+}
+
+// h as e4m3 codes; inverse[i]: 1 / scale of column 2 i + up.  Where any feature of
+// four is in y, all are (y's features are whole eights).
+__device__ __forceinline__ void store_codes(const ProductArgs& a, const float (&h)[16], const float (&inverse)[16],
+                                            int first, const int* list) {
+  const int lane = threadIdx.x & 31, up = lane >> 3 & 1, feature = swiglu_feature(first), q = lane & 3;
+  int row[4];
+#pragma unroll
+  for (int g = 0; g < 4; ++g) row[g] = feature < a.out ? list[2 * (4 * g + q) + up] : -1;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    // four columns of one feature, turned over four lanes into four features of one column
+    uint32_t b = pack_e4m3x2(h[4 * g] * inverse[4 * g], h[4 * g + 1] * inverse[4 * g + 1]) |
+                 pack_e4m3x2(h[4 * g + 2] * inverse[4 * g + 2], h[4 * g + 3] * inverse[4 * g + 3]) << 16;
+    uint32_t got = __shfl_xor_sync(0xffffffffu, b, 1);
+    b = __byte_perm(b, got, lane & 1 ? 0x3715 : 0x6240);
+    got = __shfl_xor_sync(0xffffffffu, b, 2);
+    b = __byte_perm(b, got, lane & 2 ? 0x3276 : 0x5410);
+    if (row[g] >= 0) *reinterpret_cast<uint32_t*>(in_row(a, a.y + (feature - q), row[g])) = b;
+  }
 }
 
 // ---------------------------------------------------------------------------

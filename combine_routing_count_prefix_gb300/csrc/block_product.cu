@@ -97,138 +97,41 @@ __host__ __device__ inline SmemLayout smem_layout(int stages, int E) {
 // ---------------------------------------------------------------------------
 // epilogue
 // ---------------------------------------------------------------------------
-// 32 columns (rows of y) of 32 features: lane l holds feature first + l.
-// list: the columns' rows, -1 where nothing is stored (read before the stores,
-// which the compiler cannot tell from writes to it).
-__device__ __forceinline__ void store_plain(const ProductArgs& a, const float (&v)[32], int first, const int* list) {
-  const int lane = threadIdx.x & 31;
-  if (a.out_dtype == LLMOE_DTYPE_FP32) {
-    if (first + lane >= a.out) return;
-    uint8_t* at = a.y + (uint64_t)(first + lane) * 4;
-#pragma unroll
-    for (int j = 0; j < 32; j += 4) {
-      const int4 row = *reinterpret_cast<const int4*>(list + j);
-      if (row.x >= 0) *reinterpret_cast<float*>(in_row(a, at, row.x)) = v[j];
-      if (row.y >= 0) *reinterpret_cast<float*>(in_row(a, at, row.y)) = v[j + 1];
-      if (row.z >= 0) *reinterpret_cast<float*>(in_row(a, at, row.z)) = v[j + 2];
-      if (row.w >= 0) *reinterpret_cast<float*>(in_row(a, at, row.w)) = v[j + 3];
-    }
-    return;
-  }
-  // neighbours swap so that a lane holds two features of one column: even
-  // lanes the first column of a pair, odd lanes the second
-  const bool odd = lane & 1, fp16 = a.out_dtype == LLMOE_DTYPE_FP16;
-  const int feature = first + (lane & ~1);
-  const bool in = feature < a.out;
-  uint8_t* at = a.y + (uint64_t)feature * 2;
-  int row[16];
-#pragma unroll
-  for (int i = 0; i < 16; i += 2) {
-    const int4 r = *reinterpret_cast<const int4*>(list + 2 * i);
-    row[i] = odd ? r.y : r.x;
-    row[i + 1] = odd ? r.w : r.z;
-  }
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    // both columns of this lane's feature in one word: it keeps one half
-    const uint32_t mine = pack2(v[2 * i], v[2 * i + 1], fp16), got = __shfl_xor_sync(0xffffffffu, mine, 1);
-    const uint32_t u = __byte_perm(mine, got, odd ? 0x3276 : 0x5410);
-    if (in && row[i] >= 0) *reinterpret_cast<uint32_t*>(in_row(a, at, row[i])) = u;
-  }
-}
-
-// 32 columns of 16 gate and 16 up features, eight of each in turn: lane l holds
-// gate (l & 8 == 0) or up of output feature first + l / 16 * 8 + l % 8.  The
-// two swap so that gate lanes end with h of even columns and up lanes of odd
-// ones.  MX8 output: amax is the exchange's buffer, bar its barrier, parity its
-// phase; false when the wait expired.
+// 32 columns of 16 gate and 16 up features (swiglu_columns).  MX8 output: amax is
+// the exchange's buffer, bar its barrier, parity its phase; false when the wait
+// expired.
 __device__ __forceinline__ bool store_swiglu(const ProductArgs& a, const float (&v)[32], int first, const int* list,
                                              uint32_t* amax, int warp, uint32_t bar, uint32_t parity) {
   const int lane = threadIdx.x & 31, up = lane >> 3 & 1;
-  const int feature = first + (lane >> 4) * 8 + (lane & 7);
-  if (a.out_dtype == LLMOE_DTYPE_FP32) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float got = __shfl_xor_sync(0xffffffffu, up ? v[2 * i] : v[2 * i + 1], 8);
-      const float h = silu(up ? got : v[2 * i]) * (up ? v[2 * i + 1] : got);
-      const int row = list[2 * i + up];
-      if (row >= 0 && feature < a.out) *reinterpret_cast<float*>(in_row(a, a.y + (uint64_t)feature * 4, row)) = h;
-    }
+  if (a.out_dtype != LLMOE_DTYPE_MX8) {
+    store_swiglu_values(a, v, first, list);
     return true;
   }
+  // a group of 32 outputs is this warp's 16 and its neighbour's: the two swap
+  // their largest magnitudes through shared memory
   float h[16];
+  swiglu_columns(v, h);
+  int at;
+  const uint32_t most = largest_of_columns(h, at);
+  amax[warp * 32 + up * 16 + at] = most;
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+  if (!mbar_wait_warp(bar, parity, a.err)) return false;
+  uint32_t mine = 0;  // the scale code of column 2 at + up
+  float inverse[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    const float got = __shfl_xor_sync(0xffffffffu, up ? v[2 * i] : v[2 * i + 1], 8);
-    h[i] = up ? near_silu(got) * v[2 * i + 1] : near_silu(v[2 * i]) * got;
+    const uint32_t code = scale_code(max(amax[warp * 32 + up * 16 + i], amax[(warp ^ 1) * 32 + up * 16 + i]));
+    if (i == at) mine = code;
+    inverse[i] = scale_inverse(code);
   }
-  if (a.out_dtype == LLMOE_DTYPE_MX8) {
-    // a group of 32 outputs is this warp's 16 and its neighbour's.  The largest
-    // magnitudes: lanes of the same columns halve the columns they keep at each
-    // of four exchanges, so that lane at = 0..15 of them ends with column
-    // 2 at + up's, and the two warps swap through shared memory
-    uint32_t m[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) m[i] = magnitude(h[i]);
-    int at = 0;
-#pragma unroll
-    for (int step = 0; step < 4; ++step) {
-      const int d = step == 3 ? 16 : 1 << step, keep = 8 >> step;  // lane bits 0, 1, 2, 4
-      const bool high = lane & d;
-#pragma unroll
-      for (int i = 0; i < keep; ++i) {
-        const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? m[i] : m[i + keep], d);
-        m[i] = max(high ? m[i + keep] : m[i], got);
-      }
-      at += high ? keep : 0;
-    }
-    amax[warp * 32 + up * 16 + at] = m[0];
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar);
-    if (!mbar_wait_warp(bar, parity, a.err)) return false;
-    uint32_t mine = 0;  // the scale code of column 2 at + up
-    uint32_t code[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      code[i] = scale_code(max(amax[warp * 32 + up * 16 + i], amax[(warp ^ 1) * 32 + up * 16 + i]));
-      if (i == at) mine = code[i];
-    }
-    const bool store = feature < a.out;  // whole groups: out is a multiple of 32
-    const int q = lane & 3;
-    int row[4];
-#pragma unroll
-    for (int g = 0; g < 4; ++g) row[g] = store ? list[2 * (4 * g + q) + up] : -1;
-    const int my_row = store && !(warp & 1) ? list[2 * at + up] : -1;
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      // four columns of one feature, turned over four lanes into four features of one column
-      uint32_t b = pack_e4m3x2(h[4 * g] * scale_inverse(code[4 * g]), h[4 * g + 1] * scale_inverse(code[4 * g + 1])) |
-                   pack_e4m3x2(h[4 * g + 2] * scale_inverse(code[4 * g + 2]),
-                               h[4 * g + 3] * scale_inverse(code[4 * g + 3])) << 16;
-      uint32_t got = __shfl_xor_sync(0xffffffffu, b, 1);
-      b = __byte_perm(b, got, lane & 1 ? 0x3715 : 0x6240);
-      got = __shfl_xor_sync(0xffffffffu, b, 2);
-      b = __byte_perm(b, got, lane & 2 ? 0x3276 : 0x5410);
-      if (row[g] >= 0) *reinterpret_cast<uint32_t*>(in_row(a, a.y + (feature - q), row[g])) = b;
-    }
-    if (my_row >= 0) {
-      uint8_t* s = in_row(a, a.y + a.out + first / 32, my_row);
-      *s = (uint8_t)mine;
-      if (first + 32 == a.out)
-        for (uint8_t* end = in_row(a, a.y + a.y_row, my_row); ++s < end;) *s = 0;
-    }
-    return true;
-  }
-  const bool odd = lane & 1, fp16 = a.out_dtype == LLMOE_DTYPE_FP16;
-  const int even_feature = feature & ~1;
-  int row[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) row[i] = even_feature < a.out ? list[4 * i + 2 * odd + up] : -1;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t mine = pack2(h[2 * i], h[2 * i + 1], fp16), got = __shfl_xor_sync(0xffffffffu, mine, 1);
-    const uint32_t u = __byte_perm(mine, got, odd ? 0x3276 : 0x5410);
-    if (row[i] >= 0) *reinterpret_cast<uint32_t*>(in_row(a, a.y + (uint64_t)even_feature * 2, row[i])) = u;
+  store_codes(a, h, inverse, first, list);
+  const int my_row = swiglu_feature(first) < a.out && !(warp & 1) ? list[2 * at + up] : -1;
+  if (my_row >= 0) {
+    uint8_t* s = in_row(a, a.y + a.out + first / 32, my_row);
+    *s = (uint8_t)mine;
+    if (first + 32 == a.out)
+      for (uint8_t* end = in_row(a, a.y + a.y_row, my_row); ++s < end;) *s = 0;
   }
   return true;
 }
@@ -380,7 +283,7 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
     for (int t = pair; t < ntiles; t += pairs, ++i) {
       const int slot = i % kPlanDepth;
       if (!mbar_wait_warp(plan_empty + 8 * slot, ((i / kPlanDepth) & 1) ^ 1, a.err)) break;
-      plan_tile<S::kMaxRows>(a, prefix, t, (int)rank, buckets, tiles + slot, rows + slot * S::kMaxRows, boxes + 32 * slot);
+      plan_tile<S::kMaxRows, true>(a, prefix, t, (int)rank, buckets, tiles + slot, rows + slot * S::kMaxRows, boxes + 32 * slot);
       __syncwarp();
       if (lane == 0) mbar_arrive(plan_full + 8 * slot);
     }

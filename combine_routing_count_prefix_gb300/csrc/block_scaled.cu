@@ -1,38 +1,46 @@
 // block_scaled.cu -- llmoe_expert_product_fp8b (include/llmoe_block.h): matrix
 // products grouped by expert over received FP8B rows.
 //
-// Tiles, plan, ring and pairs are block_product.cu's: the weights on the M side,
-// 256 features to a pair of CTAs, up to kMaxRows received rows on the N side.
+// Ring, plan and pairs of CTAs are block_product.cu's: a tile is 256 features and
+// up to kMaxRows received rows, 128 features and half of the rows in each CTA.
 // What differs is where the sums live.  A block's scales are fp32, so the tensor
 // core cannot apply them: it makes the sums of one block of 128 (one step of the
-// ring, four instructions) in one of two buffers of tensor memory, and eight warps
-// add them, times their scales, to sums that they hold in registers:
+// ring, four instructions) in one of two to four buffers of tensor memory, and
+// eight warps add them, times their scales, to sums that they hold in registers:
 //   acc[f][r] += P[f][r] * (s[r] * ws),
-// 128 values a thread for a full tile.  ws is one number for a CTA's 128 features
-// (two with SwiGLU, gate and up), s one for a column.  A warp reads tensor memory
-// so that a thread holds pairs of neighbouring columns of four features each: a
-// pair's two scales are one 8-byte load for four packed multiply-adds.
+// s a row's scale, ws one number for a CTA's 128 features (with SwiGLU one for its
+// gate and one for its up features).  Tiles come in two kinds:
+//   wide (more than kNarrowRows rows): the rows on the M side, the features on the
+//     N side.  A thread of the eight warps is one row and 128 features: it needs one
+//     scale a step (two with SwiGLU), and has a row's features side by side.
+//   narrow: the features on the M side, up to 128 rows on the N side, so that few
+//     rows cost few columns.  A thread is one feature and up to 64 rows, whose s * ws
+//     it reads four at a time.
+// The operands in shared memory are the same for both; only the roles differ.
 //
 // Inside a CTA of 16 warps:
 //   warps 0, 3  load (warp 3 also allocates the tensor memory)
 //   warp 1      (first CTA of the pair) issues the products
 //   warp 2      plans
 //   warps 4-11  sums, then the tile's epilogue
-//   warps 12-15 move the scales of x's rows (times ws without SwiGLU) and of w to
-//               shared memory, four steps at a time
+//   warps 12-15 bring the scales to shared memory, four steps at a time
 // The eight warps have kManyRegisters registers a thread, the others kFewRegisters.
 // Every wait is bounded, as there.
 #include "block_plan.cuh"
 
 namespace {
 
-constexpr int kMaxRows = 256, kThreads = 512;
+constexpr int kMaxRows = 256, kNarrowRows = 128, kThreads = 512;
 constexpr int kBytesA = 128 * 128, kBytesB = kMaxRows / 2 * 128, kStage = kBytesA + kBytesB;
 constexpr int kManyRegisters = 200, kFewRegisters = 56;
 static_assert(256 * (kManyRegisters + kFewRegisters) <= 65536, "what a launch of 512 threads has");
-constexpr int kSlots = 3;                      // of scales, four steps each
-constexpr int kSlot = 4 * kMaxRows * 4;        // bytes of a slot's row scales
-constexpr int kChunks = kMaxRows / 64;         // of 32 columns, for each set of four warps
+constexpr int kBuffers = 4;  // of tensor memory: 4 of 128 columns for narrow tiles, 2 of 256 for wide ones
+constexpr int kSlots = 2;    // of scales, four steps each
+// A slot: a wide tile's row scales [step][row]; a narrow one's products [step][gate,
+// up][row], the up ones 16 bytes further so that a warp's loads of both do not meet in a bank
+constexpr int kNarrowStride = kNarrowRows + 4;
+constexpr int kSlot = 4 * 2 * kNarrowStride * 4;
+static_assert(2 * kNarrowStride >= kMaxRows, "wide tiles fit too");
 
 struct ScaledArgs {
   ProductArgs p;
@@ -42,20 +50,20 @@ struct ScaledArgs {
 
 // Byte offsets in dynamic shared memory, from its first 1024-byte boundary.
 struct ScaledSmem {
-  uint32_t scales, w_scales, turn, codes, boxes, rows, tiles, bars, tmem, part, prefix, total;
+  uint32_t scales, w_scales, turn, amax, row_max, boxes, rows, tiles, bars, tmem, part, prefix, total;
 };
 __host__ __device__ inline ScaledSmem scaled_smem(int stages, int E) {
   ScaledSmem l;
   uint32_t at = stages * kStage;
   l.scales = at, at += kSlots * kSlot;
   l.w_scales = at, at += kSlots * 4 * 2 * 4;
-  at = (at + 127) / 128 * 128;
-  l.turn = at, at += 8 * kMaxRows * 4;  // 1 KB a warp to turn outputs in, or the largest magnitudes of eight warps
-  l.codes = at, at += 8 * 512;  // a warp's 32 columns of 16 codes
+  l.turn = at, at += 8 * 1024;              // for each warp, 32 bytes of 32 rows
+  l.amax = at, at += 8 * kNarrowRows * 4;   // narrow: [warp of the pair's set][row]
+  l.row_max = at, at += 2 * 2 * 128 * 4;    // wide: [tile's parity][set][row]
   l.boxes = at, at += kPlanDepth * 32 * 16;
   l.rows = at, at += kPlanDepth * kMaxRows * 4;
   l.tiles = at, at += kPlanDepth * (uint32_t)sizeof(Tile);
-  l.bars = at, at += (2 * kStages + 4 + 2 * kPlanDepth + 2 * kSlots + 4) * 8;
+  l.bars = at, at += (2 * kStages + 2 * kBuffers + 2 * kPlanDepth + 2 * kSlots + 4 + 4) * 8;
   l.tmem = at, at += 16;
   l.part = at, at += 64;
   l.prefix = at, at += (E + 1) * 4;
@@ -63,155 +71,114 @@ __host__ __device__ inline ScaledSmem scaled_smem(int stages, int E) {
   return l;
 }
 
-// One thread's sums of 32 columns: [half][j][features l / + 8], columns 8 j + 2 q
-// and the next (tmem_load_pairs).
-using Sums = Pair[2][4][2];
-
-// ---------------------------------------------------------------------------
-// epilogue: 32 columns of a warp's 32 lanes; turn: 1 KB of the warp's own
-// ---------------------------------------------------------------------------
-__device__ __forceinline__ void store_plain(const ProductArgs& a, const Sums& acc, int first, const int* list,
-                                            uint32_t turn) {
-  const int lane = threadIdx.x & 31, l = lane >> 2, q = lane & 3;
-  if (a.out_dtype == LLMOE_DTYPE_FP32) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int2 row = *reinterpret_cast<const int2*>(list + 8 * j + 2 * q);
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const float2 v = unpair(acc[b >> 1][j][b & 1]);
-        const int feature = first + 8 * b + l;
-        if (feature >= a.out) continue;
-        uint8_t* at = a.y + (uint64_t)feature * 4;
-        if (row.x >= 0) *reinterpret_cast<float*>(in_row(a, at, row.x)) = v.x;
-        if (row.y >= 0) *reinterpret_cast<float*>(in_row(a, at, row.y)) = v.y;
-      }
-    }
-    return;
+// The buffer of tensor memory that a step uses, and its barriers' phase: the
+// issuing thread and the summing warps go through the same sequence.  Where the
+// kind of tile changes, so do the buffers.
+struct Buffers {
+  uint32_t phases = 0;  // a bit each
+  int next = 0;
+  bool wide = false;
+  __device__ __forceinline__ bool change(bool w) {
+    if (w == wide) return false;
+    wide = w, next = 0;
+    return true;
   }
-  // 8 columns of 32 features at a time: 64 bytes a column, its 16-byte pieces
-  // placed so that neither the turned stores nor the loads meet in a bank
-  const bool fp16 = a.out_dtype == LLMOE_DTYPE_FP16;
-  const uint32_t put = turn + (lane & 7) * 64 + (((lane >> 3) ^ (lane >> 1 & 3)) << 4);
-  const uint32_t get = turn + l * 64 + ((q ^ (l >> 1 & 3)) << 4);
-  const int feature = first + 8 * q;
+  __device__ __forceinline__ uint32_t phase() const { return phases >> next & 1; }
+  __device__ __forceinline__ uint32_t column() const { return (uint32_t)next * (wide ? 256 : 128); }
+  __device__ __forceinline__ void advance() {
+    phases ^= 1u << next;
+    next = (next + 1) & (wide ? 1 : kBuffers - 1);
+  }
+};
+__device__ __forceinline__ bool is_wide(const Tile& t) { return t.groups > kNarrowRows / kGroup; }
+
+__device__ __forceinline__ void unpair(const Pair (&p)[16], float (&v)[32]) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    uint32_t u[4];
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const float2 v = unpair(acc[b >> 1][j][b & 1]);
-      u[b] = pack2(v.x, v.y, fp16);
-    }
-    store_turned(put + (j & 1) * 512, u[0], u[1], u[2], u[3]);
-    __syncwarp();  // and the buffer's use before the last one is over
-    const uint4 v = shared_load16(get + (j & 1) * 512);
-    const int row = list[8 * j + l];
-    if (row >= 0 && feature < a.out) *reinterpret_cast<uint4*>(in_row(a, a.y + (uint64_t)feature * 2, row)) = v;
+  for (int i = 0; i < 16; ++i) {
+    const float2 f = unpair(p[i]);
+    v[2 * i] = f.x, v[2 * i + 1] = f.y;
   }
 }
 
-// Lanes 0-7 and 16-23 of a warp are gate features, the others up; h of 16
-// features, 8 half + l, in place of the gate's sums.
-template <bool kAccurate>
-__device__ __forceinline__ void swiglu(Sums& acc) {
+// ---------------------------------------------------------------------------
+// narrow tiles: lane = feature, 32 rows in a chunk
+// ---------------------------------------------------------------------------
+// acc += v * scale
+__device__ __forceinline__ void add_rows(const uint32_t (&v)[32], const float* scale, Pair (&acc)[16]) {
 #pragma unroll
-  for (int half = 0; half < 2; ++half)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 g = unpair(acc[half][j][0]), u = unpair(acc[half][j][1]);
-      acc[half][j][0] = kAccurate ? pair(silu(g.x) * u.x, silu(g.y) * u.y) : pair(near_silu(g.x) * u.x, near_silu(g.y) * u.y);
-    }
+  for (int j = 0; j < 8; ++j) {
+    const float4 f = *reinterpret_cast<const float4*>(scale + 4 * j);
+    acc[2 * j] = fma2(pair(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1])), pair(f.x, f.y), acc[2 * j]);
+    acc[2 * j + 1] = fma2(pair(__uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3])), pair(f.z, f.w), acc[2 * j + 1]);
+  }
 }
 
-__device__ __forceinline__ void store_swiglu(const ProductArgs& a, const Sums& acc, int first, const int* list,
-                                             uint32_t turn) {
-  const int lane = threadIdx.x & 31, l = lane >> 2, q = lane & 3;
-  if (a.out_dtype == LLMOE_DTYPE_FP32) {
+// ---------------------------------------------------------------------------
+// wide tiles: lane = row, 32 features in a chunk
+// ---------------------------------------------------------------------------
+// acc += v * scale; with SwiGLU the features are eight of gate, eight of up in turn.
+template <bool kSwiglu>
+__device__ __forceinline__ void add_features(const uint32_t (&v)[32], Pair gate, Pair up, Pair (&acc)[16]) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int2 row = *reinterpret_cast<const int2*>(list + 8 * j + 2 * q);
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const float2 v = unpair(acc[half][j][0]);
-        const int feature = first + 8 * half + l;
-        if (feature >= a.out) continue;
-        uint8_t* at = a.y + (uint64_t)feature * 4;
-        if (row.x >= 0) *reinterpret_cast<float*>(in_row(a, at, row.x)) = v.x;
-        if (row.y >= 0) *reinterpret_cast<float*>(in_row(a, at, row.y)) = v.y;
-      }
-    }
-    return;
-  }
-  // 16 columns of 16 features at a time, 32 bytes a column
-  const bool fp16 = a.out_dtype == LLMOE_DTYPE_FP16;
-  const uint32_t put = turn + ((lane >> 4) * 8 + (lane & 7)) * 32 + (((lane >> 3 & 1) ^ (lane >> 2 & 1)) << 4);
-  const uint32_t get = turn + (lane >> 1) * 32 + (((lane & 1) ^ (lane >> 3 & 1)) << 4);
-  const int feature = first + 8 * (lane & 1);
+  for (int i = 0; i < 16; ++i)
+    acc[i] = fma2(pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), kSwiglu && (i & 4) ? up : gate, acc[i]);
+}
+
+// 32 bytes of each lane's row to y, `at` bytes into the row: turned through the
+// warp's 1 KB of shared memory, so that two lanes store a row's 32 bytes.
+__device__ __forceinline__ void store_pieces(const ProductArgs& a, const uint4& first, const uint4& second, int row,
+                                             uint32_t at, uint32_t end, uint32_t turn) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t swap = lane >> 2 & 1;
+  shared_store16(turn + lane * 32 + (swap << 4), first);
+  shared_store16(turn + lane * 32 + ((swap ^ 1) << 4), second);
+  __syncwarp();
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    uint32_t u[4];
+    const int from = 16 * i + (lane >> 1), piece = lane & 1;
+    const uint4 v = shared_load16(turn + from * 32 + ((piece ^ (from >> 2 & 1)) << 4));
+    const int to = __shfl_sync(0xffffffffu, row, from);
+    if (to >= 0 && at + 16 * piece < end) *reinterpret_cast<uint4*>(in_row(a, a.y + at + 16 * piece, to)) = v;
+  }
+  __syncwarp();  // read, before the next pieces are written
+}
+
+// N values of the lane's row from feature `first` on, to fp32, bf16 or fp16 (N: 16 or 32).
+template <int N>
+__device__ __forceinline__ void store_values(const ProductArgs& a, const float (&v)[N], int first, int row, uint32_t turn) {
+  if (a.out_dtype == LLMOE_DTYPE_FP32) {
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      const float2 v = unpair(acc[m & 1][2 * i + (m >> 1)][0]);
-      u[m] = pack2(v.x, v.y, fp16);
+    for (int i = 0; i < N; i += 8) {
+      uint4 q[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        q[u] = make_uint4(__float_as_uint(v[i + 4 * u]), __float_as_uint(v[i + 4 * u + 1]), __float_as_uint(v[i + 4 * u + 2]),
+                          __float_as_uint(v[i + 4 * u + 3]));
+      store_pieces(a, q[0], q[1], row, (uint32_t)(first + i) * 4, (uint32_t)a.out * 4, turn);
     }
-    store_turned(put + i * 512, u[0], u[1], u[2], u[3]);
-    __syncwarp();
-    const uint4 v = shared_load16(get + i * 512);
-    const int row = list[16 * i + (lane >> 1)];
-    if (row >= 0 && feature < a.out) *reinterpret_cast<uint4*>(in_row(a, a.y + (uint64_t)feature * 2, row)) = v;
+    return;
+  }
+  const bool fp16 = a.out_dtype == LLMOE_DTYPE_FP16;
+#pragma unroll
+  for (int i = 0; i < N; i += 16) {
+    uint4 q[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      q[u] = make_uint4(pack2(v[i + 8 * u], v[i + 8 * u + 1], fp16), pack2(v[i + 8 * u + 2], v[i + 8 * u + 3], fp16),
+                        pack2(v[i + 8 * u + 4], v[i + 8 * u + 5], fp16), pack2(v[i + 8 * u + 6], v[i + 8 * u + 7], fp16));
+    store_pieces(a, q[0], q[1], row, (uint32_t)(first + i) * 2, (uint32_t)a.out * 2, turn);
   }
 }
 
-// Largest magnitude of the warp's 16 features of h in each of 32 columns: lane's
-// column is the one returned in `column`.
-__device__ __forceinline__ uint32_t largest(const Sums& acc, int& column) {
-  const int lane = threadIdx.x & 31;
-  uint32_t m[8];  // columns 8 j + 2 q + i as 2 j + i
+// h of a chunk's 16 features.
+template <bool kAccurate>
+__device__ __forceinline__ void swiglu_row(const Pair (&acc)[16], float (&h)[16]) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float2 a = unpair(acc[0][j][0]), b = unpair(acc[1][j][0]);
-    m[2 * j] = max(magnitude(a.x), magnitude(b.x));
-    m[2 * j + 1] = max(magnitude(a.y), magnitude(b.y));
+  for (int i = 0; i < 8; ++i) {
+    const float2 g = unpair(acc[i / 4 * 8 + i % 4]), u = unpair(acc[i / 4 * 8 + 4 + i % 4]);
+    h[2 * i] = (kAccurate ? silu(g.x) : near_silu(g.x)) * u.x;
+    h[2 * i + 1] = (kAccurate ? silu(g.y) : near_silu(g.y)) * u.y;
   }
-  // lanes of the same q halve the columns they keep at each of three exchanges
-  int at = 0;
-#pragma unroll
-  for (int step = 0; step < 3; ++step) {
-    const int d = 4 << step, keep = 4 >> step;
-    const bool high = lane & d;
-#pragma unroll
-    for (int i = 0; i < keep; ++i) {
-      const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? m[i] : m[i + keep], d);
-      m[i] = max(high ? m[i + keep] : m[i], got);
-    }
-    at += high ? keep : 0;
-  }
-  column = 8 * (at >> 1) + 2 * (lane & 3) + (at & 1);
-  return m[0];
-}
-
-// Codes of 32 columns; inv: of column `lane`.
-__device__ __forceinline__ void store_codes(const ProductArgs& a, const Sums& acc, int first, const int* list, float inv,
-                                            uint32_t turn) {
-  const int lane = threadIdx.x & 31, q = lane & 3;
-  uint32_t u[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const Pair i2 = pair(__shfl_sync(0xffffffffu, inv, 8 * j + 2 * q), __shfl_sync(0xffffffffu, inv, 8 * j + 2 * q + 1));
-    const float2 lo = unpair(mul2(acc[0][j][0], i2)), hi = unpair(mul2(acc[1][j][0], i2));
-    u[j] = pack_e4m3x2(lo.x, hi.x) | pack_e4m3x2(lo.y, hi.y) << 16;  // a 16-bit value: features l and 8 + l
-  }
-  store_turned(turn + lane * 16, u[0], u[1], u[2], u[3]);
-  __syncwarp();
-  const uint4 v = shared_load16(turn + lane * 16);
-  __syncwarp();  // read, before the next columns' are stored
-  const int row = list[lane];
-  if (row >= 0 && first < a.out)
-    *reinterpret_cast<uint4*>(in_row(a, a.y + first, row)) =
-        make_uint4(__byte_perm(v.x, v.y, 0x6420), __byte_perm(v.z, v.w, 0x6420), __byte_perm(v.x, v.y, 0x7531),
-                   __byte_perm(v.z, v.w, 0x7531));
 }
 
 // ---------------------------------------------------------------------------
@@ -235,9 +202,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   Tile* tiles = reinterpret_cast<Tile*>(smem + l.tiles);
   int* prefix = reinterpret_cast<int*>(smem + l.prefix);
   const uint32_t full = sbase + l.bars, empty = full + 8 * kStages, acc_full = empty + 8 * kStages,
-                 acc_empty = acc_full + 16, plan_full = acc_empty + 16, plan_empty = plan_full + 8 * kPlanDepth,
-                 scale_full = plan_empty + 8 * kPlanDepth, scale_empty = scale_full + 8 * kSlots,
-                 amax_full = scale_empty + 8 * kSlots, amax_empty = amax_full + 16;
+                 acc_empty = acc_full + 8 * kBuffers, plan_full = acc_empty + 8 * kBuffers,
+                 plan_empty = plan_full + 8 * kPlanDepth, scale_full = plan_empty + 8 * kPlanDepth,
+                 scale_empty = scale_full + 8 * kSlots, amax_full = scale_empty + 8 * kSlots, amax_empty = amax_full + 16,
+                 row_full = amax_empty + 16;
 
   if (threadIdx.x == 0) {
     tma_prefetch_map(&maps.w);
@@ -245,16 +213,19 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       mbar_init(full + 8 * i, 1);
       mbar_init(empty + 8 * i, 1);
     }
+    for (int i = 0; i < kBuffers; ++i) {
+      mbar_init(acc_full + 8 * i, 1);
+      mbar_init(acc_empty + 8 * i, 16);  // the summing warps of both CTAs
+    }
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(scale_full + 8 * i, 4);
       mbar_init(scale_empty + 8 * i, 8);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(acc_full + 8 * i, 1);
-      mbar_init(acc_empty + 8 * i, 16);  // the summing warps of both CTAs
-      mbar_init(amax_full + 8 * i, 8);   // a set's warps of both CTAs
+      mbar_init(amax_full + 8 * i, 8);  // a set's warps of both CTAs
       mbar_init(amax_empty + 8 * i, 8);
     }
+    for (int i = 0; i < 4; ++i) mbar_init(row_full + 8 * i, 2);  // the two warps of 32 rows
     for (int i = 0; i < kPlanDepth; ++i) {
       mbar_init(plan_full + 8 * i, 1);
       mbar_init(plan_empty + 8 * i, 14 + (leader ? 1 : 0));  // warps that read a plan
@@ -284,24 +255,31 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       // ---- products: one thread -----------------------------------------------------
       if (leader && elect_one()) {
         int stage = 0, i = 0;
-        uint32_t phase = 0, step = 0;  // step: over all tiles, two buffers in turn
+        uint32_t phase = 0;
+        Buffers buffers;
         bool ok = true;
         const uint32_t desc = tile_desc(sbase);
         for (int t = pair_id; t < ntiles && ok; t += pairs, ++i) {
           const int slot = i % kPlanDepth;
-          if (!(ok = mbar_wait(plan_full + 8 * slot, (i / kPlanDepth) & 1, a.err))) break;
-          const uint32_t idesc = a.idesc | (uint32_t)(columns(tiles[slot].groups) >> 3) << 17;
+          if (!(ok = mbar_wait_cta(plan_full + 8 * slot, (i / kPlanDepth) & 1, a.err))) break;
+          const bool wide = is_wide(tiles[slot]);
+          const uint32_t n = wide ? kTileFeatures : columns(tiles[slot].groups), idesc = a.idesc | (n >> 3) << 17;
           mbar_arrive(plan_empty + 8 * slot);
-          for (int k = 0; k < a.steps; ++k, ++step) {
-            const uint32_t buf = step & 1, d = tmem + buf * kMaxRows;
-            const uint32_t da = desc + (uint32_t)(stage * (kStage >> 4)), db = da + (kBytesA >> 4);
-            if (!(ok = mbar_wait(acc_empty + 8 * buf, (step >> 1 & 1) ^ 1, a.err))) break;
-            if (!(ok = mbar_wait(full + 8 * stage, phase, a.err))) break;
+          if (buffers.change(wide))  // other columns: every buffer has to be handed back
+            for (int b = 0; b < kBuffers && ok; ++b)
+              ok = mbar_wait_cta(acc_empty + 8 * b, (buffers.phases >> b & 1) ^ 1, a.err);
+          for (int k = 0; k < a.steps && ok; ++k) {
+            const uint32_t w = desc + (uint32_t)(stage * (kStage >> 4)), x = w + (kBytesA >> 4);
+            const uint32_t m_side = wide ? x : w, n_side = wide ? w : x;
+            if (!(ok = mbar_wait_cta(acc_empty + 8 * buffers.next, buffers.phase() ^ 1, a.err))) break;
+            if (!(ok = mbar_wait_cta(full + 8 * stage, phase, a.err))) break;
             tc_fence_after();
 #pragma unroll
-            for (int j = 0; j < 4; ++j) mma_8bit(d, da + 2 * j, db + 2 * j, idesc, j > 0);
+            for (int j = 0; j < 4; ++j)
+              mma_8bit(tmem + buffers.column(), m_side + 2 * j, n_side + 2 * j, idesc, j > 0);
+            mma_commit_pair(acc_full + 8 * buffers.next);
             mma_commit_pair(empty + 8 * stage);
-            mma_commit_pair(acc_full + 8 * buf);
+            buffers.advance();
             if (++stage == a.stages) stage = 0, phase ^= 1;
           }
         }
@@ -313,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       for (int t = pair_id; t < ntiles; t += pairs, ++i) {
         const int slot = i % kPlanDepth;
         if (!mbar_wait_warp(plan_empty + 8 * slot, ((i / kPlanDepth) & 1) ^ 1, a.err)) break;
-        plan_tile<kMaxRows>(a, prefix, t, (int)rank, buckets, tiles + slot, rows + slot * kMaxRows, boxes + 32 * slot);
+        plan_tile<kMaxRows, false>(a, prefix, t, (int)rank, buckets, tiles + slot, rows + slot * kMaxRows, boxes + 32 * slot);
         __syncwarp();
         if (lane == 0) mbar_arrive(plan_full + 8 * slot);
       }
@@ -321,109 +299,210 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   } else if (warp < 12) {
     more_registers<kManyRegisters>();
     // ---- sums and epilogue ---------------------------------------------------------
-    // two sets of four warps, each taking every other 32 columns
-    const int w = warp & 3, set = warp >= 8;  // tensor-memory lanes 32 w ..
-    const uint32_t turn = sbase + l.turn + (warp - 4) * 1024;
-    uint32_t* amax = reinterpret_cast<uint32_t*>(smem + l.turn);  // [warp of the pair's set][column]
-    const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16) + 32 * set;
+    // two sets of four warps, warp w of each on tensor-memory lanes 32 w ..
+    const int w = warp & 3, set = warp >= 8;
+    const uint32_t turn = sbase + l.turn + (warp - 4) * 1024, lanes = tmem + ((uint32_t)(32 * w) << 16);
     const uint32_t leader_empty = map_rank(acc_empty, 0);
-    int i = 0, sslot = 0;
-    uint32_t step = 0, sphase = 0;
+    int i = 0, sslot = 0, narrow_tiles = 0, wide_tiles = 0;
+    uint32_t sphase = 0;
+    Buffers buffers;
     bool ok = true;
+    // a step's scales and sums are there: the scales' place
+    const auto arrive = [&](int k) -> const float* {
+      if ((k & 3) == 0 && !(ok = mbar_wait_cta_warp(scale_full + 8 * sslot, sphase, a.err))) return nullptr;
+      if (!(ok = mbar_wait_cta_warp(acc_full + 8 * buffers.next, buffers.phase(), a.err))) return nullptr;
+      tc_fence_after();
+      return reinterpret_cast<const float*>(smem + l.scales + sslot * kSlot);
+    };
+    // this warp has read the step's sums
+    const auto release = [&] {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_peer(leader_empty + 8 * buffers.next);
+    };
+    const auto leave = [&](int k) {
+      buffers.advance();
+      if ((k & 3) == 3 || k + 1 == a.steps) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(scale_empty + 8 * sslot);
+        if (++sslot == kSlots) sslot = 0, sphase ^= 1;
+      }
+    };
     for (int t = pair_id; t < ntiles && ok; t += pairs, ++i) {
       const int slot = i % kPlanDepth;
-      if (!(ok = mbar_wait_warp(plan_full + 8 * slot, (i / kPlanDepth) & 1, a.err))) break;
+      if (!(ok = mbar_wait_cta_warp(plan_full + 8 * slot, (i / kPlanDepth) & 1, a.err))) break;
       const Tile tile = tiles[slot];
-      const int chunks = (columns(tile.groups) / 32 + 1 - set) / 2;
-      Sums acc[kChunks];
+      const int* list = rows + slot * kMaxRows;
+      const bool wide = is_wide(tile);
+      buffers.change(wide);
+      if (wide) {
+        // set: which CTA's 128 features.  Rows: the pair's halves of the list.
+        const int half = columns(tile.groups) / 2, index = (int)rank * half + 32 * w + lane;
+        const bool some = 32 * w < half;
+        constexpr int kChunks = 4;
+        Pair acc[kChunks][16];
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c)
+        for (int c = 0; c < kChunks; ++c)
 #pragma unroll
-        for (int h = 0; h < 16; ++h) acc[c][h >> 3][h >> 1 & 3][h & 1] = 0;
-      for (int k = 0; k < a.steps; ++k, ++step) {
-        const uint32_t buf = step & 1;
-        if ((k & 3) == 0 && !(ok = mbar_wait_warp(scale_full + 8 * sslot, sphase, a.err))) break;
-        if (!(ok = mbar_wait_warp(acc_full + 8 * buf, step >> 1 & 1, a.err))) break;
-        tc_fence_after();
-        const float* sx = reinterpret_cast<const float*>(smem + l.scales + sslot * kSlot) + (k & 3) * kMaxRows + 32 * set +
-                          2 * (lane & 3);
-        Pair wg = 0, wu = 0;
-        if constexpr (kSwiglu) {
-          const float2 ws = *reinterpret_cast<const float2*>(smem + l.w_scales + (sslot * 4 + (k & 3)) * 8);
-          wg = pair(ws.x, ws.x), wu = pair(ws.y, ws.y);
-        }
+          for (int n = 0; n < 16; ++n) acc[c][n] = 0;
+        for (int k = 0; k < a.steps; ++k) {
+          const float* scale = arrive(k);
+          if (!ok) break;
+          if (some) {
+            const float sx = scale[(k & 3) * kMaxRows + index];
+            const float2 ws = *reinterpret_cast<const float2*>(smem + l.w_scales + (sslot * 4 + (k & 3)) * 8);
+            const float g = sx * (kSwiglu || set == 0 ? ws.x : ws.y), u = sx * ws.y;
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-          if (c < chunks) {
-            uint32_t v[2][4][4];
-            tmem_load_pairs(lanes + buf * kMaxRows + 64 * c, v);
-            if (c == chunks - 1) {  // all of the buffer is in registers
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive_peer(leader_empty + 8 * buf);
+            for (int c = 0; c < kChunks; ++c) {
+              uint32_t v[32];
+              tmem_load32_begin(lanes + buffers.column() + 128 * set + 32 * c, v);
+              tmem_load32_end(v);
+              if (c + 1 == kChunks) release();
+              add_features<kSwiglu>(v, pair(g, g), pair(u, u), acc[c]);
             }
+          } else {
+            release();
+          }
+          leave(k);
+        }
+        if (!ok) break;
+        if (some) {
+          const int row = 32 * w + lane < half ? list[index] : -1;
+          if constexpr (!kSwiglu) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float2 f = *reinterpret_cast<const float2*>(sx + 64 * c + 8 * j);
-              const Pair sc = pair(f.x, f.y);
-              const Pair g = kSwiglu ? mul2(sc, wg) : sc, u = kSwiglu ? mul2(sc, wu) : sc;
+            for (int c = 0; c < kChunks; ++c) {
+              float v[32];
+              unpair(acc[c], v);
+              store_values(a, v, tile.block * kTileFeatures + 128 * set + 32 * c, row, turn);
+            }
+          } else {
+            const int first = tile.block * 128 + 64 * set;
+            if (a.out_dtype != LLMOE_DTYPE_FP8B) {
 #pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                const uint32_t(&p)[4] = v[half][j];
-                acc[c][half][j][0] = fma2(pair(__uint_as_float(p[0]), __uint_as_float(p[1])), g, acc[c][half][j][0]);
-                acc[c][half][j][1] = fma2(pair(__uint_as_float(p[2]), __uint_as_float(p[3])), u, acc[c][half][j][1]);
+              for (int c = 0; c < kChunks; ++c) {
+                float h[16];
+                if (a.out_dtype == LLMOE_DTYPE_FP32)
+                  swiglu_row<true>(acc[c], h);
+                else
+                  swiglu_row<false>(acc[c], h);
+                store_values(a, h, first + 16 * c, row, turn);
               }
+            } else {
+              // a row's block of 128 outputs is this thread's and the other set's
+              float h[kChunks][16];
+              uint32_t most = 0;
+#pragma unroll
+              for (int c = 0; c < kChunks; ++c) {
+                swiglu_row<false>(acc[c], h[c]);
+#pragma unroll
+                for (int n = 0; n < 16; ++n) most = max(most, magnitude(h[c][n]));
+              }
+              uint32_t* swap = reinterpret_cast<uint32_t*>(smem + l.row_max) + (wide_tiles & 1) * 256 + 32 * w + lane;
+              swap[128 * set] = most;
+              __syncwarp();
+              if (lane == 0) mbar_arrive(row_full + 8 * w);
+              if (!(ok = mbar_wait_cta_warp(row_full + 8 * w, wide_tiles & 1, a.err))) break;
+              most = max(most, swap[128 * (set ^ 1)]);
+              const float scale = block_scale(__uint_as_float(most)), inverse = __frcp_rn(scale);
+#pragma unroll
+              for (int c = 0; c < kChunks; c += 2) {
+                uint4 q[2];
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                  uint32_t b[4];
+#pragma unroll
+                  for (int m = 0; m < 4; ++m)
+                    b[m] = pack_e4m3x2(h[c + n][4 * m] * inverse, h[c + n][4 * m + 1] * inverse) |
+                           pack_e4m3x2(h[c + n][4 * m + 2] * inverse, h[c + n][4 * m + 3] * inverse) << 16;
+                  q[n] = make_uint4(b[0], b[1], b[2], b[3]);
+                }
+                store_pieces(a, q[0], q[1], row, first + 16 * c, a.out, turn);
+              }
+              if (set == 0 && row >= 0) {
+                uint8_t* at = in_row(a, a.y + a.out + 4 * tile.block, row);
+                *reinterpret_cast<float*>(at) = scale;
+                if (tile.block + 1 == a.blocks)
+                  for (uint8_t* end = in_row(a, a.y + a.y_row, row); (at += 4) < end;) *reinterpret_cast<uint32_t*>(at) = 0;
+              }
+              ++wide_tiles;
             }
           }
         }
-        if (chunks == 0) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_peer(leader_empty + 8 * buf);
-        }
-        if ((k & 3) == 3 || k + 1 == a.steps) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(scale_empty + 8 * sslot);
-          if (++sslot == kSlots) sslot = 0, sphase ^= 1;
-        }
-      }
-      if (!ok) break;
-      const int* list = rows + slot * kMaxRows + 32 * set;
-      if constexpr (!kSwiglu) {
-        const int first = tile.block * kTileFeatures + (int)rank * 128 + w * 32;
+      } else {
+        // set: every other 32 rows
+        const int chunks = (columns(tile.groups) / 32 + 1 - set) / 2, up = kSwiglu ? lane >> 3 & 1 : 0;
+        constexpr int kChunks = kNarrowRows / 64;
+        Pair acc[kChunks][16];
 #pragma unroll
         for (int c = 0; c < kChunks; ++c)
-          if (c < chunks) store_plain(a, acc[c], first, list + 64 * c, turn);
-      } else {
-        const int first = tile.block * 128 + (int)rank * 64 + w * 16;
-        if (a.out_dtype == LLMOE_DTYPE_FP8B) {
-          // a block of 128 outputs is the pair's: its eight warps of this set swap
-          // their largest magnitudes, once the last tile's have been read
-          if (!(ok = mbar_wait_warp(amax_empty + 8 * set, (i & 1) ^ 1, a.err))) break;
-          const uint32_t mine = smem_addr(amax + (rank * 4 + w) * kMaxRows + 32 * set), peer = map_rank(mine, rank ^ 1);
+#pragma unroll
+          for (int n = 0; n < 16; ++n) acc[c][n] = 0;
+        for (int k = 0; k < a.steps; ++k) {
+          const float* scale = arrive(k);
+          if (!ok) break;
+          scale += (2 * (k & 3) + up) * kNarrowStride + 32 * set;
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) {
+            if (c < chunks) {
+              uint32_t v[32];
+              tmem_load32_begin(lanes + buffers.column() + 32 * set + 64 * c, v);
+              tmem_load32_end(v);
+              if (c + 1 == chunks) release();
+              add_rows(v, scale + 64 * c, acc[c]);
+            }
+          }
+          if (chunks == 0) release();
+          leave(k);
+        }
+        if (!ok) break;
+        list += 32 * set;
+        const int first = kSwiglu ? tile.block * 128 + (int)rank * 64 + w * 16
+                                  : tile.block * kTileFeatures + (int)rank * 128 + w * 32;
+        if (!kSwiglu || a.out_dtype != LLMOE_DTYPE_FP8B) {
 #pragma unroll
           for (int c = 0; c < kChunks; ++c)
             if (c < chunks) {
-              swiglu<false>(acc[c]);
-              int column;
-              const uint32_t m = largest(acc[c], column);
-              amax[(rank * 4 + w) * kMaxRows + 32 * set + 64 * c + column] = m;
-              shared_store_peer(peer + 4 * (64 * c + column), m);
+              float v[32];
+              unpair(acc[c], v);
+              if constexpr (kSwiglu)
+                store_swiglu_values(a, v, first, list + 64 * c);
+              else
+                store_plain(a, v, first, list + 64 * c);
+            }
+        } else {
+          // a block of 128 outputs is the pair's: its eight warps of this set swap
+          // their largest magnitudes, once the last tile's have been read
+          if (!(ok = mbar_wait_warp(amax_empty + 8 * set, (narrow_tiles & 1) ^ 1, a.err))) break;
+          uint32_t* amax = reinterpret_cast<uint32_t*>(smem + l.amax) + 32 * set;
+          const int source = ((int)rank * 4 + w) * kNarrowRows;
+          const uint32_t peer = map_rank(smem_addr(amax + source), rank ^ 1);
+          float h[kChunks][16];
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c)
+            if (c < chunks) {
+              float v[32];
+              unpair(acc[c], v);
+              swiglu_columns(v, h[c]);
+              int at;
+              const uint32_t most = largest_of_columns(h[c], at);
+              const int column = 64 * c + 2 * at + up;
+              amax[source + column] = most;
+              shared_store_peer(peer + 4 * column, most);
             }
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(amax_full + 8 * set);
             mbar_arrive_peer_release(map_rank(amax_full + 8 * set, rank ^ 1));
           }
-          if (!(ok = mbar_wait_warp(amax_full + 8 * set, i & 1, a.err))) break;
-          float scale[kChunks];
+          if (!(ok = mbar_wait_warp(amax_full + 8 * set, narrow_tiles & 1, a.err))) break;
+          float scale[kChunks];  // of row `lane` of each 32
 #pragma unroll
           for (int c = 0; c < kChunks; ++c)
             if (c < chunks) {
-              uint32_t m = 0;
+              uint32_t most = 0;
 #pragma unroll
-              for (int j = 0; j < 8; ++j) m = max(m, amax[j * kMaxRows + 32 * set + 64 * c + lane]);
-              scale[c] = block_scale(__uint_as_float(m));
+              for (int j = 0; j < 8; ++j) most = max(most, amax[j * kNarrowRows + 64 * c + lane]);
+              scale[c] = block_scale(__uint_as_float(most));
             }
           __syncwarp();
           if (lane == 0) {
@@ -433,7 +512,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll
           for (int c = 0; c < kChunks; ++c)
             if (c < chunks) {
-              store_codes(a, acc[c], first, list + 64 * c, __frcp_rn(scale[c]), sbase + l.codes + (warp - 4) * 512);
+              const float mine = __frcp_rn(scale[c]);
+              float inverse[16];
+#pragma unroll
+              for (int n = 0; n < 16; ++n) inverse[n] = __shfl_sync(0xffffffffu, mine, 2 * n + up);
+              store_codes(a, h[c], inverse, first, list + 64 * c);
               const int row = list[64 * c + lane];
               if (leader && w == 0 && row >= 0) {
                 uint8_t* at = in_row(a, a.y + a.out + 4 * tile.block, row);
@@ -442,16 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                   for (uint8_t* end = in_row(a, a.y + a.y_row, row); (at += 4) < end;) *reinterpret_cast<uint32_t*>(at) = 0;
               }
             }
-        } else {
-#pragma unroll
-          for (int c = 0; c < kChunks; ++c)
-            if (c < chunks) {
-              if (a.out_dtype == LLMOE_DTYPE_FP32)
-                swiglu<true>(acc[c]);
-              else
-                swiglu<false>(acc[c]);
-              store_swiglu(a, acc[c], first, list + 64 * c, turn);
-            }
+          ++narrow_tiles;
         }
       }
       __syncwarp();
@@ -460,18 +534,20 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   } else {
     fewer_registers<kFewRegisters>();
     // ---- scales ------------------------------------------------------------------
-    // Warp q's lane moves those of columns 32 q + lane and 128 + 32 q + lane, 16
-    // bytes of a row (four steps) at a time, kAhead such chunks ahead; and lane % 4
-    // (with SwiGLU lane % 8) w's of a step (and of gate or up).
-    constexpr int kAhead = 3, kParts = kSwiglu ? 2 : 1;
+    // Warp q's lane moves those of rows 32 q + lane and 128 + 32 q + lane of the
+    // tile's list, 16 bytes of a row (four steps) at a time, kAhead such chunks
+    // ahead; and lane % 4 w's of a step, for the first or (lane & 4) the second of:
+    // gate and up; a wide tile's two CTAs' features.
+    constexpr int kAhead = 3;
     const int q = warp & 3, chunks = (a.steps + 3) / 4;
     int i = 0, sslot = 0;
     uint32_t sphase = 0;
     bool ok = true;
     for (int t = pair_id; t < ntiles && ok; t += pairs, ++i) {
       const int slot = i % kPlanDepth;
-      if (!(ok = mbar_wait_warp(plan_full + 8 * slot, (i / kPlanDepth) & 1, a.err))) break;
+      if (!(ok = mbar_wait_cta_warp(plan_full + 8 * slot, (i / kPlanDepth) & 1, a.err))) break;
       const Tile tile = tiles[slot];
+      const bool wide = is_wide(tile);
       const int n = columns(tile.groups), m = 32 * q + lane;
       const int r0 = m < n ? rows[slot * kMaxRows + m] : -1;
       const int r1 = 128 + m < n ? rows[slot * kMaxRows + 128 + m] : -1;
@@ -480,9 +556,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       const uint4* src[2] = {reinterpret_cast<const uint4*>(a.x + (uint64_t)max(r0, 0) * a.x_row + a.in),
                              reinterpret_cast<const uint4*>(a.x + (uint64_t)max(r1, 0) * a.x_row + a.in)};
       const bool have[2] = {r0 >= 0, r1 >= 0};
-      // the CTA's features are in one block of w (of gate, of up); past the last one nothing is stored
-      const int block = min(kSwiglu ? tile.block : 2 * tile.block + (int)rank, s.down - 1);
-      const float* wsrc = s.w_scale + (((int64_t)tile.expert * kParts + (kSwiglu ? lane >> 2 & 1 : 0)) * s.down + block) *
+      // past the last block of w's features nothing is stored
+      const int second = lane >> 2 & 1;
+      const int block = kSwiglu ? tile.block : min(2 * tile.block + (wide ? second : (int)rank), s.down - 1);
+      const float* wsrc = s.w_scale + ((kSwiglu ? 2 * (int64_t)tile.expert + second : tile.expert) * s.down + block) *
                                           (int64_t)s.across;
       const auto load_w = [&](int c) { return 4 * c + (lane & 3) < s.across ? wsrc[4 * c + (lane & 3)] : 0.0f; };
       uint4 ahead[kAhead][2];
@@ -501,20 +578,30 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         for (int u = 0; u < kAhead; ++u) {
           const int c = c0 + u;
           if (c >= chunks || !ok) break;
-          if (!(ok = mbar_wait_warp(scale_empty + 8 * sslot, sphase ^ 1, a.err))) break;
+          if (!(ok = mbar_wait_cta_warp(scale_empty + 8 * sslot, sphase ^ 1, a.err))) break;
           float* dst = reinterpret_cast<float*>(smem + l.scales + sslot * kSlot) + m;
+          if (wide) {
 #pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const float ws = kSwiglu ? 1.0f : __shfl_sync(0xffffffffu, w_ahead[u], b);
+            for (int b = 0; b < 4; ++b)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const uint4& v = ahead[u][j];
+              for (int j = 0; j < 2; ++j) {
+                const uint4& v = ahead[u][j];
+                if (have[j]) dst[b * kMaxRows + 128 * j] = __uint_as_float(b == 0 ? v.x : b == 1 ? v.y : b == 2 ? v.z : v.w);
+              }
+            if (q == 0 && lane < 8)
+              reinterpret_cast<float*>(smem + l.w_scales)[(sslot * 4 + (lane & 3)) * 2 + second] = w_ahead[u];
+          } else {
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              const uint4& v = ahead[u][0];
               const float x = __uint_as_float(b == 0 ? v.x : b == 1 ? v.y : b == 2 ? v.z : v.w);
-              if (have[j]) dst[b * kMaxRows + j * 128] = kSwiglu ? x : x * ws;
+#pragma unroll
+              for (int p = 0; p < (kSwiglu ? 2 : 1); ++p) {
+                const float ws = __shfl_sync(0xffffffffu, w_ahead[u], 4 * p + b);
+                if (have[0]) dst[(2 * b + p) * kNarrowStride] = x * ws;
+              }
             }
           }
-          if (kSwiglu && q == 0 && lane < 8)
-            reinterpret_cast<float*>(smem + l.w_scales)[(sslot * 4 + (lane & 3)) * 2 + (lane >> 2)] = w_ahead[u];
           __syncwarp();
           if (lane == 0) mbar_arrive(scale_full + 8 * sslot);
           if (++sslot == kSlots) sslot = 0, sphase ^= 1;

@@ -84,7 +84,35 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int32_t
   return true;
 }
 
-// The same for a whole warp that goes on together: one lane's expiry is all lanes'.
+// The same where what the barrier guards is not another CTA's writes to shared
+// memory: an acquire of the cluster costs 200 cycles on a phase that is complete,
+// this one 20.
+__device__ __forceinline__ bool mbar_try_wait_cta(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+__device__ __forceinline__ bool mbar_wait_cta(uint32_t bar, uint32_t parity, int32_t* err) {
+  if (mbar_try_wait_cta(bar, parity)) return true;
+  const long long start = clock64();
+  while (!mbar_try_wait_cta(bar, parity))
+    if (clock64() - start > kSpinLimit) {
+      report(err, LLMOE_DEV_TIMEOUT);
+      return false;
+    }
+  return true;
+}
+__device__ __forceinline__ bool mbar_wait_cta_warp(uint32_t bar, uint32_t parity, int32_t* err) {
+  return __all_sync(0xffffffffu, mbar_wait_cta(bar, parity, err));
+}
+
+// mbar_wait for a whole warp that goes on together: one lane's expiry is all lanes'.
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, int32_t* err) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, err));
 }
@@ -144,39 +172,31 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// 32 columns of this warp's 32 lanes in four lanes at a time: with q = lane % 4 and
-// l = lane / 4, v[half][j][r] is lane 16 half + 8 (r / 2) + l, column 8 j + 2 q +
-// r % 2.  A thread holds pairs of neighbouring columns, and each column's value
-// for four lanes.
-__device__ __forceinline__ void tmem_load_pairs(uint32_t addr, uint32_t (&v)[2][4][4]) {
-#define LLMOE_REGS(h)                                                                                               \
-  "=r"(v[h][0][0]), "=r"(v[h][0][1]), "=r"(v[h][0][2]), "=r"(v[h][0][3]), "=r"(v[h][1][0]), "=r"(v[h][1][1]),        \
-      "=r"(v[h][1][2]), "=r"(v[h][1][3]), "=r"(v[h][2][0]), "=r"(v[h][2][1]), "=r"(v[h][2][2]), "=r"(v[h][2][3]),    \
-      "=r"(v[h][3][0]), "=r"(v[h][3][1]), "=r"(v[h][3][2]), "=r"(v[h][3][3])
+// The same in two parts.  The registers are the load's until the wait, which names
+// them so that no use of them can move before it; it waits for all of the
+// thread's loads.
+__device__ __forceinline__ void tmem_load32_begin(uint32_t addr, uint32_t (&v)[32]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32"
-      " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%32];\n\t"
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32"
-      " {%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%33];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : LLMOE_REGS(0), LLMOE_REGS(1)
-      : "r"(addr), "r"(addr + (16u << 16))
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32"
+      " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31},"
+      " [%32];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(addr)
       : "memory");
-#undef LLMOE_REGS
 }
-
-// Four 8 x 8 matrices of 16-bit values to shared memory, turned: this thread's
-// word of a matrix holds row lane / 4, columns 2 (lane % 4) and the next, and
-// lane 8 m + c gives the address where matrix m's column c goes, 16 bytes.
-__device__ __forceinline__ void store_turned(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared::cta.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
-               "r"(c), "r"(d)
+__device__ __forceinline__ void tmem_load32_end(uint32_t (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
+               :
                : "memory");
 }
 __device__ __forceinline__ uint4 shared_load16(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared::cta.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
   return v;
+}
+__device__ __forceinline__ void shared_store16(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared::cta.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 __device__ __forceinline__ void shared_store_peer(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
