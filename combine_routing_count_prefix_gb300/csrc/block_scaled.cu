@@ -50,14 +50,13 @@ struct ScaledArgs {
 
 // Byte offsets in dynamic shared memory, from its first 1024-byte boundary.
 struct ScaledSmem {
-  uint32_t scales, w_scales, turn, amax, row_max, boxes, rows, tiles, bars, tmem, part, prefix, total;
+  uint32_t scales, w_scales, amax, row_max, boxes, rows, tiles, bars, tmem, part, prefix, total;
 };
 __host__ __device__ inline ScaledSmem scaled_smem(int stages, int E) {
   ScaledSmem l;
   uint32_t at = stages * kStage;
   l.scales = at, at += kSlots * kSlot;
   l.w_scales = at, at += kSlots * 4 * 2 * 4;
-  l.turn = at, at += 8 * 1024;              // for each warp, 32 bytes of 32 rows
   l.amax = at, at += 8 * kNarrowRows * 4;   // narrow: [warp of the pair's set][row]
   l.row_max = at, at += 2 * 2 * 128 * 4;    // wide: [tile's parity][set][row]
   l.boxes = at, at += kPlanDepth * 32 * 16;
@@ -71,25 +70,8 @@ __host__ __device__ inline ScaledSmem scaled_smem(int stages, int E) {
   return l;
 }
 
-// The buffer of tensor memory that a step uses, and its barriers' phase: the
-// issuing thread and the summing warps go through the same sequence.  Where the
-// kind of tile changes, so do the buffers.
-struct Buffers {
-  uint32_t phases = 0;  // a bit each
-  int next = 0;
-  bool wide = false;
-  __device__ __forceinline__ bool change(bool w) {
-    if (w == wide) return false;
-    wide = w, next = 0;
-    return true;
-  }
-  __device__ __forceinline__ uint32_t phase() const { return phases >> next & 1; }
-  __device__ __forceinline__ uint32_t column() const { return (uint32_t)next * (wide ? 256 : 128); }
-  __device__ __forceinline__ void advance() {
-    phases ^= 1u << next;
-    next = (next + 1) & (wide ? 1 : kBuffers - 1);
-  }
-};
+// Step k of a tile uses buffer k % 2 (wide) or k % 4; a buffer's phase is a bit of a
+// word that the issuing thread and the summing warps each keep.
 __device__ __forceinline__ bool is_wide(const Tile& t) { return t.groups > kNarrowRows / kGroup; }
 
 __device__ __forceinline__ void unpair(const Pair (&p)[16], float (&v)[32]) {
@@ -124,28 +106,27 @@ __device__ __forceinline__ void add_features(const uint32_t (&v)[32], Pair gate,
     acc[i] = fma2(pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), kSwiglu && (i & 4) ? up : gate, acc[i]);
 }
 
-// 32 bytes of each lane's row to y, `at` bytes into the row: turned through the
-// warp's 1 KB of shared memory, so that two lanes store a row's 32 bytes.
+// 32 bytes of each lane's row to y, `at` bytes into the row: neighbours swap halves,
+// so that two lanes store the 32 bytes of one of their rows, then the other's.
 __device__ __forceinline__ void store_pieces(const ProductArgs& a, const uint4& first, const uint4& second, int row,
-                                             uint32_t at, uint32_t end, uint32_t turn) {
-  const int lane = threadIdx.x & 31;
-  const uint32_t swap = lane >> 2 & 1;
-  shared_store16(turn + lane * 32 + (swap << 4), first);
-  shared_store16(turn + lane * 32 + ((swap ^ 1) << 4), second);
-  __syncwarp();
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int from = 16 * i + (lane >> 1), piece = lane & 1;
-    const uint4 v = shared_load16(turn + from * 32 + ((piece ^ (from >> 2 & 1)) << 4));
-    const int to = __shfl_sync(0xffffffffu, row, from);
-    if (to >= 0 && at + 16 * piece < end) *reinterpret_cast<uint4*>(in_row(a, a.y + at + 16 * piece, to)) = v;
-  }
-  __syncwarp();  // read, before the next pieces are written
+                                             int neighbour, uint32_t at, uint32_t end) {
+  const bool odd = threadIdx.x & 1;
+  uint4 got;
+  got.x = __shfl_xor_sync(0xffffffffu, odd ? first.x : second.x, 1);
+  got.y = __shfl_xor_sync(0xffffffffu, odd ? first.y : second.y, 1);
+  got.z = __shfl_xor_sync(0xffffffffu, odd ? first.z : second.z, 1);
+  got.w = __shfl_xor_sync(0xffffffffu, odd ? first.w : second.w, 1);
+  at += odd ? 16 : 0;
+  const int even_row = odd ? neighbour : row, odd_row = odd ? row : neighbour;
+  if (at >= end) return;
+  if (even_row >= 0) *reinterpret_cast<uint4*>(in_row(a, a.y + at, even_row)) = odd ? got : first;
+  if (odd_row >= 0) *reinterpret_cast<uint4*>(in_row(a, a.y + at, odd_row)) = odd ? second : got;
 }
 
 // N values of the lane's row from feature `first` on, to fp32, bf16 or fp16 (N: 16 or 32).
 template <int N>
-__device__ __forceinline__ void store_values(const ProductArgs& a, const float (&v)[N], int first, int row, uint32_t turn) {
+__device__ __forceinline__ void store_values(const ProductArgs& a, const float (&v)[N], int first, int row,
+                                             int neighbour) {
   if (a.out_dtype == LLMOE_DTYPE_FP32) {
 #pragma unroll
     for (int i = 0; i < N; i += 8) {
@@ -154,7 +135,7 @@ __device__ __forceinline__ void store_values(const ProductArgs& a, const float (
       for (int u = 0; u < 2; ++u)
         q[u] = make_uint4(__float_as_uint(v[i + 4 * u]), __float_as_uint(v[i + 4 * u + 1]), __float_as_uint(v[i + 4 * u + 2]),
                           __float_as_uint(v[i + 4 * u + 3]));
-      store_pieces(a, q[0], q[1], row, (uint32_t)(first + i) * 4, (uint32_t)a.out * 4, turn);
+      store_pieces(a, q[0], q[1], row, neighbour, (uint32_t)(first + i) * 4, (uint32_t)a.out * 4);
     }
     return;
   }
@@ -166,7 +147,7 @@ __device__ __forceinline__ void store_values(const ProductArgs& a, const float (
     for (int u = 0; u < 2; ++u)
       q[u] = make_uint4(pack2(v[i + 8 * u], v[i + 8 * u + 1], fp16), pack2(v[i + 8 * u + 2], v[i + 8 * u + 3], fp16),
                         pack2(v[i + 8 * u + 4], v[i + 8 * u + 5], fp16), pack2(v[i + 8 * u + 6], v[i + 8 * u + 7], fp16));
-    store_pieces(a, q[0], q[1], row, (uint32_t)(first + i) * 2, (uint32_t)a.out * 2, turn);
+    store_pieces(a, q[0], q[1], row, neighbour, (uint32_t)(first + i) * 2, (uint32_t)a.out * 2);
   }
 }
 
@@ -180,6 +161,124 @@ __device__ __forceinline__ void swiglu_row(const Pair (&acc)[16], float (&h)[16]
     h[2 * i + 1] = (kAccurate ? silu(g.y) : near_silu(g.y)) * u.y;
   }
 }
+
+// ---------------------------------------------------------------------------
+// a tile's sums
+// ---------------------------------------------------------------------------
+// What a summing warp keeps from tile to tile.  The steps of a slot of scales are
+// unrolled, so that buffers and addresses are constants: with one or two warps
+// ready on a scheduler every instruction of a step costs 5 to 10 cycles.
+struct Sums {
+  uint32_t acc_full, leader_empty, scale_full, scale_empty;
+  const float* scales;
+  int32_t* err;
+  int steps;
+  uint32_t phases, slot, slot_phase;
+  bool ok;
+
+  __device__ __forceinline__ void wait_scales() { mbar_wait_cta_warp(scale_full + 8 * slot, slot_phase, ok, err); }
+  template <int kBuffer>
+  __device__ __forceinline__ void wait() {
+    mbar_wait_cta_warp<8 * kBuffer>(acc_full, phases >> kBuffer & 1, ok, err);
+    phases ^= 1u << kBuffer;
+    tc_fence_after();
+  }
+  // this warp has read the buffer
+  template <int kBuffer>
+  __device__ __forceinline__ void release() {
+    tc_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive_peer(leader_empty + 8 * kBuffer);
+  }
+  __device__ __forceinline__ void release_scales() {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(scale_empty + 8 * slot);
+    slot ^= 1;
+    slot_phase ^= slot ^ 1;
+    static_assert(kSlots == 2, "slots alternate");
+  }
+
+  // Narrow: kChunks times 32 rows, 64 columns apart from address `at` on in buffer 0;
+  // scale: their place in a step's scales.
+  template <int kChunks, int kStep>
+  __device__ __forceinline__ void narrow_step(Pair (&acc)[4][16], uint32_t at, const float* scale) {
+    wait<kStep>();
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      uint32_t v[32];
+      if (c == 0)
+        tmem_load32_begin<128 * kStep>(at, v);
+      else
+        tmem_load32_begin<128 * kStep + 64>(at, v);
+      tmem_load32_end(v);
+      if (c + 1 == kChunks) release<kStep>();
+      add_rows(v, scale + 2 * kStep * kNarrowStride + 64 * c, acc[c]);
+    }
+    if (kChunks == 0) release<kStep>();
+  }
+  template <int kChunks>
+  __device__ __forceinline__ void narrow(Pair (&acc)[4][16], uint32_t at, int scale) {
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+      for (int n = 0; n < 16; ++n) acc[c][n] = 0;
+    for (int k = 0; k < steps; k += 4) {
+      wait_scales();
+      const float* from = scales + slot * (kSlot / 4) + scale;
+      narrow_step<kChunks, 0>(acc, at, from);
+      if (k + 1 < steps) narrow_step<kChunks, 1>(acc, at, from);
+      if (k + 2 < steps) narrow_step<kChunks, 2>(acc, at, from);
+      if (k + 3 < steps) narrow_step<kChunks, 3>(acc, at, from);
+      release_scales();
+    }
+  }
+
+  // Wide: 128 features from address `at` on in buffer 0; index: the row's place in a
+  // step's scales, some: whether the warp has rows at all; w_scale: gate's, or that
+  // of the features, in a slot, with SwiGLU up's behind it.
+  template <bool kSwiglu, int kStep>
+  __device__ __forceinline__ void wide_step(Pair (&acc)[4][16], uint32_t at, const float* scale, const float* w_scale,
+                                            bool some) {
+    constexpr int kBuffer = kStep & 1;
+    wait<kBuffer>();
+    if (some) {
+      uint32_t v[32];
+      tmem_load32_begin<256 * kBuffer>(at, v);
+      const float s = scale[kStep * kMaxRows], g = s * w_scale[2 * kStep], u = kSwiglu ? s * w_scale[2 * kStep + 1] : 0;
+      tmem_load32_end(v);
+      add_features<kSwiglu>(v, pair(g, g), pair(u, u), acc[0]);
+      tmem_load32_begin<256 * kBuffer + 32>(at, v);
+      tmem_load32_end(v);
+      add_features<kSwiglu>(v, pair(g, g), pair(u, u), acc[1]);
+      tmem_load32_begin<256 * kBuffer + 64>(at, v);
+      tmem_load32_end(v);
+      add_features<kSwiglu>(v, pair(g, g), pair(u, u), acc[2]);
+      tmem_load32_begin<256 * kBuffer + 96>(at, v);
+      tmem_load32_end(v);
+      release<kBuffer>();
+      add_features<kSwiglu>(v, pair(g, g), pair(u, u), acc[3]);
+    } else {
+      release<kBuffer>();
+    }
+  }
+  template <bool kSwiglu>
+  __device__ __forceinline__ void wide(Pair (&acc)[4][16], uint32_t at, int index, bool some, const float* w_scales) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int n = 0; n < 16; ++n) acc[c][n] = 0;
+    for (int k = 0; k < steps; k += 4) {
+      wait_scales();
+      const float* from = scales + slot * (kSlot / 4) + index;
+      const float* ws = w_scales + slot * 8;
+      wide_step<kSwiglu, 0>(acc, at, from, ws, some);
+      if (k + 1 < steps) wide_step<kSwiglu, 1>(acc, at, from, ws, some);
+      if (k + 2 < steps) wide_step<kSwiglu, 2>(acc, at, from, ws, some);
+      if (k + 3 < steps) wide_step<kSwiglu, 3>(acc, at, from, ws, some);
+      release_scales();
+    }
+  }
+};
 
 // ---------------------------------------------------------------------------
 // the kernel
@@ -255,31 +354,32 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       // ---- products: one thread -----------------------------------------------------
       if (leader && elect_one()) {
         int stage = 0, i = 0;
-        uint32_t phase = 0;
-        Buffers buffers;
-        bool ok = true;
+        uint32_t phase = 0, phases = 0;
+        bool ok = true, wide = false;
         const uint32_t desc = tile_desc(sbase);
         for (int t = pair_id; t < ntiles && ok; t += pairs, ++i) {
           const int slot = i % kPlanDepth;
           if (!(ok = mbar_wait_cta(plan_full + 8 * slot, (i / kPlanDepth) & 1, a.err))) break;
-          const bool wide = is_wide(tiles[slot]);
+          const bool was_wide = wide;
+          wide = is_wide(tiles[slot]);
           const uint32_t n = wide ? kTileFeatures : columns(tiles[slot].groups), idesc = a.idesc | (n >> 3) << 17;
+          const int mask = wide ? 1 : kBuffers - 1;
+          const uint32_t stride = wide ? 256 : 128;
           mbar_arrive(plan_empty + 8 * slot);
-          if (buffers.change(wide))  // other columns: every buffer has to be handed back
-            for (int b = 0; b < kBuffers && ok; ++b)
-              ok = mbar_wait_cta(acc_empty + 8 * b, (buffers.phases >> b & 1) ^ 1, a.err);
+          if (wide != was_wide)  // other columns: every buffer has to be handed back
+            for (int b = 0; b < kBuffers && ok; ++b) ok = mbar_wait_cta(acc_empty + 8 * b, (phases >> b & 1) ^ 1, a.err);
           for (int k = 0; k < a.steps && ok; ++k) {
+            const int b = k & mask;
             const uint32_t w = desc + (uint32_t)(stage * (kStage >> 4)), x = w + (kBytesA >> 4);
-            const uint32_t m_side = wide ? x : w, n_side = wide ? w : x;
-            if (!(ok = mbar_wait_cta(acc_empty + 8 * buffers.next, buffers.phase() ^ 1, a.err))) break;
+            const uint32_t m_side = wide ? x : w, n_side = wide ? w : x, d = tmem + (uint32_t)b * stride;
+            if (!(ok = mbar_wait_cta(acc_empty + 8 * b, (phases >> b & 1) ^ 1, a.err))) break;
             if (!(ok = mbar_wait_cta(full + 8 * stage, phase, a.err))) break;
             tc_fence_after();
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              mma_8bit(tmem + buffers.column(), m_side + 2 * j, n_side + 2 * j, idesc, j > 0);
-            mma_commit_pair(acc_full + 8 * buffers.next);
+            for (int j = 0; j < 4; ++j) mma_8bit(d, m_side + 2 * j, n_side + 2 * j, idesc, j > 0);
+            mma_commit_pair(acc_full + 8 * b);
             mma_commit_pair(empty + 8 * stage);
-            buffers.advance();
+            phases ^= 1u << b;
             if (++stage == a.stages) stage = 0, phase ^= 1;
           }
         }
@@ -301,79 +401,40 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     // ---- sums and epilogue ---------------------------------------------------------
     // two sets of four warps, warp w of each on tensor-memory lanes 32 w ..
     const int w = warp & 3, set = warp >= 8;
-    const uint32_t turn = sbase + l.turn + (warp - 4) * 1024, lanes = tmem + ((uint32_t)(32 * w) << 16);
-    const uint32_t leader_empty = map_rank(acc_empty, 0);
-    int i = 0, sslot = 0, narrow_tiles = 0, wide_tiles = 0;
-    uint32_t sphase = 0;
-    Buffers buffers;
-    bool ok = true;
-    // a step's scales and sums are there: the scales' place
-    const auto arrive = [&](int k) -> const float* {
-      if ((k & 3) == 0 && !(ok = mbar_wait_cta_warp(scale_full + 8 * sslot, sphase, a.err))) return nullptr;
-      if (!(ok = mbar_wait_cta_warp(acc_full + 8 * buffers.next, buffers.phase(), a.err))) return nullptr;
-      tc_fence_after();
-      return reinterpret_cast<const float*>(smem + l.scales + sslot * kSlot);
-    };
-    // this warp has read the step's sums
-    const auto release = [&] {
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_peer(leader_empty + 8 * buffers.next);
-    };
-    const auto leave = [&](int k) {
-      buffers.advance();
-      if ((k & 3) == 3 || k + 1 == a.steps) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(scale_empty + 8 * sslot);
-        if (++sslot == kSlots) sslot = 0, sphase ^= 1;
-      }
-    };
+    Sums sums;
+    sums.acc_full = acc_full, sums.leader_empty = map_rank(acc_empty, 0);
+    sums.scale_full = scale_full, sums.scale_empty = scale_empty;
+    sums.scales = reinterpret_cast<const float*>(smem + l.scales);
+    sums.err = a.err, sums.steps = a.steps;
+    sums.phases = sums.slot = sums.slot_phase = 0;
+    sums.ok = true;
+    bool& ok = sums.ok;
+    int i = 0, narrow_tiles = 0, wide_tiles = 0;
     for (int t = pair_id; t < ntiles && ok; t += pairs, ++i) {
       const int slot = i % kPlanDepth;
-      if (!(ok = mbar_wait_cta_warp(plan_full + 8 * slot, (i / kPlanDepth) & 1, a.err))) break;
+      mbar_wait_cta_warp(plan_full + 8 * slot, (i / kPlanDepth) & 1, ok, a.err);
+      if (!ok) break;
+      uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16);
+      asm volatile("" : "+r"(lanes));  // not kept, with sums of it, from tile to tile
+      Pair acc[4][16];  // one for both kinds of tile: with an array each 1.4 KB of registers spill
       const Tile tile = tiles[slot];
       const int* list = rows + slot * kMaxRows;
-      const bool wide = is_wide(tile);
-      buffers.change(wide);
-      if (wide) {
+      if (is_wide(tile)) {
         // set: which CTA's 128 features.  Rows: the pair's halves of the list.
         const int half = columns(tile.groups) / 2, index = (int)rank * half + 32 * w + lane;
         const bool some = 32 * w < half;
         constexpr int kChunks = 4;
-        Pair acc[kChunks][16];
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c)
-#pragma unroll
-          for (int n = 0; n < 16; ++n) acc[c][n] = 0;
-        for (int k = 0; k < a.steps; ++k) {
-          const float* scale = arrive(k);
-          if (!ok) break;
-          if (some) {
-            const float sx = scale[(k & 3) * kMaxRows + index];
-            const float2 ws = *reinterpret_cast<const float2*>(smem + l.w_scales + (sslot * 4 + (k & 3)) * 8);
-            const float g = sx * (kSwiglu || set == 0 ? ws.x : ws.y), u = sx * ws.y;
-#pragma unroll
-            for (int c = 0; c < kChunks; ++c) {
-              uint32_t v[32];
-              tmem_load32_begin(lanes + buffers.column() + 128 * set + 32 * c, v);
-              tmem_load32_end(v);
-              if (c + 1 == kChunks) release();
-              add_features<kSwiglu>(v, pair(g, g), pair(u, u), acc[c]);
-            }
-          } else {
-            release();
-          }
-          leave(k);
-        }
+        sums.wide<kSwiglu>(acc, lanes + 128 * set, index, some,
+                           reinterpret_cast<const float*>(smem + l.w_scales) + (kSwiglu ? 0 : set));
         if (!ok) break;
         if (some) {
-          const int row = 32 * w + lane < half ? list[index] : -1;
+          const int row = 32 * w + lane < half ? list[index] : -1, neighbour = __shfl_xor_sync(0xffffffffu, row, 1);
           if constexpr (!kSwiglu) {
 #pragma unroll
             for (int c = 0; c < kChunks; ++c) {
               float v[32];
               unpair(acc[c], v);
-              store_values(a, v, tile.block * kTileFeatures + 128 * set + 32 * c, row, turn);
+              store_values(a, v, tile.block * kTileFeatures + 128 * set + 32 * c, row, neighbour);
             }
           } else {
             const int first = tile.block * 128 + 64 * set;
@@ -385,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                   swiglu_row<true>(acc[c], h);
                 else
                   swiglu_row<false>(acc[c], h);
-                store_values(a, h, first + 16 * c, row, turn);
+                store_values(a, h, first + 16 * c, row, neighbour);
               }
             } else {
               // a row's block of 128 outputs is this thread's and the other set's
@@ -401,7 +462,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
               swap[128 * set] = most;
               __syncwarp();
               if (lane == 0) mbar_arrive(row_full + 8 * w);
-              if (!(ok = mbar_wait_cta_warp(row_full + 8 * w, wide_tiles & 1, a.err))) break;
+              mbar_wait_cta_warp(row_full + 8 * w, wide_tiles & 1, ok, a.err);
+              if (!ok) break;
               most = max(most, swap[128 * (set ^ 1)]);
               const float scale = block_scale(__uint_as_float(most)), inverse = __frcp_rn(scale);
 #pragma unroll
@@ -416,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                            pack_e4m3x2(h[c + n][4 * m + 2] * inverse, h[c + n][4 * m + 3] * inverse) << 16;
                   q[n] = make_uint4(b[0], b[1], b[2], b[3]);
                 }
-                store_pieces(a, q[0], q[1], row, first + 16 * c, a.out, turn);
+                store_pieces(a, q[0], q[1], row, neighbour, first + 16 * c, a.out);
               }
               if (set == 0 && row >= 0) {
                 uint8_t* at = in_row(a, a.y + a.out + 4 * tile.block, row);
@@ -432,28 +494,14 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         // set: every other 32 rows
         const int chunks = (columns(tile.groups) / 32 + 1 - set) / 2, up = kSwiglu ? lane >> 3 & 1 : 0;
         constexpr int kChunks = kNarrowRows / 64;
-        Pair acc[kChunks][16];
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c)
-#pragma unroll
-          for (int n = 0; n < 16; ++n) acc[c][n] = 0;
-        for (int k = 0; k < a.steps; ++k) {
-          const float* scale = arrive(k);
-          if (!ok) break;
-          scale += (2 * (k & 3) + up) * kNarrowStride + 32 * set;
-#pragma unroll
-          for (int c = 0; c < kChunks; ++c) {
-            if (c < chunks) {
-              uint32_t v[32];
-              tmem_load32_begin(lanes + buffers.column() + 32 * set + 64 * c, v);
-              tmem_load32_end(v);
-              if (c + 1 == chunks) release();
-              add_rows(v, scale + 64 * c, acc[c]);
-            }
-          }
-          if (chunks == 0) release();
-          leave(k);
-        }
+        const int scale = up * kNarrowStride + 32 * set;
+        if (chunks == 2)
+          sums.narrow<2>(acc, lanes + 32 * set, scale);
+        else if (chunks == 1)
+          sums.narrow<1>(acc, lanes + 32 * set, scale);
+        else
+          sums.narrow<0>(acc, lanes + 32 * set, scale);
+        static_assert(kChunks == 2, "all numbers of chunks");
         if (!ok) break;
         list += 32 * set;
         const int first = kSwiglu ? tile.block * 128 + (int)rank * 64 + w * 16
@@ -545,7 +593,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     bool ok = true;
     for (int t = pair_id; t < ntiles && ok; t += pairs, ++i) {
       const int slot = i % kPlanDepth;
-      if (!(ok = mbar_wait_cta_warp(plan_full + 8 * slot, (i / kPlanDepth) & 1, a.err))) break;
+      mbar_wait_cta_warp(plan_full + 8 * slot, (i / kPlanDepth) & 1, ok, a.err);
+      if (!ok) break;
       const Tile tile = tiles[slot];
       const bool wide = is_wide(tile);
       const int n = columns(tile.groups), m = 32 * q + lane;
@@ -578,7 +627,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         for (int u = 0; u < kAhead; ++u) {
           const int c = c0 + u;
           if (c >= chunks || !ok) break;
-          if (!(ok = mbar_wait_cta_warp(scale_empty + 8 * sslot, sphase ^ 1, a.err))) break;
+          mbar_wait_cta_warp(scale_empty + 8 * sslot, sphase ^ 1, ok, a.err);
+          if (!ok) break;
           float* dst = reinterpret_cast<float*>(smem + l.scales + sslot * kSlot) + m;
           if (wide) {
 #pragma unroll

@@ -108,8 +108,22 @@ __device__ __forceinline__ bool mbar_wait_cta(uint32_t bar, uint32_t parity, int
     }
   return true;
 }
-__device__ __forceinline__ bool mbar_wait_cta_warp(uint32_t bar, uint32_t parity, int32_t* err) {
-  return __all_sync(0xffffffffu, mbar_wait_cta(bar, parity, err));
+// The same for a whole warp that goes on together, on the barrier kOffset bytes
+// further, whose phase is most often complete; once a wait has failed, ok stays
+// false and nothing is waited for.
+template <int kOffset = 0>
+__device__ __forceinline__ void mbar_wait_cta_warp(uint32_t bar, uint32_t parity, bool& ok, int32_t* err) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1 + %3], %2;\n\t"
+      "vote.sync.all.pred p, p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity), "n"(kOffset)
+      : "memory");
+  if (done) return;
+  if (ok) ok = __all_sync(0xffffffffu, mbar_wait_cta(bar + kOffset, parity, err));
 }
 
 // mbar_wait for a whole warp that goes on together: one lane's expiry is all lanes'.
@@ -174,14 +188,16 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
 
 // The same in two parts.  The registers are the load's until the wait, which names
 // them so that no use of them can move before it; it waits for all of the
-// thread's loads.
+// thread's loads.  kOffset: added to the address (an immediate: sums that the
+// compiler would otherwise keep in registers across the loops around).
+template <int kOffset>
 __device__ __forceinline__ void tmem_load32_begin(uint32_t addr, uint32_t (&v)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32"
       " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31},"
-      " [%32];"
+      " [%32 + %33];"
       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
-      : "r"(addr)
+      : "r"(addr), "n"(kOffset)
       : "memory");
 }
 __device__ __forceinline__ void tmem_load32_end(uint32_t (&v)[32]) {
@@ -189,14 +205,6 @@ __device__ __forceinline__ void tmem_load32_end(uint32_t (&v)[32]) {
                : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
                :
                : "memory");
-}
-__device__ __forceinline__ uint4 shared_load16(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared::cta.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ void shared_store16(uint32_t addr, const uint4& v) {
-  asm volatile("st.shared::cta.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 __device__ __forceinline__ void shared_store_peer(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
