@@ -165,23 +165,32 @@ __device__ __forceinline__ void swiglu_row(const Pair (&acc)[16], float (&h)[16]
 // ---------------------------------------------------------------------------
 // a tile's sums
 // ---------------------------------------------------------------------------
-// What a summing warp keeps from tile to tile.  The steps of a slot of scales are
-// unrolled, so that buffers and addresses are constants: with one or two warps
-// ready on a scheduler every instruction of a step costs 5 to 10 cycles.
+// What a summing warp keeps from tile to tile.  Under the tensor core's and the
+// loads' traffic an access to shared memory takes about 140 cycles, a test of a
+// barrier among them, so a step's are issued during the step before: whether its
+// sums are there, and its scales.  The steps of a slot of scales are unrolled, so
+// that buffers and addresses are constants.
 struct Sums {
   uint32_t acc_full, leader_empty, scale_full, scale_empty;
   const float* scales;
+  const float* w_scales;
   int32_t* err;
   int steps;
   uint32_t phases, slot, slot_phase;
+  uint32_t next_done;  // the next step's sums were there when last looked
   bool ok;
 
-  __device__ __forceinline__ void wait_scales() { mbar_wait_cta_warp(scale_full + 8 * slot, slot_phase, ok, err); }
+  // The first step's of a tile.
+  __device__ __forceinline__ void start() { next_done = 0; }
   template <int kBuffer>
   __device__ __forceinline__ void wait() {
-    mbar_wait_cta_warp<8 * kBuffer>(acc_full, phases >> kBuffer & 1, ok, err);
+    mbar_wait_cta_warp(acc_full + 8 * kBuffer, phases >> kBuffer & 1, ok, err, next_done);
     phases ^= 1u << kBuffer;
     tc_fence_after();
+  }
+  template <int kBuffer>
+  __device__ __forceinline__ void look() {
+    next_done = mbar_test_cta<8 * kBuffer>(acc_full, phases >> kBuffer & 1);
   }
   // this warp has read the buffer
   template <int kBuffer>
@@ -190,6 +199,7 @@ struct Sums {
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive_peer(leader_empty + 8 * kBuffer);
   }
+  __device__ __forceinline__ void wait_scales() { mbar_wait_cta_warp(scale_full + 8 * slot, slot_phase, ok, err); }
   __device__ __forceinline__ void release_scales() {
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(scale_empty + 8 * slot);
@@ -211,10 +221,16 @@ struct Sums {
       else
         tmem_load32_begin<128 * kStep + 64>(at, v);
       tmem_load32_end(v);
-      if (c + 1 == kChunks) release<kStep>();
+      if (c + 1 == kChunks) {
+        release<kStep>();
+        look<(kStep + 1) % kBuffers>();
+      }
       add_rows(v, scale + 2 * kStep * kNarrowStride + 64 * c, acc[c]);
     }
-    if (kChunks == 0) release<kStep>();
+    if (kChunks == 0) {
+      release<kStep>();
+      look<(kStep + 1) % kBuffers>();
+    }
   }
   template <int kChunks>
   __device__ __forceinline__ void narrow(Pair (&acc)[4][16], uint32_t at, int scale) {
@@ -222,6 +238,7 @@ struct Sums {
     for (int c = 0; c < kChunks; ++c)
 #pragma unroll
       for (int n = 0; n < 16; ++n) acc[c][n] = 0;
+    start();
     for (int k = 0; k < steps; k += 4) {
       wait_scales();
       const float* from = scales + slot * (kSlot / 4) + scale;
@@ -234,49 +251,70 @@ struct Sums {
   }
 
   // Wide: 128 features from address `at` on in buffer 0; index: the row's place in a
-  // step's scales, some: whether the warp has rows at all; w_scale: gate's, or that
-  // of the features, in a slot, with SwiGLU up's behind it.
+  // step's scales, some: whether the warp has rows at all; wi: which of a step's two
+  // scales of w is the features' (SwiGLU: 0 gate, 1 up).  row, w0, w1: the step's scales.
   template <bool kSwiglu, int kStep>
-  __device__ __forceinline__ void wide_step(Pair (&acc)[4][16], uint32_t at, const float* scale, const float* w_scale,
-                                            bool some) {
+  __device__ __forceinline__ void wide_step(Pair (&acc)[4][16], uint32_t at, int index, int wi, bool some, bool more,
+                                            float& row, float& w0, float& w1) {
     constexpr int kBuffer = kStep & 1;
     wait<kBuffer>();
     if (some) {
       uint32_t v[32];
       tmem_load32_begin<256 * kBuffer>(at, v);
-      const float s = scale[kStep * kMaxRows], g = s * w_scale[2 * kStep], u = kSwiglu ? s * w_scale[2 * kStep + 1] : 0;
+      const float g = row * w0, u = kSwiglu ? row * w1 : 0;
       tmem_load32_end(v);
+      if (kStep < 3) load_scales<kSwiglu, (kStep + 1) % 4>(index, wi, row, w0, w1);
       add_features<kSwiglu>(v, pair(g, g), pair(u, u), acc[0]);
       tmem_load32_begin<256 * kBuffer + 32>(at, v);
       tmem_load32_end(v);
       add_features<kSwiglu>(v, pair(g, g), pair(u, u), acc[1]);
       tmem_load32_begin<256 * kBuffer + 64>(at, v);
       tmem_load32_end(v);
+      if (kStep == 3) {  // the next slot's
+        release_scales();
+        if (more) {
+          wait_scales();
+          load_scales<kSwiglu, 0>(index, wi, row, w0, w1);
+        }
+      }
       add_features<kSwiglu>(v, pair(g, g), pair(u, u), acc[2]);
       tmem_load32_begin<256 * kBuffer + 96>(at, v);
       tmem_load32_end(v);
       release<kBuffer>();
+      look<kBuffer ^ 1>();
       add_features<kSwiglu>(v, pair(g, g), pair(u, u), acc[3]);
     } else {
       release<kBuffer>();
+      look<kBuffer ^ 1>();
+      if (kStep == 3) {
+        release_scales();
+        if (more) wait_scales();
+      }
     }
   }
+  template <bool kSwiglu, int kStep>
+  __device__ __forceinline__ void load_scales(int index, int wi, float& row, float& w0, float& w1) {
+    row = scales[slot * (kSlot / 4) + kStep * kMaxRows + index];
+    w0 = w_scales[slot * 8 + 2 * kStep + wi];
+    if (kSwiglu) w1 = w_scales[slot * 8 + 2 * kStep + 1];
+  }
   template <bool kSwiglu>
-  __device__ __forceinline__ void wide(Pair (&acc)[4][16], uint32_t at, int index, bool some, const float* w_scales) {
+  __device__ __forceinline__ void wide(Pair (&acc)[4][16], uint32_t at, int index, int wi, bool some) {
 #pragma unroll
     for (int c = 0; c < 4; ++c)
 #pragma unroll
       for (int n = 0; n < 16; ++n) acc[c][n] = 0;
+    start();
+    wait_scales();
+    float row, w0, w1;
+    load_scales<kSwiglu, 0>(index, wi, row, w0, w1);
     for (int k = 0; k < steps; k += 4) {
-      wait_scales();
-      const float* from = scales + slot * (kSlot / 4) + index;
-      const float* ws = w_scales + slot * 8;
-      wide_step<kSwiglu, 0>(acc, at, from, ws, some);
-      if (k + 1 < steps) wide_step<kSwiglu, 1>(acc, at, from, ws, some);
-      if (k + 2 < steps) wide_step<kSwiglu, 2>(acc, at, from, ws, some);
-      if (k + 3 < steps) wide_step<kSwiglu, 3>(acc, at, from, ws, some);
-      release_scales();
+      wide_step<kSwiglu, 0>(acc, at, index, wi, some, true, row, w0, w1);
+      if (k + 1 < steps) wide_step<kSwiglu, 1>(acc, at, index, wi, some, true, row, w0, w1);
+      if (k + 2 < steps) wide_step<kSwiglu, 2>(acc, at, index, wi, some, true, row, w0, w1);
+      if (k + 3 < steps) wide_step<kSwiglu, 3>(acc, at, index, wi, some, k + 4 < steps, row, w0, w1);
     }
+    if (steps & 3) release_scales();
   }
 };
 
@@ -372,8 +410,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             const int b = k & mask;
             const uint32_t w = desc + (uint32_t)(stage * (kStage >> 4)), x = w + (kBytesA >> 4);
             const uint32_t m_side = wide ? x : w, n_side = wide ? w : x, d = tmem + (uint32_t)b * stride;
-            if (!(ok = mbar_wait_cta(acc_empty + 8 * b, (phases >> b & 1) ^ 1, a.err))) break;
+            // the later of the two, most often, last
             if (!(ok = mbar_wait_cta(full + 8 * stage, phase, a.err))) break;
+            if (!(ok = mbar_wait_cta(acc_empty + 8 * b, (phases >> b & 1) ^ 1, a.err))) break;
             tc_fence_after();
 #pragma unroll
             for (int j = 0; j < 4; ++j) mma_8bit(d, m_side + 2 * j, n_side + 2 * j, idesc, j > 0);
@@ -405,6 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     sums.acc_full = acc_full, sums.leader_empty = map_rank(acc_empty, 0);
     sums.scale_full = scale_full, sums.scale_empty = scale_empty;
     sums.scales = reinterpret_cast<const float*>(smem + l.scales);
+    sums.w_scales = reinterpret_cast<const float*>(smem + l.w_scales);
     sums.err = a.err, sums.steps = a.steps;
     sums.phases = sums.slot = sums.slot_phase = 0;
     sums.ok = true;
@@ -424,8 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         const int half = columns(tile.groups) / 2, index = (int)rank * half + 32 * w + lane;
         const bool some = 32 * w < half;
         constexpr int kChunks = 4;
-        sums.wide<kSwiglu>(acc, lanes + 128 * set, index, some,
-                           reinterpret_cast<const float*>(smem + l.w_scales) + (kSwiglu ? 0 : set));
+        sums.wide<kSwiglu>(acc, lanes + 128 * set, index, kSwiglu ? 0 : set, some);
         if (!ok) break;
         if (some) {
           const int row = 32 * w + lane < half ? list[index] : -1, neighbour = __shfl_xor_sync(0xffffffffu, row, 1);

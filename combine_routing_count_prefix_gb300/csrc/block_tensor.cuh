@@ -108,22 +108,25 @@ __device__ __forceinline__ bool mbar_wait_cta(uint32_t bar, uint32_t parity, int
     }
   return true;
 }
-// The same for a whole warp that goes on together, on the barrier kOffset bytes
-// further, whose phase is most often complete; once a wait has failed, ok stays
-// false and nothing is waited for.
+// Whether the phase is complete, without waiting; kOffset: bytes from bar.
 template <int kOffset = 0>
-__device__ __forceinline__ void mbar_wait_cta_warp(uint32_t bar, uint32_t parity, bool& ok, int32_t* err) {
+__device__ __forceinline__ uint32_t mbar_test_cta(uint32_t bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1 + %3], %2;\n\t"
-      "vote.sync.all.pred p, p, 0xffffffff;\n\t"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1 + %3], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(done)
       : "r"(bar), "r"(parity), "n"(kOffset)
       : "memory");
-  if (done) return;
-  if (ok) ok = __all_sync(0xffffffffu, mbar_wait_cta(bar + kOffset, parity, err));
+  return done;
+}
+// mbar_wait_cta for a whole warp that goes on together; once a wait has failed, ok
+// stays false and nothing is waited for.  done: an earlier mbar_test_cta's result.
+__device__ __forceinline__ void mbar_wait_cta_warp(uint32_t bar, uint32_t parity, bool& ok, int32_t* err,
+                                                   uint32_t done = 0) {
+  if (__all_sync(0xffffffffu, done)) return;
+  if (ok) ok = __all_sync(0xffffffffu, mbar_wait_cta(bar, parity, err));
 }
 
 // mbar_wait for a whole warp that goes on together: one lane's expiry is all lanes'.
