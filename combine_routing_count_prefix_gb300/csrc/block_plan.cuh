@@ -275,7 +275,7 @@ struct RingBars {
 
 // One thread of each of two warps, on alternate steps: one box of w and those of
 // x's rows per 128 bytes of K.
-template <int kStage, int kBytesA, int kStepValues, bool kSwiglu>
+template <int kStage, int kBytesA, int kStepValues, bool kSwiglu, int kKept>
 __device__ __forceinline__ void load_tiles(const ProductArgs& a, const ProductMaps& maps, uint32_t sbase,
                                            const RingBars& bars, const Tile* tiles, const Box* boxes, bool second,
                                            uint32_t rank, int pair, int pairs, int ntiles) {
@@ -289,7 +289,6 @@ __device__ __forceinline__ void load_tiles(const ProductArgs& a, const ProductMa
     const Tile tile = tiles[slot];
     // the first boxes stay in registers: read from shared memory at every
     // step, each load would wait for its box
-    constexpr int kKept = 6;
     Box kept[kKept];
 #pragma unroll
     for (int b = 0; b < kKept; ++b) kept[b] = b < tile.boxes ? boxes[32 * slot + b] : Box{};

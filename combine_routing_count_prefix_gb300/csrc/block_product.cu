@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
 
   if (warp == 0 || warp == 3) {
     if (elect_one())
-      load_tiles<S::kStage, S::kBytesA, kMx ? 128 : 64, kSwiglu>(a, maps, sbase, bars, tiles, boxes, warp == 3, rank, pair,
+      load_tiles<S::kStage, S::kBytesA, kMx ? 128 : 64, kSwiglu, 6>(a, maps, sbase, bars, tiles, boxes, warp == 3, rank, pair,
                                                                  pairs, ntiles);
   } else if (warp == 1 && leader) {
     // ---- products: one thread -----------------------------------------------------

@@ -32,9 +32,9 @@ namespace {
 
 constexpr int kMaxRows = 256, kNarrowRows = 128, kThreads = 512;
 constexpr int kBytesA = 128 * 128, kBytesB = kMaxRows / 2 * 128, kStage = kBytesA + kBytesB;
-constexpr int kManyRegisters = 200, kFewRegisters = 56;
+constexpr int kManyRegisters = 216, kFewRegisters = 40;
 static_assert(256 * (kManyRegisters + kFewRegisters) <= 65536, "what a launch of 512 threads has");
-constexpr int kBuffers = 4;  // of tensor memory: 4 of 128 columns for narrow tiles, 2 of 256 for wide ones
+constexpr int kBuffers = 4;  // of tensor memory, 128 columns each
 constexpr int kSlots = 2;    // of scales, four steps each
 // A slot: a wide tile's row scales [step][row]; a narrow one's products [step][gate,
 // up][row], the up ones 16 bytes further so that a warp's loads of both do not meet in a bank
@@ -70,29 +70,23 @@ __host__ __device__ inline ScaledSmem scaled_smem(int stages, int E) {
   return l;
 }
 
-// Step k of a tile uses buffer k % 2 (wide) or k % 4; a buffer's phase is a bit of a
-// word that the issuing thread and the summing warps each keep.
+// Step k of a tile uses buffer k % 4 (narrow), or (wide) 2 (k % 2) and the next, one
+// for each set of four warps; a buffer's phase is a bit of a word that the issuing
+// thread and the summing warps each keep.
 __device__ __forceinline__ bool is_wide(const Tile& t) { return t.groups > kNarrowRows / kGroup; }
-
-__device__ __forceinline__ void unpair(const Pair (&p)[16], float (&v)[32]) {
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float2 f = unpair(p[i]);
-    v[2 * i] = f.x, v[2 * i + 1] = f.y;
-  }
-}
 
 // ---------------------------------------------------------------------------
 // narrow tiles: lane = feature, 32 rows in a chunk
 // ---------------------------------------------------------------------------
-// acc += v * scale
-__device__ __forceinline__ void add_rows(const uint32_t (&v)[32], const float* scale, Pair (&acc)[16]) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float4 f = *reinterpret_cast<const float4*>(scale + 4 * j);
-    acc[2 * j] = fma2(pair(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1])), pair(f.x, f.y), acc[2 * j]);
-    acc[2 * j + 1] = fma2(pair(__uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3])), pair(f.z, f.w), acc[2 * j + 1]);
-  }
+// acc += v * scale; scale: shared address
+template <int kOffset, int kColumn = 0>
+__device__ __forceinline__ void add_rows(const uint32_t (&v)[32], uint32_t scale, float (&acc)[32]) {
+  const float4 f = shared_load4<kOffset + 4 * kColumn>(scale);
+  acc[kColumn] = __fmaf_rn(__uint_as_float(v[kColumn]), f.x, acc[kColumn]);
+  acc[kColumn + 1] = __fmaf_rn(__uint_as_float(v[kColumn + 1]), f.y, acc[kColumn + 1]);
+  acc[kColumn + 2] = __fmaf_rn(__uint_as_float(v[kColumn + 2]), f.z, acc[kColumn + 2]);
+  acc[kColumn + 3] = __fmaf_rn(__uint_as_float(v[kColumn + 3]), f.w, acc[kColumn + 3]);
+  if constexpr (kColumn + 4 < 32) add_rows<kOffset, kColumn + 4>(v, scale, acc);
 }
 
 // ---------------------------------------------------------------------------
@@ -100,10 +94,9 @@ __device__ __forceinline__ void add_rows(const uint32_t (&v)[32], const float* s
 // ---------------------------------------------------------------------------
 // acc += v * scale; with SwiGLU the features are eight of gate, eight of up in turn.
 template <bool kSwiglu>
-__device__ __forceinline__ void add_features(const uint32_t (&v)[32], Pair gate, Pair up, Pair (&acc)[16]) {
+__device__ __forceinline__ void add_features(const uint32_t (&v)[32], float gate, float up, float (&acc)[32]) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
-    acc[i] = fma2(pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), kSwiglu && (i & 4) ? up : gate, acc[i]);
+  for (int i = 0; i < 32; ++i) acc[i] = __fmaf_rn(__uint_as_float(v[i]), kSwiglu && (i & 8) ? up : gate, acc[i]);
 }
 
 // 32 bytes of each lane's row to y, `at` bytes into the row: neighbours swap halves,
@@ -153,12 +146,11 @@ __device__ __forceinline__ void store_values(const ProductArgs& a, const float (
 
 // h of a chunk's 16 features.
 template <bool kAccurate>
-__device__ __forceinline__ void swiglu_row(const Pair (&acc)[16], float (&h)[16]) {
+__device__ __forceinline__ void swiglu_row(const float (&acc)[32], float (&h)[16]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float2 g = unpair(acc[i / 4 * 8 + i % 4]), u = unpair(acc[i / 4 * 8 + 4 + i % 4]);
-    h[2 * i] = (kAccurate ? silu(g.x) : near_silu(g.x)) * u.x;
-    h[2 * i + 1] = (kAccurate ? silu(g.y) : near_silu(g.y)) * u.y;
+  for (int i = 0; i < 16; ++i) {
+    const float gate = acc[i / 8 * 16 + i % 8], up = acc[i / 8 * 16 + 8 + i % 8];
+    h[i] = (kAccurate ? silu(gate) : near_silu(gate)) * up;
   }
 }
 
@@ -170,151 +162,172 @@ __device__ __forceinline__ void swiglu_row(const Pair (&acc)[16], float (&h)[16]
 // barrier among them, so a step's are issued during the step before: whether its
 // sums are there, and its scales.  The steps of a slot of scales are unrolled, so
 // that buffers and addresses are constants.
+// (Few registers are left beside a wide tile's 128 sums and 64 loaded ones: so one
+// address for all barriers here, and what is constant of the call from its arguments.)
 struct Sums {
-  uint32_t acc_full, leader_empty, scale_full, scale_empty;
-  const float* scales;
-  const float* w_scales;
-  int32_t* err;
-  int steps;
-  uint32_t phases, slot, slot_phase;
-  uint32_t next_done;  // the next step's sums were there when last looked
+  static constexpr int kScaleFull = 8 * (2 * kBuffers + 2 * kPlanDepth), kScaleEmpty = kScaleFull + 8 * kSlots;
+  static constexpr int kWeightScales = kSlots * kSlot;  // behind the rows'
+  uint32_t acc_full;     // the first barrier; those of the scales are behind it
+  uint32_t leader_empty;
+  uint32_t scales;
+  uint32_t phases, slots;  // of buffers; slots of scales used
+  uint32_t next_done;      // the next step's sums were there when last looked
   bool ok;
 
-  // The first step's of a tile.
-  __device__ __forceinline__ void start() { next_done = 0; }
-  template <int kBuffer>
-  __device__ __forceinline__ void wait() {
-    mbar_wait_cta_warp(acc_full + 8 * kBuffer, phases >> kBuffer & 1, ok, err, next_done);
-    phases ^= 1u << kBuffer;
+  // kBuffer: from the warp's first buffer on, whose barriers are full, empty and
+  // whose phase bit is `first` (a wide tile's come in pairs, one for each set: kPair).
+  template <int kBuffer, bool kPair>
+  __device__ __forceinline__ void wait(const ProductArgs& a, uint32_t full, int first) {
+    mbar_wait_cta_warp(full + 8 * kBuffer, phases >> (first + kBuffer) & 1, ok, a.err, next_done);
+    phases ^= (kPair ? 3u : 1u) << kBuffer;
     tc_fence_after();
   }
   template <int kBuffer>
-  __device__ __forceinline__ void look() {
-    next_done = mbar_test_cta<8 * kBuffer>(acc_full, phases >> kBuffer & 1);
+  __device__ __forceinline__ void look(uint32_t full, int first) {
+    next_done = mbar_test_cta<8 * kBuffer>(full, phases >> (first + kBuffer) & 1);
   }
-  // this warp has read the buffer
-  template <int kBuffer>
-  __device__ __forceinline__ void release() {
+  // this warp has read the buffer; kCount: of the barrier's 16 arrivals
+  template <int kBuffer, int kCount>
+  __device__ __forceinline__ void release(uint32_t empty) {
     tc_fence_before();
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive_peer(leader_empty + 8 * kBuffer);
+    if ((threadIdx.x & 31) == 0) mbar_arrive_peer<kCount>(empty + 8 * kBuffer);
   }
-  __device__ __forceinline__ void wait_scales() { mbar_wait_cta_warp(scale_full + 8 * slot, slot_phase, ok, err); }
+  static_assert(kSlots == 2, "slots alternate");
+  __device__ __forceinline__ uint32_t slot() const { return slots & 1; }
+  __device__ __forceinline__ void wait_scales(const ProductArgs& a, uint32_t done = 0) {
+    mbar_wait_cta_warp(acc_full + kScaleFull + 8 * slot(), slots >> 1 & 1, ok, a.err, done);
+  }
+  __device__ __forceinline__ uint32_t look_scales() const {  // the next slot's
+    return mbar_test_cta<kScaleFull>(acc_full + 8 * (slot() ^ 1), (slots + 1) >> 1 & 1);
+  }
   __device__ __forceinline__ void release_scales() {
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(scale_empty + 8 * slot);
-    slot ^= 1;
-    slot_phase ^= slot ^ 1;
-    static_assert(kSlots == 2, "slots alternate");
+    if ((threadIdx.x & 31) == 0) mbar_arrive(acc_full + kScaleEmpty + 8 * slot());
+    ++slots;
   }
 
   // Narrow: kChunks times 32 rows, 64 columns apart from address `at` on in buffer 0;
-  // scale: their place in a step's scales.
+  // scale: their place in the slot's scales.
   template <int kChunks, int kStep>
-  __device__ __forceinline__ void narrow_step(Pair (&acc)[4][16], uint32_t at, const float* scale) {
-    wait<kStep>();
-#pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
+  __device__ __forceinline__ void narrow_step(const ProductArgs& a, float (&acc)[4][32], uint32_t at, uint32_t scale) {
+    constexpr int kScale = 4 * 2 * kStep * kNarrowStride, kNext = (kStep + 1) % kBuffers;
+    wait<kStep, false>(a, acc_full, 0);
+    if constexpr (kChunks > 0) {
       uint32_t v[32];
-      if (c == 0)
-        tmem_load32_begin<128 * kStep>(at, v);
-      else
-        tmem_load32_begin<128 * kStep + 64>(at, v);
+      tmem_load32_begin<128 * kStep>(at, v);
       tmem_load32_end(v);
-      if (c + 1 == kChunks) {
-        release<kStep>();
-        look<(kStep + 1) % kBuffers>();
+      if (kChunks == 1) {
+        release<kStep, 1>(leader_empty);
+        look<kNext>(acc_full, 0);
       }
-      add_rows(v, scale + 2 * kStep * kNarrowStride + 64 * c, acc[c]);
+      add_rows<kScale>(v, scale, acc[0]);
     }
-    if (kChunks == 0) {
-      release<kStep>();
-      look<(kStep + 1) % kBuffers>();
+    if constexpr (kChunks > 1) {
+      uint32_t v[32];
+      tmem_load32_begin<128 * kStep + 64>(at, v);
+      tmem_load32_end(v);
+      release<kStep, 1>(leader_empty);
+      look<kNext>(acc_full, 0);
+      add_rows<kScale + 256>(v, scale, acc[1]);
+    }
+    if constexpr (kChunks == 0) {
+      release<kStep, 1>(leader_empty);
+      look<kNext>(acc_full, 0);
     }
   }
   template <int kChunks>
-  __device__ __forceinline__ void narrow(Pair (&acc)[4][16], uint32_t at, int scale) {
+  __device__ __forceinline__ void narrow(const ProductArgs& a, float (&acc)[4][32], uint32_t at, uint32_t scale) {
 #pragma unroll
     for (int c = 0; c < kChunks; ++c)
 #pragma unroll
-      for (int n = 0; n < 16; ++n) acc[c][n] = 0;
-    start();
-    for (int k = 0; k < steps; k += 4) {
-      wait_scales();
-      const float* from = scales + slot * (kSlot / 4) + scale;
-      narrow_step<kChunks, 0>(acc, at, from);
-      if (k + 1 < steps) narrow_step<kChunks, 1>(acc, at, from);
-      if (k + 2 < steps) narrow_step<kChunks, 2>(acc, at, from);
-      if (k + 3 < steps) narrow_step<kChunks, 3>(acc, at, from);
+      for (int n = 0; n < 32; ++n) acc[c][n] = 0;
+    next_done = 0;
+    for (int k = 0; k < a.steps; k += 4) {
+      wait_scales(a);
+      const uint32_t from = scales + slot() * kSlot + scale;
+      narrow_step<kChunks, 0>(a, acc, at, from);
+      if (k + 1 < a.steps) narrow_step<kChunks, 1>(a, acc, at, from);
+      if (k + 2 < a.steps) narrow_step<kChunks, 2>(a, acc, at, from);
+      if (k + 3 < a.steps) narrow_step<kChunks, 3>(a, acc, at, from);
       release_scales();
     }
   }
 
-  // Wide: 128 features from address `at` on in buffer 0; index: the row's place in a
-  // step's scales, some: whether the warp has rows at all; wi: which of a step's two
-  // scales of w is the features' (SwiGLU: 0 gate, 1 up).  row, w0, w1: the step's scales.
+  // Wide: the set's 128 features from address `at` on in buffer 0; row: the place of the
+  // thread's row in a slot's scales, some: whether the warp has rows at all; s: the
+  // step's scales: the row's, and w's for gate and up with SwiGLU, or for the first
+  // and the last 64 features.
+  struct Scales {
+    float row;
+    float2 w;
+  };
+  template <int kStep>
+  __device__ __forceinline__ void load_scales(uint32_t row, Scales& s) const {
+    s.row = shared_load<4 * kStep * kMaxRows>(row + slot() * kSlot);
+    s.w = shared_load2<kWeightScales + 8 * kStep>(scales + slot() * 32);
+  }
   template <bool kSwiglu, int kStep>
-  __device__ __forceinline__ void wide_step(Pair (&acc)[4][16], uint32_t at, int index, int wi, bool some, bool more,
-                                            float& row, float& w0, float& w1) {
-    constexpr int kBuffer = kStep & 1;
-    wait<kBuffer>();
+  __device__ __forceinline__ void wide_step(const ProductArgs& a, float (&acc)[4][32], uint32_t at, int set, uint32_t row,
+                                            bool some, bool more, Scales& s, uint32_t& scales_done) {
+    constexpr int kBuffer = 2 * (kStep & 1), kNext = kBuffer ^ 2;
+    const uint32_t full = acc_full + 8 * set, empty = leader_empty + 8 * set;
+    wait<kBuffer, true>(a, full, set);
     if (some) {
-      uint32_t v[32];
-      tmem_load32_begin<256 * kBuffer>(at, v);
-      const float g = row * w0, u = kSwiglu ? row * w1 : 0;
-      tmem_load32_end(v);
-      if (kStep < 3) load_scales<kSwiglu, (kStep + 1) % 4>(index, wi, row, w0, w1);
-      add_features<kSwiglu>(v, pair(g, g), pair(u, u), acc[0]);
-      tmem_load32_begin<256 * kBuffer + 32>(at, v);
-      tmem_load32_end(v);
-      add_features<kSwiglu>(v, pair(g, g), pair(u, u), acc[1]);
-      tmem_load32_begin<256 * kBuffer + 64>(at, v);
-      tmem_load32_end(v);
+      // 32 columns load while the last 32 are added
+      uint32_t v[2][32];
+      tmem_load32_begin<128 * kBuffer>(at, v[0]);
+      const float g = s.row * s.w.x, u = s.row * s.w.y;
+      tmem_load32_end(v[0]);
+      tmem_load32_begin<128 * kBuffer + 32>(at, v[1]);
+      add_features<kSwiglu>(v[0], g, u, acc[0]);
+      if (kStep < 3) load_scales<(kStep + 1) % 4>(row, s);
+      if (kStep == 2) scales_done = look_scales();
+      tmem_load32_end(v[1]);
+      tmem_load32_begin<128 * kBuffer + 64>(at, v[0]);
+      add_features<kSwiglu>(v[1], g, u, acc[1]);
+      tmem_load32_end(v[0]);
+      tmem_load32_begin<128 * kBuffer + 96>(at, v[1]);
+      add_features<kSwiglu>(v[0], kSwiglu ? g : u, u, acc[2]);
+      tmem_load32_end(v[1]);
+      release<kBuffer, 2>(empty);
+      look<kNext>(full, set);
       if (kStep == 3) {  // the next slot's
         release_scales();
         if (more) {
-          wait_scales();
-          load_scales<kSwiglu, 0>(index, wi, row, w0, w1);
+          wait_scales(a, scales_done);
+          load_scales<0>(row, s);
         }
       }
-      add_features<kSwiglu>(v, pair(g, g), pair(u, u), acc[2]);
-      tmem_load32_begin<256 * kBuffer + 96>(at, v);
-      tmem_load32_end(v);
-      release<kBuffer>();
-      look<kBuffer ^ 1>();
-      add_features<kSwiglu>(v, pair(g, g), pair(u, u), acc[3]);
+      add_features<kSwiglu>(v[1], kSwiglu ? g : u, u, acc[3]);
     } else {
-      release<kBuffer>();
-      look<kBuffer ^ 1>();
+      release<kBuffer, 2>(empty);
+      look<kNext>(full, set);
       if (kStep == 3) {
         release_scales();
-        if (more) wait_scales();
+        if (more) wait_scales(a);
       }
     }
   }
-  template <bool kSwiglu, int kStep>
-  __device__ __forceinline__ void load_scales(int index, int wi, float& row, float& w0, float& w1) {
-    row = scales[slot * (kSlot / 4) + kStep * kMaxRows + index];
-    w0 = w_scales[slot * 8 + 2 * kStep + wi];
-    if (kSwiglu) w1 = w_scales[slot * 8 + 2 * kStep + 1];
-  }
   template <bool kSwiglu>
-  __device__ __forceinline__ void wide(Pair (&acc)[4][16], uint32_t at, int index, int wi, bool some) {
+  __device__ __forceinline__ void wide(const ProductArgs& a, float (&acc)[4][32], uint32_t at, int set, uint32_t row,
+                                       bool some) {
 #pragma unroll
     for (int c = 0; c < 4; ++c)
 #pragma unroll
-      for (int n = 0; n < 16; ++n) acc[c][n] = 0;
-    start();
-    wait_scales();
-    float row, w0, w1;
-    load_scales<kSwiglu, 0>(index, wi, row, w0, w1);
-    for (int k = 0; k < steps; k += 4) {
-      wide_step<kSwiglu, 0>(acc, at, index, wi, some, true, row, w0, w1);
-      if (k + 1 < steps) wide_step<kSwiglu, 1>(acc, at, index, wi, some, true, row, w0, w1);
-      if (k + 2 < steps) wide_step<kSwiglu, 2>(acc, at, index, wi, some, true, row, w0, w1);
-      if (k + 3 < steps) wide_step<kSwiglu, 3>(acc, at, index, wi, some, k + 4 < steps, row, w0, w1);
+      for (int n = 0; n < 32; ++n) acc[c][n] = 0;
+    next_done = 0;
+    wait_scales(a);
+    Scales s;
+    uint32_t done = 0;
+    load_scales<0>(row, s);
+    for (int k = 0; k < a.steps; k += 4) {
+      wide_step<kSwiglu, 0>(a, acc, at, set, row, some, true, s, done);
+      if (k + 1 < a.steps) wide_step<kSwiglu, 1>(a, acc, at, set, row, some, true, s, done);
+      if (k + 2 < a.steps) wide_step<kSwiglu, 2>(a, acc, at, set, row, some, true, s, done);
+      if (k + 3 < a.steps) wide_step<kSwiglu, 3>(a, acc, at, set, row, some, k + 4 < a.steps, s, done);
     }
-    if (steps & 3) release_scales();
+    if (a.steps & 3) release_scales();
   }
 };
 
@@ -386,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     fewer_registers<kFewRegisters>();
     if (warp == 0 || warp == 3) {
       if (elect_one())
-        load_tiles<kStage, kBytesA, 128, kSwiglu>(a, maps, sbase, bars, tiles, boxes, warp == 3, rank, pair_id, pairs,
+        load_tiles<kStage, kBytesA, 128, kSwiglu, 4>(a, maps, sbase, bars, tiles, boxes, warp == 3, rank, pair_id, pairs,
                                                   ntiles);
     } else if (warp == 1) {
       // ---- products: one thread -----------------------------------------------------
@@ -400,25 +413,36 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           if (!(ok = mbar_wait_cta(plan_full + 8 * slot, (i / kPlanDepth) & 1, a.err))) break;
           const bool was_wide = wide;
           wide = is_wide(tiles[slot]);
-          const uint32_t n = wide ? kTileFeatures : columns(tiles[slot].groups), idesc = a.idesc | (n >> 3) << 17;
-          const int mask = wide ? 1 : kBuffers - 1;
-          const uint32_t stride = wide ? 256 : 128;
+          const uint32_t n = wide ? 128 : columns(tiles[slot].groups), idesc = a.idesc | (n >> 3) << 17;
           mbar_arrive(plan_empty + 8 * slot);
-          if (wide != was_wide)  // other columns: every buffer has to be handed back
+          if (wide != was_wide)  // other warps hand the buffers back: all of them have to be free
             for (int b = 0; b < kBuffers && ok; ++b) ok = mbar_wait_cta(acc_empty + 8 * b, (phases >> b & 1) ^ 1, a.err);
           for (int k = 0; k < a.steps && ok; ++k) {
-            const int b = k & mask;
             const uint32_t w = desc + (uint32_t)(stage * (kStage >> 4)), x = w + (kBytesA >> 4);
-            const uint32_t m_side = wide ? x : w, n_side = wide ? w : x, d = tmem + (uint32_t)b * stride;
-            // the later of the two, most often, last
             if (!(ok = mbar_wait_cta(full + 8 * stage, phase, a.err))) break;
-            if (!(ok = mbar_wait_cta(acc_empty + 8 * b, (phases >> b & 1) ^ 1, a.err))) break;
-            tc_fence_after();
+            if (wide) {  // a product for each set's 128 features, 64 of each CTA's
 #pragma unroll
-            for (int j = 0; j < 4; ++j) mma_8bit(d, m_side + 2 * j, n_side + 2 * j, idesc, j > 0);
-            mma_commit_pair(acc_full + 8 * b);
+              for (int h = 0; h < 2; ++h) {
+                const int b = 2 * (k & 1) + h;
+                if (!(ok = mbar_wait_cta(acc_empty + 8 * b, (phases >> b & 1) ^ 1, a.err))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  mma_8bit(tmem + 128 * b, x + 2 * j, w + h * (64 * 128 >> 4) + 2 * j, idesc, j > 0);
+                mma_commit_pair(acc_full + 8 * b);
+                phases ^= 1u << b;
+              }
+              if (!ok) break;
+            } else {
+              const int b = k & (kBuffers - 1);
+              if (!(ok = mbar_wait_cta(acc_empty + 8 * b, (phases >> b & 1) ^ 1, a.err))) break;
+              tc_fence_after();
+#pragma unroll
+              for (int j = 0; j < 4; ++j) mma_8bit(tmem + 128 * b, w + 2 * j, x + 2 * j, idesc, j > 0);
+              mma_commit_pair(acc_full + 8 * b);
+              phases ^= 1u << b;
+            }
             mma_commit_pair(empty + 8 * stage);
-            phases ^= 1u << b;
             if (++stage == a.stages) stage = 0, phase ^= 1;
           }
         }
@@ -442,11 +466,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     const int w = warp & 3, set = warp >= 8;
     Sums sums;
     sums.acc_full = acc_full, sums.leader_empty = map_rank(acc_empty, 0);
-    sums.scale_full = scale_full, sums.scale_empty = scale_empty;
-    sums.scales = reinterpret_cast<const float*>(smem + l.scales);
-    sums.w_scales = reinterpret_cast<const float*>(smem + l.w_scales);
-    sums.err = a.err, sums.steps = a.steps;
-    sums.phases = sums.slot = sums.slot_phase = 0;
+    sums.scales = sbase + l.scales;
+    sums.phases = sums.slots = 0;
     sums.ok = true;
     bool& ok = sums.ok;
     int i = 0, narrow_tiles = 0, wide_tiles = 0;
@@ -456,27 +477,25 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       if (!ok) break;
       uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16);
       asm volatile("" : "+r"(lanes));  // not kept, with sums of it, from tile to tile
-      Pair acc[4][16];  // one for both kinds of tile: with an array each 1.4 KB of registers spill
+      float acc[4][32];  // one for both kinds of tile: with an array each 1.4 KB of registers spill
       const Tile tile = tiles[slot];
       const int* list = rows + slot * kMaxRows;
       if (is_wide(tile)) {
-        // set: which CTA's 128 features.  Rows: the pair's halves of the list.
+        // set: which half of each CTA's features.  Rows: the pair's halves of the list.
         const int half = columns(tile.groups) / 2, index = (int)rank * half + 32 * w + lane;
         const bool some = 32 * w < half;
         constexpr int kChunks = 4;
-        sums.wide<kSwiglu>(acc, lanes + 128 * set, index, kSwiglu ? 0 : set, some);
+        sums.wide<kSwiglu>(a, acc, lanes + 128 * set, set, sums.scales + 4 * index, some);
         if (!ok) break;
         if (some) {
           const int row = 32 * w + lane < half ? list[index] : -1, neighbour = __shfl_xor_sync(0xffffffffu, row, 1);
           if constexpr (!kSwiglu) {
 #pragma unroll
             for (int c = 0; c < kChunks; ++c) {
-              float v[32];
-              unpair(acc[c], v);
-              store_values(a, v, tile.block * kTileFeatures + 128 * set + 32 * c, row, neighbour);
+              store_values(a, acc[c], tile.block * kTileFeatures + c / 2 * 128 + 64 * set + c % 2 * 32, row, neighbour);
             }
           } else {
-            const int first = tile.block * 128 + 64 * set;
+            const int first = tile.block * 128 + 32 * set;  // and 64 further
             if (a.out_dtype != LLMOE_DTYPE_FP8B) {
 #pragma unroll
               for (int c = 0; c < kChunks; ++c) {
@@ -485,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                   swiglu_row<true>(acc[c], h);
                 else
                   swiglu_row<false>(acc[c], h);
-                store_values(a, h, first + 16 * c, row, neighbour);
+                store_values(a, h, first + c / 2 * 64 + c % 2 * 16, row, neighbour);
               }
             } else {
               // a row's block of 128 outputs is this thread's and the other set's
@@ -517,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                            pack_e4m3x2(h[c + n][4 * m + 2] * inverse, h[c + n][4 * m + 3] * inverse) << 16;
                   q[n] = make_uint4(b[0], b[1], b[2], b[3]);
                 }
-                store_pieces(a, q[0], q[1], row, neighbour, first + 16 * c, a.out);
+                store_pieces(a, q[0], q[1], row, neighbour, first + 32 * c, a.out);
               }
               if (set == 0 && row >= 0) {
                 uint8_t* at = in_row(a, a.y + a.out + 4 * tile.block, row);
@@ -533,13 +552,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         // set: every other 32 rows
         const int chunks = (columns(tile.groups) / 32 + 1 - set) / 2, up = kSwiglu ? lane >> 3 & 1 : 0;
         constexpr int kChunks = kNarrowRows / 64;
-        const int scale = up * kNarrowStride + 32 * set;
+        const uint32_t scale = 4 * (up * kNarrowStride + 32 * set);
         if (chunks == 2)
-          sums.narrow<2>(acc, lanes + 32 * set, scale);
+          sums.narrow<2>(a, acc, lanes + 32 * set, scale);
         else if (chunks == 1)
-          sums.narrow<1>(acc, lanes + 32 * set, scale);
+          sums.narrow<1>(a, acc, lanes + 32 * set, scale);
         else
-          sums.narrow<0>(acc, lanes + 32 * set, scale);
+          sums.narrow<0>(a, acc, lanes + 32 * set, scale);
         static_assert(kChunks == 2, "all numbers of chunks");
         if (!ok) break;
         list += 32 * set;
@@ -549,12 +568,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll
           for (int c = 0; c < kChunks; ++c)
             if (c < chunks) {
-              float v[32];
-              unpair(acc[c], v);
               if constexpr (kSwiglu)
-                store_swiglu_values(a, v, first, list + 64 * c);
+                store_swiglu_values(a, acc[c], first, list + 64 * c);
               else
-                store_plain(a, v, first, list + 64 * c);
+                store_plain(a, acc[c], first, list + 64 * c);
             }
         } else {
           // a block of 128 outputs is the pair's: its eight warps of this set swap
@@ -567,9 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll
           for (int c = 0; c < kChunks; ++c)
             if (c < chunks) {
-              float v[32];
-              unpair(acc[c], v);
-              swiglu_columns(v, h[c]);
+              swiglu_columns(acc[c], h[c]);
               int at;
               const uint32_t most = largest_of_columns(h[c], at);
               const int column = 64 * c + 2 * at + up;
@@ -625,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     // tile's list, 16 bytes of a row (four steps) at a time, kAhead such chunks
     // ahead; and lane % 4 w's of a step, for the first or (lane & 4) the second of:
     // gate and up; a wide tile's two CTAs' features.
-    constexpr int kAhead = 3;
+    constexpr int kAhead = 1;
     const int q = warp & 3, chunks = (a.steps + 3) / 4;
     int i = 0, sslot = 0;
     uint32_t sphase = 0;

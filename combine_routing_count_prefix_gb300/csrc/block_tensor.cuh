@@ -51,8 +51,9 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
 // that loads ahead).  Its uses need none: tensor memory that has been read, and
 // shared memory that only the tensor core of this SM reads, which the writers'
 // fence_async_shared has made visible to it.
+template <int kCount = 1>
 __device__ __forceinline__ void mbar_arrive_peer(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "n"(kCount) : "memory");
 }
 // The same with what this thread wrote to the cluster's shared memory before it,
 // for a peer's thread that waits on the barrier.
@@ -208,6 +209,26 @@ __device__ __forceinline__ void tmem_load32_end(uint32_t (&v)[32]) {
                : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
                :
                : "memory");
+}
+template <int kOffset>
+__device__ __forceinline__ float shared_load(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cta.f32 %0, [%1 + %2];" : "=f"(v) : "r"(addr), "n"(kOffset));
+  return v;
+}
+template <int kOffset>
+__device__ __forceinline__ float2 shared_load2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cta.v2.f32 {%0, %1}, [%2 + %3];" : "=f"(v.x), "=f"(v.y) : "r"(addr), "n"(kOffset));
+  return v;
+}
+template <int kOffset>
+__device__ __forceinline__ float4 shared_load4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cta.v4.f32 {%0, %1, %2, %3}, [%4 + %5];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr), "n"(kOffset));
+  return v;
 }
 __device__ __forceinline__ void shared_store_peer(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
