@@ -32,15 +32,14 @@ namespace {
 
 constexpr int kMaxRows = 256, kNarrowRows = 128, kThreads = 512;
 constexpr int kBytesA = 128 * 128, kBytesB = kMaxRows / 2 * 128, kStage = kBytesA + kBytesB;
-constexpr int kManyRegisters = 216, kFewRegisters = 40;
+constexpr int kManyRegisters = 200, kFewRegisters = 56;
 static_assert(256 * (kManyRegisters + kFewRegisters) <= 65536, "what a launch of 512 threads has");
-constexpr int kBuffers = 4;  // of tensor memory, 128 columns each
+constexpr int kBuffers = 4;  // of tensor memory, 128 columns each; wide tiles take two of 256
 constexpr int kSlots = 2;    // of scales, four steps each
-// A slot: a wide tile's row scales [step][row]; a narrow one's products [step][gate,
-// up][row], the up ones 16 bytes further so that a warp's loads of both do not meet in a bank
+// A slot: a narrow tile's products of scales [step][gate, up][row], the up ones 16
+// bytes further so that a warp's loads of both do not meet in a bank
 constexpr int kNarrowStride = kNarrowRows + 4;
 constexpr int kSlot = 4 * 2 * kNarrowStride * 4;
-static_assert(2 * kNarrowStride >= kMaxRows, "wide tiles fit too");
 
 struct ScaledArgs {
   ProductArgs p;
@@ -50,13 +49,12 @@ struct ScaledArgs {
 
 // Byte offsets in dynamic shared memory, from its first 1024-byte boundary.
 struct ScaledSmem {
-  uint32_t scales, w_scales, amax, row_max, boxes, rows, tiles, bars, tmem, part, prefix, total;
+  uint32_t scales, amax, row_max, boxes, rows, tiles, bars, tmem, part, prefix, total;
 };
 __host__ __device__ inline ScaledSmem scaled_smem(int stages, int E) {
   ScaledSmem l;
   uint32_t at = stages * kStage;
   l.scales = at, at += kSlots * kSlot;
-  l.w_scales = at, at += kSlots * 4 * 2 * 4;
   l.amax = at, at += 8 * kNarrowRows * 4;   // narrow: [warp of the pair's set][row]
   l.row_max = at, at += 2 * 2 * 128 * 4;    // wide: [tile's parity][set][row]
   l.boxes = at, at += kPlanDepth * 32 * 16;
@@ -70,10 +68,18 @@ __host__ __device__ inline ScaledSmem scaled_smem(int stages, int E) {
   return l;
 }
 
-// Step k of a tile uses buffer k % 4 (narrow), or (wide) 2 (k % 2) and the next, one
-// for each set of four warps; a buffer's phase is a bit of a word that the issuing
-// thread and the summing warps each keep.
+// Step k of a tile uses buffer k % 4 (narrow) or k % 2 (wide, two buffers' columns); a
+// buffer's phase is a bit of a word that the issuing thread and the summing warps keep.
 __device__ __forceinline__ bool is_wide(const Tile& t) { return t.groups > kNarrowRows / kGroup; }
+
+// The scales of w for a tile's gate (part 0) or up features, or for those of the
+// pair's first or second CTA: one for each step.  Past the last block of features,
+// where nothing is stored, the last one's.
+template <bool kSwiglu>
+__device__ __forceinline__ const float* weight_scales(const ScaledArgs& s, const Tile& tile, int part) {
+  const int64_t matrix = kSwiglu ? 2 * (int64_t)tile.expert + part : tile.expert;
+  return s.w_scale + (matrix * s.down + (kSwiglu ? tile.block : min(2 * tile.block + part, s.down - 1))) * (int64_t)s.across;
+}
 
 // ---------------------------------------------------------------------------
 // narrow tiles: lane = feature, 32 rows in a chunk
@@ -166,7 +172,6 @@ __device__ __forceinline__ void swiglu_row(const float (&acc)[32], float (&h)[16
 // address for all barriers here, and what is constant of the call from its arguments.)
 struct Sums {
   static constexpr int kScaleFull = 8 * (2 * kBuffers + 2 * kPlanDepth), kScaleEmpty = kScaleFull + 8 * kSlots;
-  static constexpr int kWeightScales = kSlots * kSlot;  // behind the rows'
   uint32_t acc_full;     // the first barrier; those of the scales are behind it
   uint32_t leader_empty;
   uint32_t scales;
@@ -174,32 +179,30 @@ struct Sums {
   uint32_t next_done;      // the next step's sums were there when last looked
   bool ok;
 
-  // kBuffer: from the warp's first buffer on, whose barriers are full, empty and
-  // whose phase bit is `first` (a wide tile's come in pairs, one for each set: kPair).
-  template <int kBuffer, bool kPair>
-  __device__ __forceinline__ void wait(const ProductArgs& a, uint32_t full, int first) {
-    mbar_wait_cta_warp(full + 8 * kBuffer, phases >> (first + kBuffer) & 1, ok, a.err, next_done);
-    phases ^= (kPair ? 3u : 1u) << kBuffer;
+  // ok is a lane's own until the tile's end: a vote in every step took 4% of a dense call.
+  template <int kBuffer>
+  __device__ __forceinline__ void wait(const ProductArgs& a) {
+    if (!next_done && ok) ok = mbar_wait_cta(acc_full + 8 * kBuffer, phases >> kBuffer & 1, a.err);
+    __syncwarp();
+    phases ^= 1u << kBuffer;
     tc_fence_after();
   }
   template <int kBuffer>
-  __device__ __forceinline__ void look(uint32_t full, int first) {
-    next_done = mbar_test_cta<8 * kBuffer>(full, phases >> (first + kBuffer) & 1);
+  __device__ __forceinline__ void look() {
+    next_done = mbar_test_cta<8 * kBuffer>(acc_full, phases >> kBuffer & 1);
   }
-  // this warp has read the buffer; kCount: of the barrier's 16 arrivals
-  template <int kBuffer, int kCount>
-  __device__ __forceinline__ void release(uint32_t empty) {
+  // this warp has read the buffer
+  template <int kBuffer>
+  __device__ __forceinline__ void release() {
     tc_fence_before();
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive_peer<kCount>(empty + 8 * kBuffer);
+    if ((threadIdx.x & 31) == 0) mbar_arrive_peer(leader_empty + 8 * kBuffer);
   }
   static_assert(kSlots == 2, "slots alternate");
   __device__ __forceinline__ uint32_t slot() const { return slots & 1; }
-  __device__ __forceinline__ void wait_scales(const ProductArgs& a, uint32_t done = 0) {
-    mbar_wait_cta_warp(acc_full + kScaleFull + 8 * slot(), slots >> 1 & 1, ok, a.err, done);
-  }
-  __device__ __forceinline__ uint32_t look_scales() const {  // the next slot's
-    return mbar_test_cta<kScaleFull>(acc_full + 8 * (slot() ^ 1), (slots + 1) >> 1 & 1);
+  __device__ __forceinline__ void wait_scales(const ProductArgs& a) {
+    if (ok) ok = mbar_wait_cta(acc_full + kScaleFull + 8 * slot(), slots >> 1 & 1, a.err);
+    __syncwarp();
   }
   __device__ __forceinline__ void release_scales() {
     __syncwarp();
@@ -212,14 +215,14 @@ struct Sums {
   template <int kChunks, int kStep>
   __device__ __forceinline__ void narrow_step(const ProductArgs& a, float (&acc)[4][32], uint32_t at, uint32_t scale) {
     constexpr int kScale = 4 * 2 * kStep * kNarrowStride, kNext = (kStep + 1) % kBuffers;
-    wait<kStep, false>(a, acc_full, 0);
+    wait<kStep>(a);
     if constexpr (kChunks > 0) {
       uint32_t v[32];
       tmem_load32_begin<128 * kStep>(at, v);
       tmem_load32_end(v);
       if (kChunks == 1) {
-        release<kStep, 1>(leader_empty);
-        look<kNext>(acc_full, 0);
+        release<kStep>();
+        look<kNext>();
       }
       add_rows<kScale>(v, scale, acc[0]);
     }
@@ -227,13 +230,13 @@ struct Sums {
       uint32_t v[32];
       tmem_load32_begin<128 * kStep + 64>(at, v);
       tmem_load32_end(v);
-      release<kStep, 1>(leader_empty);
-      look<kNext>(acc_full, 0);
+      release<kStep>();
+      look<kNext>();
       add_rows<kScale + 256>(v, scale, acc[1]);
     }
     if constexpr (kChunks == 0) {
-      release<kStep, 1>(leader_empty);
-      look<kNext>(acc_full, 0);
+      release<kStep>();
+      look<kNext>();
     }
   }
   template <int kChunks>
@@ -254,80 +257,74 @@ struct Sums {
     }
   }
 
-  // Wide: the set's 128 features from address `at` on in buffer 0; row: the place of the
-  // thread's row in a slot's scales, some: whether the warp has rows at all; s: the
-  // step's scales: the row's, and w's for gate and up with SwiGLU, or for the first
-  // and the last 64 features.
+  // Wide: the set's 128 features from address `at` on in buffer 0; some: whether the
+  // warp has rows at all.  A thread reads its row's scales from memory itself, four
+  // steps at a time and four ahead, and w's of a step with a lane each.
   struct Scales {
-    float row;
-    float2 w;
+    const float4* row;   // of the thread's row
+    const float* w;      // of step lane % 4: gate or up with SwiGLU, or the first or the last 64 features (lane / 4 % 2)
+    float4 now, next;    // of four steps and the next four
+    float w_now, w_next;
+    float r, w0, w1;     // the step's
+    __device__ __forceinline__ void load(int k, int steps) {
+      next = make_float4(0, 0, 0, 0), w_next = 0;
+      if (k < steps) next = row[k >> 2];
+      if (k + (int)(threadIdx.x & 3) < steps) w_next = w[k];
+    }
+    template <int kStep, bool kBoth>
+    __device__ __forceinline__ void take(int kFirst) {
+      r = kStep == 0 ? now.x : kStep == 1 ? now.y : kStep == 2 ? now.z : now.w;
+      w0 = __shfl_sync(0xffffffffu, w_now, kFirst + kStep);
+      if (kBoth) w1 = __shfl_sync(0xffffffffu, w_now, 4 + kStep);
+    }
   };
-  template <int kStep>
-  __device__ __forceinline__ void load_scales(uint32_t row, Scales& s) const {
-    s.row = shared_load<4 * kStep * kMaxRows>(row + slot() * kSlot);
-    s.w = shared_load2<kWeightScales + 8 * kStep>(scales + slot() * 32);
-  }
   template <bool kSwiglu, int kStep>
-  __device__ __forceinline__ void wide_step(const ProductArgs& a, float (&acc)[4][32], uint32_t at, int set, uint32_t row,
-                                            bool some, bool more, Scales& s, uint32_t& scales_done) {
-    constexpr int kBuffer = 2 * (kStep & 1), kNext = kBuffer ^ 2;
-    const uint32_t full = acc_full + 8 * set, empty = leader_empty + 8 * set;
-    wait<kBuffer, true>(a, full, set);
+  __device__ __forceinline__ void wide_step(const ProductArgs& a, float (&acc)[4][32], uint32_t at, int set, bool some,
+                                            Scales& s) {
+    constexpr int kBuffer = kStep & 1, kNext = kBuffer ^ 1;
+    wait<kBuffer>(a);
     if (some) {
       // 32 columns load while the last 32 are added
       uint32_t v[2][32];
-      tmem_load32_begin<128 * kBuffer>(at, v[0]);
-      const float g = s.row * s.w.x, u = s.row * s.w.y;
+      tmem_load32_begin<256 * kBuffer>(at, v[0]);
+      const float g = s.r * s.w0, u = kSwiglu ? s.r * s.w1 : g;
       tmem_load32_end(v[0]);
-      tmem_load32_begin<128 * kBuffer + 32>(at, v[1]);
+      tmem_load32_begin<256 * kBuffer + 32>(at, v[1]);
       add_features<kSwiglu>(v[0], g, u, acc[0]);
-      if (kStep < 3) load_scales<(kStep + 1) % 4>(row, s);
-      if (kStep == 2) scales_done = look_scales();
+      if (kStep == 3) s.now = s.next, s.w_now = s.w_next;
+      s.take<(kStep + 1) % 4, kSwiglu>(kSwiglu ? 0 : 4 * set);
       tmem_load32_end(v[1]);
-      tmem_load32_begin<128 * kBuffer + 64>(at, v[0]);
+      tmem_load32_begin<256 * kBuffer + 64>(at, v[0]);
       add_features<kSwiglu>(v[1], g, u, acc[1]);
       tmem_load32_end(v[0]);
-      tmem_load32_begin<128 * kBuffer + 96>(at, v[1]);
-      add_features<kSwiglu>(v[0], kSwiglu ? g : u, u, acc[2]);
+      tmem_load32_begin<256 * kBuffer + 96>(at, v[1]);
+      add_features<kSwiglu>(v[0], g, u, acc[2]);
       tmem_load32_end(v[1]);
-      release<kBuffer, 2>(empty);
-      look<kNext>(full, set);
-      if (kStep == 3) {  // the next slot's
-        release_scales();
-        if (more) {
-          wait_scales(a, scales_done);
-          load_scales<0>(row, s);
-        }
-      }
-      add_features<kSwiglu>(v[1], kSwiglu ? g : u, u, acc[3]);
+      release<kBuffer>();
+      look<kNext>();
+      add_features<kSwiglu>(v[1], g, u, acc[3]);
     } else {
-      release<kBuffer, 2>(empty);
-      look<kNext>(full, set);
-      if (kStep == 3) {
-        release_scales();
-        if (more) wait_scales(a);
-      }
+      release<kBuffer>();
+      look<kNext>();
     }
   }
   template <bool kSwiglu>
-  __device__ __forceinline__ void wide(const ProductArgs& a, float (&acc)[4][32], uint32_t at, int set, uint32_t row,
-                                       bool some) {
+  __device__ __forceinline__ void wide(const ProductArgs& a, float (&acc)[4][32], uint32_t at, int set, bool some,
+                                       Scales& s) {
 #pragma unroll
     for (int c = 0; c < 4; ++c)
 #pragma unroll
       for (int n = 0; n < 32; ++n) acc[c][n] = 0;
     next_done = 0;
-    wait_scales(a);
-    Scales s;
-    uint32_t done = 0;
-    load_scales<0>(row, s);
+    s.now = s.next, s.w_now = s.w_next;
+    s.take<0, kSwiglu>(kSwiglu ? 0 : 4 * set);
     for (int k = 0; k < a.steps; k += 4) {
-      wide_step<kSwiglu, 0>(a, acc, at, set, row, some, true, s, done);
-      if (k + 1 < a.steps) wide_step<kSwiglu, 1>(a, acc, at, set, row, some, true, s, done);
-      if (k + 2 < a.steps) wide_step<kSwiglu, 2>(a, acc, at, set, row, some, true, s, done);
-      if (k + 3 < a.steps) wide_step<kSwiglu, 3>(a, acc, at, set, row, some, k + 4 < a.steps, s, done);
+      s.load(k + 4, a.steps);
+      wide_step<kSwiglu, 0>(a, acc, at, set, some, s);
+      if (k + 1 < a.steps) wide_step<kSwiglu, 1>(a, acc, at, set, some, s);
+      if (k + 2 < a.steps) wide_step<kSwiglu, 2>(a, acc, at, set, some, s);
+      if (k + 3 < a.steps) wide_step<kSwiglu, 3>(a, acc, at, set, some, s);
     }
-    if (a.steps & 3) release_scales();
   }
 };
 
@@ -372,8 +369,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       mbar_init(scale_empty + 8 * i, 8);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(amax_full + 8 * i, 8);  // a set's warps of both CTAs
-      mbar_init(amax_empty + 8 * i, 8);
+      mbar_init(amax_full + 8 * i, 4);   // a set's warps, and the bytes that the peer's send
+      mbar_init(amax_empty + 8 * i, 8);  // a set's warps of both CTAs
     }
     for (int i = 0; i < 4; ++i) mbar_init(row_full + 8 * i, 2);  // the two warps of 32 rows
     for (int i = 0; i < kPlanDepth; ++i) {
@@ -413,26 +410,21 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           if (!(ok = mbar_wait_cta(plan_full + 8 * slot, (i / kPlanDepth) & 1, a.err))) break;
           const bool was_wide = wide;
           wide = is_wide(tiles[slot]);
-          const uint32_t n = wide ? 128 : columns(tiles[slot].groups), idesc = a.idesc | (n >> 3) << 17;
+          const uint32_t n = wide ? 256 : columns(tiles[slot].groups), idesc = a.idesc | (n >> 3) << 17;
           mbar_arrive(plan_empty + 8 * slot);
-          if (wide != was_wide)  // other warps hand the buffers back: all of them have to be free
+          if (wide != was_wide)  // other columns: every buffer has to be handed back
             for (int b = 0; b < kBuffers && ok; ++b) ok = mbar_wait_cta(acc_empty + 8 * b, (phases >> b & 1) ^ 1, a.err);
           for (int k = 0; k < a.steps && ok; ++k) {
             const uint32_t w = desc + (uint32_t)(stage * (kStage >> 4)), x = w + (kBytesA >> 4);
             if (!(ok = mbar_wait_cta(full + 8 * stage, phase, a.err))) break;
-            if (wide) {  // a product for each set's 128 features, 64 of each CTA's
+            if (wide) {
+              const int b = k & 1;
+              if (!(ok = mbar_wait_cta(acc_empty + 8 * b, (phases >> b & 1) ^ 1, a.err))) break;
+              tc_fence_after();
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const int b = 2 * (k & 1) + h;
-                if (!(ok = mbar_wait_cta(acc_empty + 8 * b, (phases >> b & 1) ^ 1, a.err))) break;
-                tc_fence_after();
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  mma_8bit(tmem + 128 * b, x + 2 * j, w + h * (64 * 128 >> 4) + 2 * j, idesc, j > 0);
-                mma_commit_pair(acc_full + 8 * b);
-                phases ^= 1u << b;
-              }
-              if (!ok) break;
+              for (int j = 0; j < 4; ++j) mma_8bit(tmem + 256 * b, x + 2 * j, w + 2 * j, idesc, j > 0);
+              mma_commit_pair(acc_full + 8 * b);
+              phases ^= 1u << b;
             } else {
               const int b = k & (kBuffers - 1);
               if (!(ok = mbar_wait_cta(acc_empty + 8 * b, (phases >> b & 1) ^ 1, a.err))) break;
@@ -471,31 +463,47 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     sums.ok = true;
     bool& ok = sums.ok;
     int i = 0, narrow_tiles = 0, wide_tiles = 0;
-    for (int t = pair_id; t < ntiles && ok; t += pairs, ++i) {
+    // the i-th tile's plan; of a wide one this thread's row and first scales, which are
+    // asked for before the tile before it is stored
+    int row = -1;
+    Sums::Scales scales;
+    const auto open = [&] {
       const int slot = i % kPlanDepth;
       mbar_wait_cta_warp(plan_full + 8 * slot, (i / kPlanDepth) & 1, ok, a.err);
-      if (!ok) break;
+      const Tile tile = tiles[slot];
+      if (!ok || !is_wide(tile)) return;
+      const int half = columns(tile.groups) / 2;  // the pair's halves of the list
+      row = 32 * w + lane < half ? rows[slot * kMaxRows + (int)rank * half + 32 * w + lane] : -1;
+      scales.row = reinterpret_cast<const float4*>(a.x + (uint64_t)max(row, 0) * a.x_row + a.in);
+      scales.w = weight_scales<kSwiglu>(s, tile, lane >> 2 & 1) + (lane & 3);
+      scales.load(0, a.steps);
+    };
+    if (pair_id < ntiles) open();
+    for (int t = pair_id; t < ntiles && ok; t += pairs) {
+      const int slot = i % kPlanDepth;
       uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16);
       asm volatile("" : "+r"(lanes));  // not kept, with sums of it, from tile to tile
       float acc[4][32];  // one for both kinds of tile: with an array each 1.4 KB of registers spill
       const Tile tile = tiles[slot];
       const int* list = rows + slot * kMaxRows;
+      ++i;
       if (is_wide(tile)) {
-        // set: which half of each CTA's features.  Rows: the pair's halves of the list.
-        const int half = columns(tile.groups) / 2, index = (int)rank * half + 32 * w + lane;
-        const bool some = 32 * w < half;
+        // set: which half of each CTA's features
+        const bool some = 32 * w < columns(tile.groups) / 2;
         constexpr int kChunks = 4;
-        sums.wide<kSwiglu>(a, acc, lanes + 128 * set, set, sums.scales + 4 * index, some);
+        sums.wide<kSwiglu>(a, acc, lanes + 128 * set, set, some, scales);
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
+        const int own = row, neighbour = __shfl_xor_sync(0xffffffffu, row, 1);
+        if (t + pairs < ntiles) open();
         if (some) {
-          const int row = 32 * w + lane < half ? list[index] : -1, neighbour = __shfl_xor_sync(0xffffffffu, row, 1);
           if constexpr (!kSwiglu) {
 #pragma unroll
             for (int c = 0; c < kChunks; ++c) {
-              store_values(a, acc[c], tile.block * kTileFeatures + c / 2 * 128 + 64 * set + c % 2 * 32, row, neighbour);
+              store_values(a, acc[c], tile.block * kTileFeatures + 128 * set + 32 * c, own, neighbour);
             }
           } else {
-            const int first = tile.block * 128 + 32 * set;  // and 64 further
+            const int first = tile.block * 128 + 64 * set;
             if (a.out_dtype != LLMOE_DTYPE_FP8B) {
 #pragma unroll
               for (int c = 0; c < kChunks; ++c) {
@@ -504,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                   swiglu_row<true>(acc[c], h);
                 else
                   swiglu_row<false>(acc[c], h);
-                store_values(a, h, first + c / 2 * 64 + c % 2 * 16, row, neighbour);
+                store_values(a, h, first + 16 * c, own, neighbour);
               }
             } else {
               // a row's block of 128 outputs is this thread's and the other set's
@@ -536,13 +544,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                            pack_e4m3x2(h[c + n][4 * m + 2] * inverse, h[c + n][4 * m + 3] * inverse) << 16;
                   q[n] = make_uint4(b[0], b[1], b[2], b[3]);
                 }
-                store_pieces(a, q[0], q[1], row, neighbour, first + 32 * c, a.out);
+                store_pieces(a, q[0], q[1], own, neighbour, first + 16 * c, a.out);
               }
-              if (set == 0 && row >= 0) {
-                uint8_t* at = in_row(a, a.y + a.out + 4 * tile.block, row);
+              if (set == 0 && own >= 0) {
+                uint8_t* at = in_row(a, a.y + a.out + 4 * tile.block, own);
                 *reinterpret_cast<float*>(at) = scale;
                 if (tile.block + 1 == a.blocks)
-                  for (uint8_t* end = in_row(a, a.y + a.y_row, row); (at += 4) < end;) *reinterpret_cast<uint32_t*>(at) = 0;
+                  for (uint8_t* end = in_row(a, a.y + a.y_row, own); (at += 4) < end;) *reinterpret_cast<uint32_t*>(at) = 0;
               }
               ++wide_tiles;
             }
@@ -560,7 +568,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         else
           sums.narrow<0>(a, acc, lanes + 32 * set, scale);
         static_assert(kChunks == 2, "all numbers of chunks");
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
+        if (t + pairs < ntiles) open();
         list += 32 * set;
         const int first = kSwiglu ? tile.block * 128 + (int)rank * 64 + w * 16
                                   : tile.block * kTileFeatures + (int)rank * 128 + w * 32;
@@ -579,7 +589,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           if (!(ok = mbar_wait_warp(amax_empty + 8 * set, (narrow_tiles & 1) ^ 1, a.err))) break;
           uint32_t* amax = reinterpret_cast<uint32_t*>(smem + l.amax) + 32 * set;
           const int source = ((int)rank * 4 + w) * kNarrowRows;
-          const uint32_t peer = map_rank(smem_addr(amax + source), rank ^ 1);
+          const uint32_t peer = map_rank(smem_addr(amax + source), rank ^ 1), told = map_rank(amax_full + 8 * set, rank ^ 1);
+          if (lane == 0) mbar_expect_bytes(amax_full + 8 * set, 128 * chunks);
           float h[kChunks][16];
 #pragma unroll
           for (int c = 0; c < kChunks; ++c)
@@ -589,13 +600,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
               const uint32_t most = largest_of_columns(h[c], at);
               const int column = 64 * c + 2 * at + up;
               amax[source + column] = most;
-              shared_store_peer(peer + 4 * column, most);
+              shared_store_peer(peer + 4 * column, most, told);
             }
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(amax_full + 8 * set);
-            mbar_arrive_peer_release(map_rank(amax_full + 8 * set, rank ^ 1));
-          }
+          if (lane == 0) mbar_arrive(amax_full + 8 * set);
           if (!(ok = mbar_wait_warp(amax_full + 8 * set, narrow_tiles & 1, a.err))) break;
           float scale[kChunks];  // of row `lane` of each 32
 #pragma unroll
@@ -609,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(amax_empty + 8 * set);
-            mbar_arrive_peer_release(map_rank(amax_empty + 8 * set, rank ^ 1));
+            mbar_arrive_peer(map_rank(amax_empty + 8 * set, rank ^ 1));
           }
 #pragma unroll
           for (int c = 0; c < kChunks; ++c)
@@ -636,11 +644,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   } else {
     fewer_registers<kFewRegisters>();
     // ---- scales ------------------------------------------------------------------
-    // Warp q's lane moves those of rows 32 q + lane and 128 + 32 q + lane of the
-    // tile's list, 16 bytes of a row (four steps) at a time, kAhead such chunks
-    // ahead; and lane % 4 w's of a step, for the first or (lane & 4) the second of:
-    // gate and up; a wide tile's two CTAs' features.
-    constexpr int kAhead = 1;
+    // Of narrow tiles.  Warp q's lane makes those of row 32 q + lane of the tile's
+    // list, 16 bytes of it (four steps) at a time, the next on their way; lane % 4
+    // brings w's of a step (with SwiGLU of gate or, lane & 4, up).
     const int q = warp & 3, chunks = (a.steps + 3) / 4;
     int i = 0, sslot = 0;
     uint32_t sphase = 0;
@@ -650,70 +656,38 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       mbar_wait_cta_warp(plan_full + 8 * slot, (i / kPlanDepth) & 1, ok, a.err);
       if (!ok) break;
       const Tile tile = tiles[slot];
-      const bool wide = is_wide(tile);
-      const int n = columns(tile.groups), m = 32 * q + lane;
-      const int r0 = m < n ? rows[slot * kMaxRows + m] : -1;
-      const int r1 = 128 + m < n ? rows[slot * kMaxRows + 128 + m] : -1;
+      const int m = 32 * q + lane, row = m < columns(tile.groups) && !is_wide(tile) ? rows[slot * kMaxRows + m] : -1;
       __syncwarp();
       if (lane == 0) mbar_arrive(plan_empty + 8 * slot);
-      const uint4* src[2] = {reinterpret_cast<const uint4*>(a.x + (uint64_t)max(r0, 0) * a.x_row + a.in),
-                             reinterpret_cast<const uint4*>(a.x + (uint64_t)max(r1, 0) * a.x_row + a.in)};
-      const bool have[2] = {r0 >= 0, r1 >= 0};
-      // past the last block of w's features nothing is stored
-      const int second = lane >> 2 & 1;
-      const int block = kSwiglu ? tile.block : min(2 * tile.block + (wide ? second : (int)rank), s.down - 1);
-      const float* wsrc = s.w_scale + ((kSwiglu ? 2 * (int64_t)tile.expert + second : tile.expert) * s.down + block) *
-                                          (int64_t)s.across;
-      const auto load_w = [&](int c) { return 4 * c + (lane & 3) < s.across ? wsrc[4 * c + (lane & 3)] : 0.0f; };
-      uint4 ahead[kAhead][2];
-      float w_ahead[kAhead];
+      if (is_wide(tile)) continue;
+      const uint4* src = reinterpret_cast<const uint4*>(a.x + (uint64_t)max(row, 0) * a.x_row + a.in);
+      const float* wsrc = weight_scales<kSwiglu>(s, tile, kSwiglu ? lane >> 2 & 1 : (int)rank) + (lane & 3);
+      uint4 next = make_uint4(0, 0, 0, 0);
+      float w_next = 0;
+      const auto load = [&](int c) {
+        if (row >= 0 && c < chunks) next = src[c];
+        if (4 * c + (lane & 3) < s.across) w_next = wsrc[4 * c];
+      };
+      load(0);
+      for (int c = 0; c < chunks; ++c) {
+        const uint4 v = next;
+        const float wv = w_next;
+        load(c + 1);
+        mbar_wait_cta_warp(scale_empty + 8 * sslot, sphase ^ 1, ok, a.err);
+        if (!ok) break;
+        float* dst = reinterpret_cast<float*>(smem + l.scales + sslot * kSlot) + m;
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
+        for (int b = 0; b < 4; ++b) {
+          const float x = __uint_as_float(b == 0 ? v.x : b == 1 ? v.y : b == 2 ? v.z : v.w);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          ahead[u][j] = make_uint4(0, 0, 0, 0);
-          if (have[j] && u < chunks) ahead[u][j] = src[j][u];
-        }
-        w_ahead[u] = load_w(u);
-      }
-      for (int c0 = 0; c0 < chunks && ok; c0 += kAhead) {
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-          const int c = c0 + u;
-          if (c >= chunks || !ok) break;
-          mbar_wait_cta_warp(scale_empty + 8 * sslot, sphase ^ 1, ok, a.err);
-          if (!ok) break;
-          float* dst = reinterpret_cast<float*>(smem + l.scales + sslot * kSlot) + m;
-          if (wide) {
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const uint4& v = ahead[u][j];
-                if (have[j]) dst[b * kMaxRows + 128 * j] = __uint_as_float(b == 0 ? v.x : b == 1 ? v.y : b == 2 ? v.z : v.w);
-              }
-            if (q == 0 && lane < 8)
-              reinterpret_cast<float*>(smem + l.w_scales)[(sslot * 4 + (lane & 3)) * 2 + second] = w_ahead[u];
-          } else {
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              const uint4& v = ahead[u][0];
-              const float x = __uint_as_float(b == 0 ? v.x : b == 1 ? v.y : b == 2 ? v.z : v.w);
-#pragma unroll
-              for (int p = 0; p < (kSwiglu ? 2 : 1); ++p) {
-                const float ws = __shfl_sync(0xffffffffu, w_ahead[u], 4 * p + b);
-                if (have[0]) dst[(2 * b + p) * kNarrowStride] = x * ws;
-              }
-            }
+          for (int p = 0; p < (kSwiglu ? 2 : 1); ++p) {
+            const float ws = __shfl_sync(0xffffffffu, wv, 4 * p + b);
+            if (row >= 0) dst[(2 * b + p) * kNarrowStride] = x * ws;
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(scale_full + 8 * sslot);
-          if (++sslot == kSlots) sslot = 0, sphase ^= 1;
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            if (have[j] && c + kAhead < chunks) ahead[u][j] = src[j][c + kAhead];
-          w_ahead[u] = load_w(c + kAhead);
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(scale_full + 8 * sslot);
+        if (++sslot == kSlots) sslot = 0, sphase ^= 1;
       }
     }
   }

@@ -42,6 +42,10 @@ __device__ __forceinline__ void mbar_init_fence() { asm volatile("fence.mbarrier
 __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
+// More bytes for the phase, without an arrival.
+__device__ __forceinline__ void mbar_expect_bytes(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -51,14 +55,8 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
 // that loads ahead).  Its uses need none: tensor memory that has been read, and
 // shared memory that only the tensor core of this SM reads, which the writers'
 // fence_async_shared has made visible to it.
-template <int kCount = 1>
 __device__ __forceinline__ void mbar_arrive_peer(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "n"(kCount) : "memory");
-}
-// The same with what this thread wrote to the cluster's shared memory before it,
-// for a peer's thread that waits on the barrier.
-__device__ __forceinline__ void mbar_arrive_peer_release(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   uint32_t done;
@@ -123,10 +121,8 @@ __device__ __forceinline__ uint32_t mbar_test_cta(uint32_t bar, uint32_t parity)
   return done;
 }
 // mbar_wait_cta for a whole warp that goes on together; once a wait has failed, ok
-// stays false and nothing is waited for.  done: an earlier mbar_test_cta's result.
-__device__ __forceinline__ void mbar_wait_cta_warp(uint32_t bar, uint32_t parity, bool& ok, int32_t* err,
-                                                   uint32_t done = 0) {
-  if (__all_sync(0xffffffffu, done)) return;
+// stays false and nothing is waited for.
+__device__ __forceinline__ void mbar_wait_cta_warp(uint32_t bar, uint32_t parity, bool& ok, int32_t* err) {
   if (ok) ok = __all_sync(0xffffffffu, mbar_wait_cta(bar, parity, err));
 }
 
@@ -230,8 +226,10 @@ __device__ __forceinline__ float4 shared_load4(uint32_t addr) {
                : "r"(addr), "n"(kOffset));
   return v;
 }
-__device__ __forceinline__ void shared_store_peer(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+// To a peer's shared memory, four bytes that its barrier counts.
+__device__ __forceinline__ void shared_store_peer(uint32_t addr, uint32_t v, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(addr), "r"(v), "r"(bar)
+               : "memory");
 }
 
 // Registers of this warpgroup's threads from here on.
