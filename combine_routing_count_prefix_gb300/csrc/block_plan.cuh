@@ -471,16 +471,23 @@ __device__ __forceinline__ void store_codes(const ProductArgs& a, const float (&
   int row[4];
 #pragma unroll
   for (int g = 0; g < 4; ++g) row[g] = feature < a.out ? list[2 * (4 * g + q) + up] : -1;
+  // four columns of one feature, turned over four lanes into four features of one
+  // column; each exchange for all four groups at once, for they take long
+  uint32_t b[4], got[4];
+#pragma unroll
+  for (int g = 0; g < 4; ++g)
+    b[g] = pack_e4m3x2(h[4 * g] * inverse[4 * g], h[4 * g + 1] * inverse[4 * g + 1]) |
+           pack_e4m3x2(h[4 * g + 2] * inverse[4 * g + 2], h[4 * g + 3] * inverse[4 * g + 3]) << 16;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) got[g] = __shfl_xor_sync(0xffffffffu, b[g], 1);
+#pragma unroll
+  for (int g = 0; g < 4; ++g) b[g] = __byte_perm(b[g], got[g], lane & 1 ? 0x3715 : 0x6240);
+#pragma unroll
+  for (int g = 0; g < 4; ++g) got[g] = __shfl_xor_sync(0xffffffffu, b[g], 2);
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
-    // four columns of one feature, turned over four lanes into four features of one column
-    uint32_t b = pack_e4m3x2(h[4 * g] * inverse[4 * g], h[4 * g + 1] * inverse[4 * g + 1]) |
-                 pack_e4m3x2(h[4 * g + 2] * inverse[4 * g + 2], h[4 * g + 3] * inverse[4 * g + 3]) << 16;
-    uint32_t got = __shfl_xor_sync(0xffffffffu, b, 1);
-    b = __byte_perm(b, got, lane & 1 ? 0x3715 : 0x6240);
-    got = __shfl_xor_sync(0xffffffffu, b, 2);
-    b = __byte_perm(b, got, lane & 2 ? 0x3276 : 0x5410);
-    if (row[g] >= 0) *reinterpret_cast<uint32_t*>(in_row(a, a.y + (feature - q), row[g])) = b;
+    b[g] = __byte_perm(b[g], got[g], lane & 2 ? 0x3276 : 0x5410);
+    if (row[g] >= 0) *reinterpret_cast<uint32_t*>(in_row(a, a.y + (feature - q), row[g])) = b[g];
   }
 }
 

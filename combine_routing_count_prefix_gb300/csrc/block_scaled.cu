@@ -586,7 +586,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         } else {
           // a block of 128 outputs is the pair's: its eight warps of this set swap
           // their largest magnitudes, once the last tile's have been read
-          if (!(ok = mbar_wait_warp(amax_empty + 8 * set, (narrow_tiles & 1) ^ 1, a.err))) break;
+          mbar_wait_cta_warp(amax_empty + 8 * set, (narrow_tiles & 1) ^ 1, ok, a.err);
+          if (!ok) break;
           uint32_t* amax = reinterpret_cast<uint32_t*>(smem + l.amax) + 32 * set;
           const int source = ((int)rank * 4 + w) * kNarrowRows;
           const uint32_t peer = map_rank(smem_addr(amax + source), rank ^ 1), told = map_rank(amax_full + 8 * set, rank ^ 1);
@@ -604,7 +605,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             }
           __syncwarp();
           if (lane == 0) mbar_arrive(amax_full + 8 * set);
-          if (!(ok = mbar_wait_warp(amax_full + 8 * set, narrow_tiles & 1, a.err))) break;
+          mbar_wait_cta_warp(amax_full + 8 * set, narrow_tiles & 1, ok, a.err);  // counted bytes, as loads are
+          if (!ok) break;
           float scale[kChunks];  // of row `lane` of each 32
 #pragma unroll
           for (int c = 0; c < kChunks; ++c)
