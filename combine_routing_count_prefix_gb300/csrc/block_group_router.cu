@@ -1,9 +1,15 @@
 // block_group_router.cu -- llmoe_group_router (include/llmoe_block.h).
 //
-// A group of one warp (a CTA of eight for many experts) owns a token.  Its keys,
-// 32-bit integers that order like the floats (0: cannot be chosen), lie in shared
-// memory; a lane finds the score of whole groups of experts, groups are ranked by
-// counting those ahead of them, and K rounds of two reductions choose the experts.
+// Where the number of groups divides 32 and a warp's registers hold a row (512
+// experts), a warp owns a token and 32 / num_groups lanes a group of experts
+// (lanes_kernel): a group's best two keys come from a butterfly over its lanes,
+// groups are ranked by counting those ahead of them, and the experts are chosen
+// from the few keys that reach a bound: the K-th largest of the kept lanes' best
+// keys, which at least K keys do.  Those few go to shared memory, a lane each, and
+// their rank among them, counted too, is their place in the result.  Keys are
+// 32-bit integers that order like the floats (0: cannot be chosen).
+// Any other row lies in shared memory as keys (rows_kernel, a warp or a CTA of
+// eight): a lane scores whole groups, and K rounds of two reductions choose.
 #include "block_router.cuh"
 
 namespace {
@@ -34,8 +40,44 @@ __device__ __forceinline__ uint32_t score_order(float v) {
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
+// A group's score from its best two keys (second: 0 where there is one, or the score
+// is of the best alone), 0 where nothing can be chosen.
+__device__ __forceinline__ uint32_t group_score(uint32_t best, uint32_t second) {
+  return second == 0 ? best : score_order(unorder(best) + unorder(second));
+}
+
+// The row's result from a warp's choices: `place` of lane's expert `mine` (-1: none),
+// whose logit is v; places from `chosen` on have none.  top, total: an
+// unrenormalised softmax's, over all experts.
+template <bool kSoftmax>
+__device__ __forceinline__ void store_choice(const GroupRouterArgs& a, int64_t row, int mine, float v, int place,
+                                             int chosen, float top, float total) {
+  const int lane = threadIdx.x & 31;
+  if (kSoftmax && a.renorm) {  // a softmax of the chosen alone
+    top = v;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  }
+  float s = 0.0f;
+  if (mine >= 0) s = !kSoftmax ? sigmoid_score(v) : a.renorm ? softmax_score(v, top) : softmax_score(v, top) / total;
+  if (a.renorm) {
+    float sum = s;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    s = sum > 0.0f ? s / sum : 0.0f;  // before the scale: scale / sum may be above fp32's largest
+  }
+  if (mine >= 0) {
+    a.topk_idx[row * a.K + place] = mine;
+    a.topk_w[row * a.K + place] = s * a.scale;
+  }
+  if (lane >= chosen && lane < a.K) {
+    a.topk_idx[row * a.K + lane] = -1;
+    a.topk_w[row * a.K + lane] = 0.0f;
+  }
+}
+
 template <int W, bool kSoftmax>
-__global__ void __launch_bounds__(256) group_router_kernel(GroupRouterArgs a) {
+__global__ void __launch_bounds__(256) rows_kernel(GroupRouterArgs a) {
   extern __shared__ uint32_t smem[];
   __shared__ uint32_t part[W];
   wait_prior_grid();
@@ -72,7 +114,7 @@ __global__ void __launch_bounds__(256) group_router_kernel(GroupRouterArgs a) {
         second = max(second, min(best, k));
         best = max(best, k);
       }
-      score[g] = best == 0 ? 0 : a.top2 && second != 0 ? score_order(unorder(best) + unorder(second)) : best;
+      score[g] = group_score(best, a.top2 ? second : 0);
     }
     group_sync<W>();
     for (int g = lane; g < a.G; g += kLanes) {
@@ -97,35 +139,164 @@ __global__ void __launch_bounds__(256) group_router_kernel(GroupRouterArgs a) {
     }
     if (W > 1 && lane >= 32) continue;
     const float v = mine >= 0 ? load_logit(a.logits, a.dtype, row * a.E + mine) : -INFINITY;
-    if (kSoftmax && a.renorm) {  // a softmax of the chosen alone
-      top = v;
+    store_choice<kSoftmax>(a, row, mine, v, lane, __popc(__ballot_sync(0xffffffffu, mine >= 0)), top, total);
+  }
+}
+
+// V: experts a lane holds at most; kVec: fp32 logits, four experts of a lane in a row.
+template <int V, bool kVec, bool kSoftmax>
+__global__ void __launch_bounds__(256, V > 8 ? 3 : 5) lanes_kernel(GroupRouterArgs a) {
+  __shared__ uint2 gathered[8][32];
+  wait_prior_grid();
+  release_next_grid();
+  const int lane = threadIdx.x & 31, L = 32 / a.G, g = lane / L, q = lane - g * L;
+  uint2* list = gathered[threadIdx.x >> 5];
+  // the lane's i-th expert, of its group: in order over the group's lanes, or four in a row
+  const auto expert = [&](int i) { return kVec ? (i / 4 * L + q) * 4 + i % 4 : i * L + q; };
+  const int64_t step = ((int64_t)gridDim.x * blockDim.x) >> 5;
+  for (int64_t row = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; row < a.rows; row += step) {
+    const bool on = a.active == nullptr || a.active[row] != 0;
+    const int64_t at = row * a.E + g * a.S;
+    float l[V];
+    if constexpr (kVec) {
+#pragma unroll
+      for (int i = 0; i < V; i += 4) {
+        float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (on && expert(i) < a.S) v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) + at + expert(i));
+        l[i] = v.x, l[i + 1] = v.y, l[i + 2] = v.z, l[i + 3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) l[i] = on && expert(i) < a.S ? load_logit(a.logits, a.dtype, at + expert(i)) : -INFINITY;
+    }
+    uint32_t key[V], best = 0, second = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float k = kSoftmax ? l[i] : sigmoid_score(l[i]);
+      if (a.bias != nullptr && expert(i) < a.S) k += a.bias[g * a.S + expert(i)];
+      key[i] = order(l[i], k);
+      second = max(second, min(best, key[i]));
+      best = max(best, key[i]);
+    }
+    float top = -INFINITY, total = 0.0f;
+    if (kSoftmax && !a.renorm) {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (key[i] != 0) top = fmaxf(top, l[i]);
 #pragma unroll
       for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    }
-    float s = 0.0f;
-    if (mine >= 0) s = !kSoftmax ? sigmoid_score(v) : a.renorm ? softmax_score(v, top) : softmax_score(v, top) / total;
-    if (a.renorm) {
-      float sum = s;
 #pragma unroll
-      for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-      s = sum > 0.0f ? s / sum : 0.0f;  // before the scale: scale / sum may be above fp32's largest
+      for (int i = 0; i < V; ++i)
+        if (key[i] != 0) total += softmax_score(l[i], top);
+#pragma unroll
+      for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
     }
-    if (lane < a.K) {
-      a.topk_idx[row * a.K + lane] = mine;
-      a.topk_w[row * a.K + lane] = s * a.scale;
+    uint32_t lane_best = best;
+    if (a.kept < a.G) {
+      if (a.top2) {
+        for (int d = 1; d < L; d <<= 1) {
+          const uint32_t b = __shfl_xor_sync(0xffffffffu, best, d), s = __shfl_xor_sync(0xffffffffu, second, d);
+          second = max(max(second, s), min(best, b));
+          best = max(best, b);
+        }
+      } else {
+        second = 0;
+        for (int d = 1; d < L; d <<= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, d));
+      }
+      const uint32_t score = group_score(best, second);
+      int ahead = 0;
+      for (int o = 0; o < a.G; ++o) {
+        const uint32_t other = __shfl_sync(0xffffffffu, score, o * L);
+        ahead += other > score || (other == score && o < g);
+      }
+      if (ahead >= a.kept) {
+        lane_best = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) key[i] = 0;
+      }
     }
+    uint32_t bound = 0, left = lane_best;
+    for (int k = 0; k < a.K; ++k) {
+      bound = __reduce_max_sync(0xffffffffu, left);
+      if (bound == 0) break;  // fewer lanes than K: every key
+      if (left == bound) left = 0;
+    }
+    const uint32_t least = max(bound, 1u);
+    int n = 0;
+    __syncwarp();  // the previous row's list has been read
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const bool in = key[i] >= least;
+      const uint32_t who = __ballot_sync(0xffffffffu, in);
+      const int to = n + __popc(who & ((1u << lane) - 1));
+      if (in && to < 32) {
+        list[to] = make_uint2(key[i], (uint32_t)(g * a.S + expert(i)));
+      }
+      n += __popc(who);
+    }
+    __syncwarp();
+    if (n <= 32) {
+      const uint2 mine = lane < n ? list[lane] : make_uint2(0, 0);
+      int place = 0;
+      for (int o = 0; o < n; ++o) {
+        const uint2 other = list[o];
+        place += other.x > mine.x || (other.x == mine.x && other.y < mine.y);
+      }
+      const bool chosen = lane < n && place < a.K;
+      store_choice<kSoftmax>(a, row, chosen ? (int)mine.y : -1, chosen ? load_logit(a.logits, a.dtype, row * a.E + (int)mine.y) : -INFINITY, place, min(n, a.K), top,
+                             total);
+      continue;
+    }
+    // many keys at the bound, or few lanes: rounds of two reductions, over all keys
+    int mine = -1;
+    float v = -INFINITY;
+    for (int k = 0; k < a.K; ++k) {
+      uint32_t most = 0, e = 0xffffffffu;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const uint32_t at_e = (uint32_t)(g * a.S + expert(i));
+        if (key[i] > most || (key[i] == most && most != 0 && at_e < e)) most = key[i], e = at_e;
+      }
+      const uint32_t win = __reduce_max_sync(0xffffffffu, most);
+      if (win == 0) break;
+      e = __reduce_min_sync(0xffffffffu, most == win ? e : 0xffffffffu);
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (key[i] != 0 && (uint32_t)(g * a.S + expert(i)) == e) key[i] = 0;
+      if (lane == k) mine = (int)e;
+    }
+    if (mine >= 0) v = load_logit(a.logits, a.dtype, row * a.E + mine);
+    store_choice<kSoftmax>(a, row, mine, v, lane, __popc(__ballot_sync(0xffffffffu, mine >= 0)), top, total);
   }
+}
+
+template <int V, bool kSoftmax>
+int launch_lanes(const GroupRouterArgs& a, bool vec, llmoe_stream_t stream) {
+  const unsigned grid = (unsigned)std::min<int64_t>((int64_t)num_sms() * 8, (a.rows + 7) / 8);
+  if constexpr (V >= 4)
+    if (vec) return launch_block(lanes_kernel<V, true, kSoftmax>, grid, 256, 0, stream, a);
+  return launch_block(lanes_kernel<V, false, kSoftmax>, grid, 256, 0, stream, a);
 }
 
 template <bool kSoftmax>
 int launch_group_router(const GroupRouterArgs& a, llmoe_stream_t stream) {
+  if (32 % a.G == 0) {
+    const int L = 32 / a.G, each = (a.S + L - 1) / L;  // experts a lane holds
+    // a lane's experts four in a row where the group's are whole fours for each lane
+    const bool vec = a.dtype == LLMOE_DTYPE_FP32 && a.S % (4 * L) == 0 && aligned(a.logits, 16);
+    if (each <= 1) return launch_lanes<1, kSoftmax>(a, vec, stream);
+    if (each <= 2) return launch_lanes<2, kSoftmax>(a, vec, stream);
+    if (each <= 4) return launch_lanes<4, kSoftmax>(a, vec, stream);
+    if (each <= 8) return launch_lanes<8, kSoftmax>(a, vec, stream);
+    if (each <= 16) return launch_lanes<16, kSoftmax>(a, vec, stream);
+  }
   const size_t words = (size_t)a.E + a.G;
   if (a.E <= 512) {
     const unsigned grid = (unsigned)std::min<int64_t>((int64_t)num_sms() * 8, (a.rows + 7) / 8);
-    return launch_block(group_router_kernel<1, kSoftmax>, grid, 256, 8 * words * 4, stream, a);
+    return launch_block(rows_kernel<1, kSoftmax>, grid, 256, 8 * words * 4, stream, a);
   }
   const unsigned grid = (unsigned)std::min<int64_t>((int64_t)num_sms() * 4, a.rows);
-  return launch_block(group_router_kernel<8, kSoftmax>, grid, 256, words * 4, stream, a);
+  return launch_block(rows_kernel<8, kSoftmax>, grid, 256, words * 4, stream, a);
 }
 
 }  // namespace

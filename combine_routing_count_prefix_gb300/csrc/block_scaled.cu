@@ -34,7 +34,7 @@ constexpr int kMaxRows = 256, kNarrowRows = 128, kThreads = 512;
 constexpr int kBytesA = 128 * 128, kBytesB = kMaxRows / 2 * 128, kStage = kBytesA + kBytesB;
 constexpr int kManyRegisters = 200, kFewRegisters = 56;
 static_assert(256 * (kManyRegisters + kFewRegisters) <= 65536, "what a launch of 512 threads has");
-constexpr int kBuffers = 4;  // of tensor memory, 128 columns each; wide tiles take two of 256
+constexpr int kBuffers = 8;  // of tensor memory: 8 of 64 columns, 4 of 128 or, for wide tiles, 2 of 256
 constexpr int kSlots = 2;    // of scales, four steps each
 // A slot: a narrow tile's products of scales [step][gate, up][row], the up ones 16
 // bytes further so that a warp's loads of both do not meet in a bank
@@ -68,8 +68,10 @@ __host__ __device__ inline ScaledSmem scaled_smem(int stages, int E) {
   return l;
 }
 
-// Step k of a tile uses buffer k % 4 (narrow) or k % 2 (wide, two buffers' columns); a
-// buffer's phase is a bit of a word that the issuing thread and the summing warps keep.
+// Buffers a tile uses in turn: as many as its columns leave room for, so that the
+// products of narrow tiles run on while the last tile is stored.  A buffer's phase is
+// a bit of a word that the issuing thread and the summing warps each keep.
+__device__ __forceinline__ int buffers_of(int columns) { return columns > kNarrowRows ? 2 : columns > 64 ? 4 : 8; }
 __device__ __forceinline__ bool is_wide(const Tile& t) { return t.groups > kNarrowRows / kGroup; }
 
 // The scales of w for a tile's gate (part 0) or up features, or for those of the
@@ -180,23 +182,20 @@ struct Sums {
   bool ok;
 
   // ok is a lane's own until the tile's end: a vote in every step took 4% of a dense call.
-  template <int kBuffer>
-  __device__ __forceinline__ void wait(const ProductArgs& a) {
-    if (!next_done && ok) ok = mbar_wait_cta(acc_full + 8 * kBuffer, phases >> kBuffer & 1, a.err);
+  __device__ __forceinline__ void wait(const ProductArgs& a, int buffer) {
+    if (!next_done && ok) ok = mbar_wait_cta(acc_full + 8 * buffer, phases >> buffer & 1, a.err);
     __syncwarp();
-    phases ^= 1u << kBuffer;
+    phases ^= 1u << buffer;
     tc_fence_after();
   }
-  template <int kBuffer>
-  __device__ __forceinline__ void look() {
-    next_done = mbar_test_cta<8 * kBuffer>(acc_full, phases >> kBuffer & 1);
+  __device__ __forceinline__ void look(int buffer) {
+    next_done = mbar_test_cta(acc_full + 8 * buffer, phases >> buffer & 1);
   }
   // this warp has read the buffer
-  template <int kBuffer>
-  __device__ __forceinline__ void release() {
+  __device__ __forceinline__ void release(int buffer) {
     tc_fence_before();
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive_peer(leader_empty + 8 * kBuffer);
+    if ((threadIdx.x & 31) == 0) mbar_arrive_peer(leader_empty + 8 * buffer);
   }
   static_assert(kSlots == 2, "slots alternate");
   __device__ __forceinline__ uint32_t slot() const { return slots & 1; }
@@ -211,35 +210,38 @@ struct Sums {
   }
 
   // Narrow: kChunks times 32 rows, 64 columns apart from address `at` on in buffer 0;
-  // scale: their place in the slot's scales.
-  template <int kChunks, int kStep>
-  __device__ __forceinline__ void narrow_step(const ProductArgs& a, float (&acc)[4][32], uint32_t at, uint32_t scale) {
-    constexpr int kScale = 4 * 2 * kStep * kNarrowStride, kNext = (kStep + 1) % kBuffers;
-    wait<kStep>(a);
+  // scale: their place in the slot's scales; first: the first of the slot's buffers
+  // (kCount of them in turn).
+  template <int kChunks, int kCount, int kStep>
+  __device__ __forceinline__ void narrow_step(const ProductArgs& a, float (&acc)[4][32], uint32_t at, uint32_t scale,
+                                              int first) {
+    constexpr int kScale = 4 * 2 * kStep * kNarrowStride, kOffset = 512 / kCount * kStep;
+    const int next = kStep < 3 ? first + kStep + 1 : kCount == 8 ? first ^ 4 : 0;
+    wait(a, first + kStep);
     if constexpr (kChunks > 0) {
       uint32_t v[32];
-      tmem_load32_begin<128 * kStep>(at, v);
+      tmem_load32_begin<kOffset>(at, v);
       tmem_load32_end(v);
       if (kChunks == 1) {
-        release<kStep>();
-        look<kNext>();
+        release(first + kStep);
+        look(next);
       }
       add_rows<kScale>(v, scale, acc[0]);
     }
     if constexpr (kChunks > 1) {
       uint32_t v[32];
-      tmem_load32_begin<128 * kStep + 64>(at, v);
+      tmem_load32_begin<kOffset + 64>(at, v);
       tmem_load32_end(v);
-      release<kStep>();
-      look<kNext>();
+      release(first + kStep);
+      look(next);
       add_rows<kScale + 256>(v, scale, acc[1]);
     }
     if constexpr (kChunks == 0) {
-      release<kStep>();
-      look<kNext>();
+      release(first + kStep);
+      look(next);
     }
   }
-  template <int kChunks>
+  template <int kChunks, int kCount>
   __device__ __forceinline__ void narrow(const ProductArgs& a, float (&acc)[4][32], uint32_t at, uint32_t scale) {
 #pragma unroll
     for (int c = 0; c < kChunks; ++c)
@@ -248,11 +250,12 @@ struct Sums {
     next_done = 0;
     for (int k = 0; k < a.steps; k += 4) {
       wait_scales(a);
-      const uint32_t from = scales + slot() * kSlot + scale;
-      narrow_step<kChunks, 0>(a, acc, at, from);
-      if (k + 1 < a.steps) narrow_step<kChunks, 1>(a, acc, at, from);
-      if (k + 2 < a.steps) narrow_step<kChunks, 2>(a, acc, at, from);
-      if (k + 3 < a.steps) narrow_step<kChunks, 3>(a, acc, at, from);
+      const int first = kCount == 8 ? k & 4 : 0;
+      const uint32_t from = scales + slot() * kSlot + scale, here = at + 64 * first;
+      narrow_step<kChunks, kCount, 0>(a, acc, here, from, first);
+      if (k + 1 < a.steps) narrow_step<kChunks, kCount, 1>(a, acc, here, from, first);
+      if (k + 2 < a.steps) narrow_step<kChunks, kCount, 2>(a, acc, here, from, first);
+      if (k + 3 < a.steps) narrow_step<kChunks, kCount, 3>(a, acc, here, from, first);
       release_scales();
     }
   }
@@ -282,8 +285,8 @@ struct Sums {
   __device__ __forceinline__ void wide_step(const ProductArgs& a, float (&acc)[4][32], uint32_t at, int set, bool some,
                                             Scales& s) {
     constexpr int kBuffer = kStep & 1, kNext = kBuffer ^ 1;
-    wait<kBuffer>(a);
-    if (some) {
+    wait(a, kBuffer);
+    {
       // 32 columns load while the last 32 are added
       uint32_t v[2][32];
       tmem_load32_begin<256 * kBuffer>(at, v[0]);
@@ -300,12 +303,9 @@ struct Sums {
       tmem_load32_begin<256 * kBuffer + 96>(at, v[1]);
       add_features<kSwiglu>(v[0], g, u, acc[2]);
       tmem_load32_end(v[1]);
-      release<kBuffer>();
-      look<kNext>();
+      release(kBuffer);
+      look(kNext);
       add_features<kSwiglu>(v[1], g, u, acc[3]);
-    } else {
-      release<kBuffer>();
-      look<kNext>();
     }
   }
   template <bool kSwiglu>
@@ -316,6 +316,15 @@ struct Sums {
 #pragma unroll
       for (int n = 0; n < 32; ++n) acc[c][n] = 0;
     next_done = 0;
+    if (!some) {
+#pragma unroll 1
+      for (int k = 0; k < a.steps; ++k) {
+        wait(a, k & 1);
+        release(k & 1);
+        look(k & 1 ^ 1);
+      }
+      return;
+    }
     s.now = s.next, s.w_now = s.w_next;
     s.take<0, kSwiglu>(kSwiglu ? 0 : 4 * set);
     for (int k = 0; k < a.steps; k += 4) {
@@ -403,37 +412,32 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       if (leader && elect_one()) {
         int stage = 0, i = 0;
         uint32_t phase = 0, phases = 0;
-        bool ok = true, wide = false;
+        bool ok = true;
+        int count = 0;  // of buffers
         const uint32_t desc = tile_desc(sbase);
         for (int t = pair_id; t < ntiles && ok; t += pairs, ++i) {
           const int slot = i % kPlanDepth;
           if (!(ok = mbar_wait_cta(plan_full + 8 * slot, (i / kPlanDepth) & 1, a.err))) break;
-          const bool was_wide = wide;
-          wide = is_wide(tiles[slot]);
-          const uint32_t n = wide ? 256 : columns(tiles[slot].groups), idesc = a.idesc | (n >> 3) << 17;
+          const int rows_n = columns(tiles[slot].groups), was = count;
+          const bool wide = rows_n > kNarrowRows;
+          const uint32_t n = wide ? kTileFeatures : rows_n, idesc = a.idesc | (n >> 3) << 17;
           mbar_arrive(plan_empty + 8 * slot);
-          if (wide != was_wide)  // other columns: every buffer has to be handed back
+          count = buffers_of(rows_n);
+          const uint32_t stride = 512 / count;
+          if (count != was)  // other columns: every buffer has to be handed back
             for (int b = 0; b < kBuffers && ok; ++b) ok = mbar_wait_cta(acc_empty + 8 * b, (phases >> b & 1) ^ 1, a.err);
           for (int k = 0; k < a.steps && ok; ++k) {
             const uint32_t w = desc + (uint32_t)(stage * (kStage >> 4)), x = w + (kBytesA >> 4);
+            const uint32_t m_side = wide ? x : w, n_side = wide ? w : x;
+            const int b = k & (count - 1);
+            // the later of the two, most often, last
             if (!(ok = mbar_wait_cta(full + 8 * stage, phase, a.err))) break;
-            if (wide) {
-              const int b = k & 1;
-              if (!(ok = mbar_wait_cta(acc_empty + 8 * b, (phases >> b & 1) ^ 1, a.err))) break;
-              tc_fence_after();
+            if (!(ok = mbar_wait_cta(acc_empty + 8 * b, (phases >> b & 1) ^ 1, a.err))) break;
+            tc_fence_after();
 #pragma unroll
-              for (int j = 0; j < 4; ++j) mma_8bit(tmem + 256 * b, x + 2 * j, w + 2 * j, idesc, j > 0);
-              mma_commit_pair(acc_full + 8 * b);
-              phases ^= 1u << b;
-            } else {
-              const int b = k & (kBuffers - 1);
-              if (!(ok = mbar_wait_cta(acc_empty + 8 * b, (phases >> b & 1) ^ 1, a.err))) break;
-              tc_fence_after();
-#pragma unroll
-              for (int j = 0; j < 4; ++j) mma_8bit(tmem + 128 * b, w + 2 * j, x + 2 * j, idesc, j > 0);
-              mma_commit_pair(acc_full + 8 * b);
-              phases ^= 1u << b;
-            }
+            for (int j = 0; j < 4; ++j) mma_8bit(tmem + b * stride, m_side + 2 * j, n_side + 2 * j, idesc, j > 0);
+            mma_commit_pair(acc_full + 8 * b);
+            phases ^= 1u << b;
             mma_commit_pair(empty + 8 * stage);
             if (++stage == a.stages) stage = 0, phase ^= 1;
           }
@@ -561,12 +565,18 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         const int chunks = (columns(tile.groups) / 32 + 1 - set) / 2, up = kSwiglu ? lane >> 3 & 1 : 0;
         constexpr int kChunks = kNarrowRows / 64;
         const uint32_t scale = 4 * (up * kNarrowStride + 32 * set);
-        if (chunks == 2)
-          sums.narrow<2>(a, acc, lanes + 32 * set, scale);
-        else if (chunks == 1)
-          sums.narrow<1>(a, acc, lanes + 32 * set, scale);
-        else
-          sums.narrow<0>(a, acc, lanes + 32 * set, scale);
+        const uint32_t at = lanes + 32 * set;
+        if (buffers_of(columns(tile.groups)) == 8) {
+          if (chunks == 1)
+            sums.narrow<1, 8>(a, acc, at, scale);
+          else
+            sums.narrow<0, 8>(a, acc, at, scale);
+        } else {
+          if (chunks == 2)
+            sums.narrow<2, 4>(a, acc, at, scale);
+          else
+            sums.narrow<1, 4>(a, acc, at, scale);
+        }
         static_assert(kChunks == 2, "all numbers of chunks");
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;

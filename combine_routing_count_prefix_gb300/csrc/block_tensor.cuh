@@ -107,16 +107,15 @@ __device__ __forceinline__ bool mbar_wait_cta(uint32_t bar, uint32_t parity, int
     }
   return true;
 }
-// Whether the phase is complete, without waiting; kOffset: bytes from bar.
-template <int kOffset = 0>
+// Whether the phase is complete, without waiting.
 __device__ __forceinline__ uint32_t mbar_test_cta(uint32_t bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1 + %3], %2;\n\t"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(done)
-      : "r"(bar), "r"(parity), "n"(kOffset)
+      : "r"(bar), "r"(parity)
       : "memory");
   return done;
 }
