@@ -8,8 +8,12 @@
 // keys, which at least K keys do.  Those few go to shared memory, a lane each, and
 // their rank among them, counted too, is their place in the result.  Keys are
 // 32-bit integers that order like the floats (0: cannot be chosen).
-// Any other row lies in shared memory as keys (rows_kernel, a warp or a CTA of
-// eight): a lane scores whole groups, and K rounds of two reductions choose.
+// Instructions bound a large batch: about 1070 a token of 256 experts in 8 groups,
+// 8192 tokens 9.9 us (with keys in shared memory, a lane scoring whole groups and K
+// rounds of reductions over all keys 21.3), one token 3.5; 4096 tokens of 160 experts,
+// softmax, 7.1.
+// Any other row lies in shared memory as keys (rows_kernel, a warp or, above 512
+// experts, a CTA of eight): a lane scores whole groups, and K rounds choose.
 #include "block_router.cuh"
 
 namespace {

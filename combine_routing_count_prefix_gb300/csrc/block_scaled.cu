@@ -5,17 +5,18 @@
 // up to kMaxRows received rows, 128 features and half of the rows in each CTA.
 // What differs is where the sums live.  A block's scales are fp32, so the tensor
 // core cannot apply them: it makes the sums of one block of 128 (one step of the
-// ring, four instructions) in one of two to four buffers of tensor memory, and
+// ring, four instructions) in one of two to eight buffers of tensor memory, and
 // eight warps add them, times their scales, to sums that they hold in registers:
 //   acc[f][r] += P[f][r] * (s[r] * ws),
 // s a row's scale, ws one number for a CTA's 128 features (with SwiGLU one for its
 // gate and one for its up features).  Tiles come in two kinds:
 //   wide (more than kNarrowRows rows): the rows on the M side, the features on the
 //     N side.  A thread of the eight warps is one row and 128 features: it needs one
-//     scale a step (two with SwiGLU), and has a row's features side by side.
+//     scale a step (two with SwiGLU), read from memory four steps ahead, and has a
+//     row's features side by side.
 //   narrow: the features on the M side, up to 128 rows on the N side, so that few
 //     rows cost few columns.  A thread is one feature and up to 64 rows, whose s * ws
-//     it reads four at a time.
+//     it reads four at a time from shared memory.
 // The operands in shared memory are the same for both; only the roles differ.
 //
 // Inside a CTA of 16 warps:
@@ -23,9 +24,30 @@
 //   warp 1      (first CTA of the pair) issues the products
 //   warp 2      plans
 //   warps 4-11  sums, then the tile's epilogue
-//   warps 12-15 bring the scales to shared memory, four steps at a time
+//   warps 12-15 make narrow tiles' products of scales in shared memory, four steps at
+//               a time
 // The eight warps have kManyRegisters registers a thread, the others kFewRegisters.
 // Every wait is bounded, as there.
+//
+// What bounds it, on one GB300:
+// - few rows per expert: the weights' bytes.  256 experts x ~32 rows, 7168 -> 2 x
+//   2048, rows to rows: 1.19-1.22 ms of 1.14 (6.2-6.4 TB/s); 2048 -> 7168, 0.59 of
+//   0.58.  One row: eight experts' weights, 45-46 us of 35; 6 are launch, plan, first
+//   load and last stores.
+// - many rows: the summing warps.  A step of a wide tile is 505 cycles of the tensor
+//   core and 750 to 800 of a warp: a wait, four loads of 32 columns, 128
+//   multiply-adds, the arrival that hands the buffer back, each in the shadow of the
+//   tensor core's and the loads' traffic (an access to shared memory takes 140 cycles
+//   there).  16 experts x ~1024 rows, 7168 -> 2 x 2048: 409-417 us in a burst (2.3-2.4
+//   PFLOP/s), 445 steadily; 2048 -> 7168: 274-280, a quarter of it the epilogues of
+//   tiles of 16 steps.
+// What the structure bought, in microseconds (dense gate / up, dense down, decode):
+// the features on the M side of all tiles 963 / 436 / 1866; wide tiles, waits that
+// acquire no cluster 622 / 405 / 1827; the steps of four unrolled 534 / 412 / 1319; a
+// step's tests and scales issued in the step before 472 / 361 / 1304; scalar instead
+// of packed multiply-adds, which cost a move for every loaded pair 454 / 286 / 1278;
+// row scales from memory, no vote in a step 414 / 277 / 1239; eight buffers for tiles
+// of up to 64 rows 413 / 274 / 1218.
 #include "block_plan.cuh"
 
 namespace {
