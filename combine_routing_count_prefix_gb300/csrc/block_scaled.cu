@@ -122,11 +122,13 @@ __device__ __forceinline__ void add_rows(const uint32_t (&v)[32], uint32_t scale
 // ---------------------------------------------------------------------------
 // wide tiles: lane = row, 32 features in a chunk
 // ---------------------------------------------------------------------------
-// acc += v * scale; with SwiGLU the features are eight of gate, eight of up in turn.
-template <bool kSwiglu>
-__device__ __forceinline__ void add_features(const uint32_t (&v)[32], float gate, float up, float (&acc)[32]) {
+// acc += v * scale, from column kFrom of 32 on; with SwiGLU the features are eight of
+// gate, eight of up in turn.
+template <bool kSwiglu, int kFrom, int N>
+__device__ __forceinline__ void add_features(const uint32_t (&v)[N], float gate, float up, float (&acc)[32]) {
 #pragma unroll
-  for (int i = 0; i < 32; ++i) acc[i] = __fmaf_rn(__uint_as_float(v[i]), kSwiglu && (i & 8) ? up : gate, acc[i]);
+  for (int i = 0; i < N; ++i)
+    acc[kFrom + i] = __fmaf_rn(__uint_as_float(v[i]), kSwiglu && (i & 8) ? up : gate, acc[kFrom + i]);
 }
 
 // 32 bytes of each lane's row to y, `at` bytes into the row: neighbours swap halves,
@@ -242,8 +244,8 @@ struct Sums {
     wait(a, first + kStep);
     if constexpr (kChunks > 0) {
       uint32_t v[32];
-      tmem_load32_begin<kOffset>(at, v);
-      tmem_load32_end(v);
+      tmem_load_begin<kOffset>(at, v);
+      tmem_load_end(v);
       if (kChunks == 1) {
         release(first + kStep);
         look(next);
@@ -252,8 +254,8 @@ struct Sums {
     }
     if constexpr (kChunks > 1) {
       uint32_t v[32];
-      tmem_load32_begin<kOffset + 64>(at, v);
-      tmem_load32_end(v);
+      tmem_load_begin<kOffset + 64>(at, v);
+      tmem_load_end(v);
       release(first + kStep);
       look(next);
       add_rows<kScale + 256>(v, scale, acc[1]);
@@ -303,32 +305,36 @@ struct Sums {
       if (kBoth) w1 = __shfl_sync(0xffffffffu, w_now, 4 + kStep);
     }
   };
-  template <bool kSwiglu, int kStep>
-  __device__ __forceinline__ void wide_step(const ProductArgs& a, float (&acc)[4][32], uint32_t at, int set, bool some,
-                                            Scales& s) {
-    constexpr int kBuffer = kStep & 1, kNext = kBuffer ^ 1;
-    wait(a, kBuffer);
-    {
-      // 32 columns load while the last 32 are added
-      uint32_t v[2][32];
-      tmem_load32_begin<256 * kBuffer>(at, v[0]);
-      const float g = s.r * s.w0, u = kSwiglu ? s.r * s.w1 : g;
-      tmem_load32_end(v[0]);
-      tmem_load32_begin<256 * kBuffer + 32>(at, v[1]);
-      add_features<kSwiglu>(v[0], g, u, acc[0]);
-      if (kStep == 3) s.now = s.next, s.w_now = s.w_next;
-      s.take<(kStep + 1) % 4, kSwiglu>(kSwiglu ? 0 : 4 * set);
-      tmem_load32_end(v[1]);
-      tmem_load32_begin<256 * kBuffer + 64>(at, v[0]);
-      add_features<kSwiglu>(v[1], g, u, acc[1]);
-      tmem_load32_end(v[0]);
-      tmem_load32_begin<256 * kBuffer + 96>(at, v[1]);
-      add_features<kSwiglu>(v[0], g, u, acc[2]);
-      tmem_load32_end(v[1]);
+  // The step's columns from kAt on: N load while the last N are added.
+  template <bool kSwiglu, int kStep, int kAt, int N>
+  __device__ __forceinline__ void wide_columns(uint32_t (&v)[2][N], float (&acc)[4][32], uint32_t at, int set, float g,
+                                               float u, Scales& s) {
+    constexpr int kBuffer = kStep & 1, kNext = kBuffer ^ 1, kNow = kAt / N & 1;
+    tmem_load_end(v[kNow]);
+    if constexpr (kAt + N < 128) {
+      tmem_load_begin<256 * kBuffer + kAt + N>(at, v[kNow ^ 1]);
+    } else {
       release(kBuffer);
       look(kNext);
-      add_features<kSwiglu>(v[1], g, u, acc[3]);
     }
+    add_features<kSwiglu, kAt % 32>(v[kNow], g, u, acc[kAt / 32]);
+    if constexpr (kAt + N == 32) {
+      if (kStep == 3) s.now = s.next, s.w_now = s.w_next;
+      s.take<(kStep + 1) % 4, kSwiglu>(kSwiglu ? 0 : 4 * set);
+    }
+    if constexpr (kAt + N < 128) wide_columns<kSwiglu, kStep, kAt + N>(v, acc, at, set, g, u, s);
+  }
+  template <bool kSwiglu, int kStep>
+  __device__ __forceinline__ void wide_step(const ProductArgs& a, float (&acc)[4][32], uint32_t at, int set, Scales& s) {
+    constexpr int kBuffer = kStep & 1;
+    wait(a, kBuffer);
+    // 16 columns at a time in the plain product, which spills fewer registers for it than
+    // with 32 (2048 -> 7168 of 2048 rows an expert 264 against 274 us); 32 with SwiGLU,
+    // which spills few either way (7168 -> 2 x 2048 410 against 422)
+    uint32_t v[2][kSwiglu ? 32 : 16];
+    tmem_load_begin<256 * kBuffer>(at, v[0]);
+    const float g = s.r * s.w0, u = kSwiglu ? s.r * s.w1 : g;
+    wide_columns<kSwiglu, kStep, 0>(v, acc, at, set, g, u, s);
   }
   template <bool kSwiglu>
   __device__ __forceinline__ void wide(const ProductArgs& a, float (&acc)[4][32], uint32_t at, int set, bool some,
@@ -351,10 +357,10 @@ struct Sums {
     s.take<0, kSwiglu>(kSwiglu ? 0 : 4 * set);
     for (int k = 0; k < a.steps; k += 4) {
       s.load(k + 4, a.steps);
-      wide_step<kSwiglu, 0>(a, acc, at, set, some, s);
-      if (k + 1 < a.steps) wide_step<kSwiglu, 1>(a, acc, at, set, some, s);
-      if (k + 2 < a.steps) wide_step<kSwiglu, 2>(a, acc, at, set, some, s);
-      if (k + 3 < a.steps) wide_step<kSwiglu, 3>(a, acc, at, set, some, s);
+      wide_step<kSwiglu, 0>(a, acc, at, set, s);
+      if (k + 1 < a.steps) wide_step<kSwiglu, 1>(a, acc, at, set, s);
+      if (k + 2 < a.steps) wide_step<kSwiglu, 2>(a, acc, at, set, s);
+      if (k + 3 < a.steps) wide_step<kSwiglu, 3>(a, acc, at, set, s);
     }
   }
 };
