@@ -328,9 +328,9 @@ struct Sums {
   __device__ __forceinline__ void wide_step(const ProductArgs& a, float (&acc)[4][32], uint32_t at, int set, Scales& s) {
     constexpr int kBuffer = kStep & 1;
     wait(a, kBuffer);
-    // 16 columns at a time in the plain product, which spills fewer registers for it than
-    // with 32 (2048 -> 7168 of 2048 rows an expert 264 against 274 us); 32 with SwiGLU,
-    // which spills few either way (7168 -> 2 x 2048 410 against 422)
+    // 16 columns at a time in the plain product, whose rows' and features' epilogue then
+    // spills half the registers (2048 -> 7168 of 2048 rows an expert 264 us, 274 with 32);
+    // with SwiGLU 32 (7168 -> 2 x 2048 410 us, 422 with 16)
     uint32_t v[2][kSwiglu ? 32 : 16];
     tmem_load_begin<256 * kBuffer>(at, v[0]);
     const float g = s.r * s.w0, u = kSwiglu ? s.r * s.w1 : g;
