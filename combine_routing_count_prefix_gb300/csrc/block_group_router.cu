@@ -8,10 +8,9 @@
 // keys, which at least K keys do.  Those few go to shared memory, a lane each, and
 // their rank among them, counted too, is their place in the result.  Keys are
 // 32-bit integers that order like the floats (0: cannot be chosen).
-// Instructions bound a large batch: about 1070 a token of 256 experts in 8 groups,
-// 8192 tokens 9.9 us (with keys in shared memory, a lane scoring whole groups and K
-// rounds of reductions over all keys 21.3), one token 3.5; 4096 tokens of 160 experts,
-// softmax, 7.1.
+// Instructions bound a large batch: 8192 tokens of 256 experts in 8 groups 8.2 us (with
+// keys in shared memory, a lane scoring whole groups and K rounds of reductions over
+// all keys 21.3), one token 2.3; 4096 tokens of 160 experts, softmax, 5.4.
 // Any other row lies in shared memory as keys (rows_kernel, a warp or, above 512
 // experts, a CTA of eight): a lane scores whole groups, and K rounds choose.
 #include "block_router.cuh"
@@ -78,6 +77,18 @@ __device__ __forceinline__ void store_choice(const GroupRouterArgs& a, int64_t r
     a.topk_idx[row * a.K + lane] = -1;
     a.topk_w[row * a.K + lane] = 0.0f;
   }
+}
+
+// 1 / d to the nearest fp32, what __frcp_rn gives, for d from 1 to 2^126 (all of them
+// compared): the hardware's reciprocal and one step of Newton's, whose remainder is
+// exact in a fused multiply-add.  Without the general one's other ranges, which a
+// lane's experts would each have in line: one token 2.9 us against 3.8, 8192 tokens
+// 9.1 against 9.9.  So 1 / (1 + exp(-v)) for v from -87 on; a token with a logit below
+// (-infinity among them) takes the general one.
+__device__ __forceinline__ float one_over(float d) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+  return fmaf(fmaf(-d, r, 1.0f), r, r);
 }
 
 template <int W, bool kSoftmax>
@@ -148,39 +159,67 @@ __global__ void __launch_bounds__(256) rows_kernel(GroupRouterArgs a) {
 }
 
 // V: experts a lane holds at most; kVec: fp32 logits, four experts of a lane in a row.
+// Biases are asked for with the logits (read where they are added: 9.1 us against 8.7).
+// Experts that a lane has not, and a masked token's, are NaN: no key, and not far.
+// CTAs an SM: a softmax keeps its logits too, and with 51 registers a thread, not 64,
+// asks for them in parts (6.4 us against 5.4); a large sigmoid gains by a fifth CTA (8.2, 8.1).
 template <int V, bool kVec, bool kSoftmax>
-__global__ void __launch_bounds__(256, V > 8 ? 3 : 5) lanes_kernel(GroupRouterArgs a) {
-  __shared__ uint2 gathered[8][32];
+__global__ void __launch_bounds__(256, V > 8 ? 3 : kSoftmax ? 4 : 5) lanes_kernel(GroupRouterArgs a) {
+  __shared__ __align__(16) uint64_t gathered[8][32];  // a key, and below it ~expert: the lower of equals is ahead
   wait_prior_grid();
   release_next_grid();
   const int lane = threadIdx.x & 31, L = 32 / a.G, g = lane / L, q = lane - g * L;
-  uint2* list = gathered[threadIdx.x >> 5];
+  uint64_t* list = gathered[threadIdx.x >> 5];
   // the lane's i-th expert, of its group: in order over the group's lanes, or four in a row
   const auto expert = [&](int i) { return kVec ? (i / 4 * L + q) * 4 + i % 4 : i * L + q; };
   const int64_t step = ((int64_t)gridDim.x * blockDim.x) >> 5;
   for (int64_t row = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; row < a.rows; row += step) {
     const bool on = a.active == nullptr || a.active[row] != 0;
     const int64_t at = row * a.E + g * a.S;
-    float l[V];
+    float l[V], b[V];
     if constexpr (kVec) {
 #pragma unroll
       for (int i = 0; i < V; i += 4) {
-        float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (a.bias != nullptr && expert(i) < a.S) v = *reinterpret_cast<const float4*>(a.bias + g * a.S + expert(i));
+        b[i] = v.x, b[i + 1] = v.y, b[i + 2] = v.z, b[i + 3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) b[i] = a.bias != nullptr && expert(i) < a.S ? a.bias[g * a.S + expert(i)] : 0.0f;
+    }
+    if constexpr (kVec) {
+#pragma unroll
+      for (int i = 0; i < V; i += 4) {
+        float4 v = make_float4(NAN, NAN, NAN, NAN);
         if (on && expert(i) < a.S) v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) + at + expert(i));
         l[i] = v.x, l[i + 1] = v.y, l[i + 2] = v.z, l[i + 3] = v.w;
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < V; ++i) l[i] = on && expert(i) < a.S ? load_logit(a.logits, a.dtype, at + expert(i)) : -INFINITY;
+      for (int i = 0; i < V; ++i) l[i] = on && expert(i) < a.S ? load_logit(a.logits, a.dtype, at + expert(i)) : NAN;
     }
     uint32_t key[V], best = 0, second = 0;
+    const auto keys = [&](auto score) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      float k = kSoftmax ? l[i] : sigmoid_score(l[i]);
-      if (a.bias != nullptr && expert(i) < a.S) k += a.bias[g * a.S + expert(i)];
-      key[i] = order(l[i], k);
-      second = max(second, min(best, key[i]));
-      best = max(best, key[i]);
+      for (int i = 0; i < V; ++i) {
+        float k = score(l[i]);
+        k += b[i];
+        key[i] = order(l[i], k);
+        second = max(second, min(best, key[i]));
+        best = max(best, key[i]);
+      }
+    };
+    if constexpr (kSoftmax) {
+      keys([](float v) { return v; });
+    } else {
+      float far = 0.0f;  // NaN is not far
+#pragma unroll
+      for (int i = 0; i < V; ++i) far = fmaxf(far, -l[i]);
+      if (__all_sync(0xffffffffu, far <= 87.0f))
+        keys([](float v) { return one_over(1.0f + expf(-v)); });
+      else
+        keys([](float v) { return sigmoid_score(v); });
     }
     float top = -INFINITY, total = 0.0f;
     if (kSoftmax && !a.renorm) {
@@ -208,11 +247,14 @@ __global__ void __launch_bounds__(256, V > 8 ? 3 : 5) lanes_kernel(GroupRouterAr
         for (int d = 1; d < L; d <<= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, d));
       }
       const uint32_t score = group_score(best, second);
-      int ahead = 0;
-      for (int o = 0; o < a.G; ++o) {
+      int ahead = 0;  // the group's lanes count a part of the others each (all by each: 8.3 us against 8.2)
+#pragma unroll 1
+      for (int first = 0; first < a.G; first += L) {
+        const int o = first + q;
         const uint32_t other = __shfl_sync(0xffffffffu, score, o * L);
-        ahead += other > score || (other == score && o < g);
+        ahead += o < a.G && (other > score || (other == score && o < g));
       }
+      for (int d = 1; d < L; d <<= 1) ahead += __shfl_xor_sync(0xffffffffu, ahead, d);
       if (ahead >= a.kept) {
         lane_best = 0;
 #pragma unroll
@@ -222,7 +264,6 @@ __global__ void __launch_bounds__(256, V > 8 ? 3 : 5) lanes_kernel(GroupRouterAr
     uint32_t bound = 0, left = lane_best;
     for (int k = 0; k < a.K; ++k) {
       bound = __reduce_max_sync(0xffffffffu, left);
-      if (bound == 0) break;  // fewer lanes than K: every key
       if (left == bound) left = 0;
     }
     const uint32_t least = max(bound, 1u);
@@ -233,22 +274,23 @@ __global__ void __launch_bounds__(256, V > 8 ? 3 : 5) lanes_kernel(GroupRouterAr
       const bool in = key[i] >= least;
       const uint32_t who = __ballot_sync(0xffffffffu, in);
       const int to = n + __popc(who & ((1u << lane) - 1));
-      if (in && to < 32) {
-        list[to] = make_uint2(key[i], (uint32_t)(g * a.S + expert(i)));
-      }
+      if (in && to < 32) list[to] = (uint64_t)key[i] << 32 | (uint32_t)~(g * a.S + expert(i));
       n += __popc(who);
     }
     __syncwarp();
     if (n <= 32) {
-      const uint2 mine = lane < n ? list[lane] : make_uint2(0, 0);
+      if (lane >= n) list[lane] = 0;
+      __syncwarp();
+      const uint64_t mine = list[lane];
+      const int e = (int)~(uint32_t)mine;
       int place = 0;
-      for (int o = 0; o < n; ++o) {
-        const uint2 other = list[o];
-        place += other.x > mine.x || (other.x == mine.x && other.y < mine.y);
+      for (int o = 0; o < n; o += 4) {
+        const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(list + o), y = *reinterpret_cast<const ulonglong2*>(list + o + 2);
+        place += (x.x > mine) + (x.y > mine) + (y.x > mine) + (y.y > mine);
       }
       const bool chosen = lane < n && place < a.K;
-      store_choice<kSoftmax>(a, row, chosen ? (int)mine.y : -1, chosen ? load_logit(a.logits, a.dtype, row * a.E + (int)mine.y) : -INFINITY, place, min(n, a.K), top,
-                             total);
+      const float v = chosen ? load_logit(a.logits, a.dtype, row * a.E + e) : -INFINITY;
+      store_choice<kSoftmax>(a, row, chosen ? e : -1, v, place, min(n, a.K), top, total);
       continue;
     }
     // many keys at the bound, or few lanes: rounds of two reductions, over all keys
@@ -287,7 +329,7 @@ int launch_group_router(const GroupRouterArgs& a, llmoe_stream_t stream) {
   if (32 % a.G == 0) {
     const int L = 32 / a.G, each = (a.S + L - 1) / L;  // experts a lane holds
     // a lane's experts four in a row where the group's are whole fours for each lane
-    const bool vec = a.dtype == LLMOE_DTYPE_FP32 && a.S % (4 * L) == 0 && aligned(a.logits, 16);
+    const bool vec = a.dtype == LLMOE_DTYPE_FP32 && a.S % (4 * L) == 0 && aligned(a.logits, 16) && aligned(a.bias, 16);
     if (each <= 1) return launch_lanes<1, kSoftmax>(a, vec, stream);
     if (each <= 2) return launch_lanes<2, kSoftmax>(a, vec, stream);
     if (each <= 4) return launch_lanes<4, kSoftmax>(a, vec, stream);

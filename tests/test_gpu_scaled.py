@@ -286,6 +286,42 @@ def test_group_router_masked_experts(L, E, scoring, top2):
         assert np.allclose(gw, w, rtol=64 * 2.0 ** -23, atol=0)
 
 
+@pytest.mark.parametrize("E,K,groups,kept", [(256, 8, 8, 4), (160, 6, 8, 3), (512, 8, 16, 5), (96, 3, 3, 2), (32, 4, 4, 2)])
+@pytest.mark.parametrize("top2", [True, False])
+def test_group_router_far_logits(L, E, K, groups, kept, top2):
+    """Sigmoids near fp32's smallest: still the largest logits', and with their weights.
+    Keys a 16th apart differ by 6%; -88.5 has 2^21 of fp32's smallest steps (2^-149),
+    so half a step is less than 2^-22 of it."""
+    rows = 24
+    g = rnd(E + kept)
+    logits = torch.stack([torch.randperm(E, generator=g).float() / 16 - 88.5 for _ in range(rows)])
+    other = torch.rand(rows, E, generator=g)
+    logits[8:16] += (other[8:16] < 0.1) * 60.0  # near ones among them, no sigmoid of them 1
+    logits[16:][other[16:] < 0.5] = -float("inf")
+    gi, gw = route(L, logits, None, None, K, groups, kept, top2, "fp32", "sigmoid", True, 2.5)
+    idx, w, _ = fp8b.group_router(logits.numpy(), None, None, K, groups, kept, top2, "sigmoid", True, 2.5, same=0)
+    if top2:  # sums of two keys may be as near as rounding
+        same = (gi == idx).all(1)
+        assert same.mean() > 0.9
+        gi, gw, idx, w = gi[same], gw[same], idx[same], w[same]
+    assert np.array_equal(gi, idx)
+    assert (np.abs(gw - w) <= w * (K + 32 + 2 * 2) * 2.0 ** -23 + 2.5 * 2.0 ** -149).all()
+
+
+@pytest.mark.parametrize("E,groups", [(256, 8), (160, 8), (264, 8)])
+def test_group_router_bias_not_16_byte_aligned(L, E, groups):
+    rows, K = 70, 6
+    logits = torch.randint(-24, 25, (rows, E), generator=rnd(E)).float() / 8
+    flat = torch.randint(-8, 9, (E + 1,), generator=rnd(1)).float() / 8
+    idx = torch.empty(rows, K, dtype=torch.int64, device="cuda")
+    w = torch.empty(rows, K, device="cuda")
+    L.llmoe_group_router(logits.cuda(), flat.cuda()[1:], None, idx, w, rows, E, K, groups, 3, L.LLMOE_DTYPE_FP32,
+                         L.LLMOE_SCORE_SOFTMAX, 0, 1.0)
+    want, ww, _ = fp8b.group_router(logits.numpy(), flat[1:].numpy(), None, K, groups, 3, False, "softmax", False, 1.0)
+    assert np.array_equal(idx.cpu().numpy(), want)
+    assert (np.abs(wide(w) - ww) <= ww * (E / 32 + K + 32) * 2.0 ** -23).all()
+
+
 @pytest.mark.parametrize("E,groups", [(256, 8), (100, 5), (264, 8), (768, 8)])
 def test_group_router_logits_not_16_byte_aligned(L, E, groups):
     rows, K = 70, 6
