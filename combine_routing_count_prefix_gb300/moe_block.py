@@ -49,11 +49,15 @@ def pack_mx8(w: torch.Tensor) -> torch.Tensor:
 def pack_fp8b_weights(w: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
     """Matrices [..., rows, cols] as e4m3 codes (uint8, the same shape) and the fp32
     scales [..., ceil(rows / 128), ceil(cols / 128)] of their 128 x 128 blocks."""
+    code = {torch.bfloat16: llmoe.LLMOE_DTYPE_BF16, torch.float16: llmoe.LLMOE_DTYPE_FP16,
+            torch.float32: llmoe.LLMOE_DTYPE_FP32}.get(w.dtype)
+    if code is None:
+        raise ValueError(f"weights are bf16, fp16 or fp32, not {w.dtype}")
+    if w.dim() < 2 or 0 in w.shape[-2:]:
+        raise ValueError(f"no matrices: {tuple(w.shape)}")
     rows, cols = w.shape[-2:]
     if cols % 16:
         raise ValueError(f"rows of {cols} codes are not whole 16 bytes")
-    code = {torch.bfloat16: llmoe.LLMOE_DTYPE_BF16, torch.float16: llmoe.LLMOE_DTYPE_FP16,
-            torch.float32: llmoe.LLMOE_DTYPE_FP32}[w.dtype]
     codes = torch.empty(w.shape, dtype=torch.uint8, device=w.device)
     scales = torch.empty(*w.shape[:-2], _blocks(rows), _blocks(cols), dtype=torch.float32, device=w.device)
     llmoe.llmoe_pack_fp8b_weights(w.contiguous(), codes, scales, w.numel() // (rows * cols), rows, cols, code)

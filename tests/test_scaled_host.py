@@ -147,3 +147,13 @@ def test_block_refusals(lib, what, kw):
     a.update(kw)
     with pytest.raises(ValueError, match=rf"\b{what}\b"):
         MoEBlock(**a)
+
+
+@pytest.mark.parametrize("what,w", [("16 bytes", z(2, 4, 24)), ("bf16", z(2, 4, 32, dtype=torch.float64)),
+                                    ("no matrices", z(32)), ("no matrices", z(2, 0, 32)), ("no matrices", z(2, 4, 0)),
+                                    ("CUDA", z(2, 4, 32))])
+def test_weight_packing_refusals(lib, what, w):
+    from combine_routing_count_prefix_gb300.moe_block import pack_fp8b_weights
+
+    with pytest.raises(ValueError, match=what):
+        pack_fp8b_weights(w)
