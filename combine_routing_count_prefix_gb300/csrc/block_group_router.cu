@@ -8,7 +8,7 @@
 // keys, which at least K keys do.  Those few go to shared memory, a lane each, and
 // their rank among them, counted too, is their place in the result.  Keys are
 // 32-bit integers that order like the floats (0: cannot be chosen).
-// Instructions bound a large batch: 8192 tokens of 256 experts in 8 groups 8.2 us (with
+// Instructions bound a large batch: 8192 tokens of 256 experts in 8 groups 7.8 us (with
 // keys in shared memory, a lane scoring whole groups and K rounds of reductions over
 // all keys 21.3), one token 2.3; 4096 tokens of 160 experts, softmax, 5.4.
 // Any other row lies in shared memory as keys (rows_kernel, a warp or, above 512
@@ -158,9 +158,17 @@ __global__ void __launch_bounds__(256) rows_kernel(GroupRouterArgs a) {
   }
 }
 
+// order() of a key that is NaN where its logit may not be chosen, and never -0: a sum
+// of 1 / (1 + exp(-l)) and a bias (l of -infinity: one_over gives NaN).
+__device__ __forceinline__ uint32_t order_of_sum(float key) {
+  const uint32_t b = __float_as_uint(key);
+  return key > -INFINITY ? b ^ ((uint32_t)((int)b >> 31) | 0x80000000u) : 0u;
+}
+
 // V: experts a lane holds at most; kVec: fp32 logits, four experts of a lane in a row.
 // Biases are asked for with the logits (read where they are added: 9.1 us against 8.7).
-// Experts that a lane has not, and a masked token's, are NaN: no key, and not far.
+// Experts that a lane has not are NaN: no key, and not far.  A masked token's logits are
+// asked for too, not behind its mask (8.1 us against 7.9, a tenth masked).
 // CTAs an SM: a softmax keeps its logits too, and with 51 registers a thread, not 64,
 // asks for them in parts (6.4 us against 5.4); a large sigmoid gains by a fifth CTA (8.2, 8.1).
 template <int V, bool kVec, bool kSoftmax>
@@ -192,15 +200,19 @@ __global__ void __launch_bounds__(256, V > 8 ? 3 : kSoftmax ? 4 : 5) lanes_kerne
 #pragma unroll
       for (int i = 0; i < V; i += 4) {
         float4 v = make_float4(NAN, NAN, NAN, NAN);
-        if (on && expert(i) < a.S) v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) + at + expert(i));
+        if (expert(i) < a.S) v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) + at + expert(i));
         l[i] = v.x, l[i + 1] = v.y, l[i + 2] = v.z, l[i + 3] = v.w;
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < V; ++i) l[i] = on && expert(i) < a.S ? load_logit(a.logits, a.dtype, at + expert(i)) : NAN;
+      for (int i = 0; i < V; ++i) l[i] = expert(i) < a.S ? load_logit(a.logits, a.dtype, at + expert(i)) : NAN;
+    }
+    if (!on) {  // chooses nothing
+      if (lane < a.K) a.topk_idx[row * a.K + lane] = -1, a.topk_w[row * a.K + lane] = 0.0f;
+      continue;
     }
     uint32_t key[V], best = 0, second = 0;
-    const auto keys = [&](auto score) {
+    const auto keys = [&](auto score, auto order) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         float k = score(l[i]);
@@ -211,15 +223,15 @@ __global__ void __launch_bounds__(256, V > 8 ? 3 : kSoftmax ? 4 : 5) lanes_kerne
       }
     };
     if constexpr (kSoftmax) {
-      keys([](float v) { return v; });
+      keys([](float v) { return v; }, order);
     } else {
       float far = 0.0f;  // NaN is not far
 #pragma unroll
       for (int i = 0; i < V; ++i) far = fmaxf(far, -l[i]);
       if (__all_sync(0xffffffffu, far <= 87.0f))
-        keys([](float v) { return one_over(1.0f + expf(-v)); });
+        keys([](float v) { return one_over(1.0f + expf(-v)); }, [](float, float k) { return order_of_sum(k); });
       else
-        keys([](float v) { return sigmoid_score(v); });
+        keys([](float v) { return sigmoid_score(v); }, order);
     }
     float top = -INFINITY, total = 0.0f;
     if (kSoftmax && !a.renorm) {

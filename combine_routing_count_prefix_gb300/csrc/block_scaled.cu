@@ -35,11 +35,11 @@
 //   0.58.  One row: eight experts' weights, 45-46 us of 35; 6 are launch, plan, first
 //   load and last stores.
 // - many rows: the summing warps.  A step of a wide tile is 505 cycles of the tensor
-//   core and 750 to 800 of a warp: a wait, four loads of 32 columns, 128
+//   core and 750 to 800 of a warp: a wait, loads of 128 columns, 128
 //   multiply-adds, the arrival that hands the buffer back, each in the shadow of the
 //   tensor core's and the loads' traffic (an access to shared memory takes 140 cycles
 //   there).  16 experts x ~1024 rows, 7168 -> 2 x 2048: 409-417 us in a burst (2.3-2.4
-//   PFLOP/s), 445 steadily; 2048 -> 7168: 274-280, a quarter of it the epilogues of
+//   PFLOP/s), 445 steadily; 2048 -> 7168: 264-272, a quarter of it the epilogues of
 //   tiles of 16 steps.
 // What the structure bought, in microseconds (dense gate / up, dense down, decode):
 // the features on the M side of all tiles 963 / 436 / 1866; wide tiles, waits that
@@ -47,7 +47,8 @@
 // step's tests and scales issued in the step before 472 / 361 / 1304; scalar instead
 // of packed multiply-adds, which cost a move for every loaded pair 454 / 286 / 1278;
 // row scales from memory, no vote in a step 414 / 277 / 1239; eight buffers for tiles
-// of up to 64 rows 413 / 274 / 1218.
+// of up to 64 rows 413 / 274 / 1218; a plain product's sums read 16 columns at a time
+// 410 / 264 / 1219.
 #include "block_plan.cuh"
 
 namespace {
