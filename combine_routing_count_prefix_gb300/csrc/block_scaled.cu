@@ -418,12 +418,16 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     mbar_init_fence();
   }
   if (warp == 3) tmem_alloc_pair(sbase + l.tmem, 512);
+  // The pair's barriers and tensor memory are there behind the wait, which the prior
+  // grid's and the counting hide (a call of one tile a pair 7.5 us, 8.0 with both parts there)
+  tc_fence_before();
+  __syncwarp();
+  cluster_arrive();
   wait_prior_grid();
   release_next_grid();
   count_shares<kMaxRows, kThreads>(a, prefix, reinterpret_cast<int*>(smem + l.part));
-  tc_fence_before();
   __syncthreads();
-  cluster_sync();
+  cluster_wait();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + l.tmem);
 
