@@ -32,8 +32,8 @@
 // What bounds it, on one GB300:
 // - few rows per expert: the weights' bytes.  256 experts x ~32 rows, 7168 -> 2 x
 //   2048, rows to rows: 1.19-1.22 ms of 1.14 (6.2-6.4 TB/s); 2048 -> 7168, 0.59 of
-//   0.58.  One row: eight experts' weights, 45-46 us of 35; 6 are launch, plan, first
-//   load and last stores.
+//   0.58.  One row: eight experts' weights, 44 us of 35; 6 are launch, plan, first
+//   load and last stores, and the tiles are 1.7 rounds of the pairs.
 // - many rows: the summing warps.  A step of a wide tile is 505 cycles of the tensor
 //   core and 750 to 800 of a warp: a wait, loads of 128 columns, 128
 //   multiply-adds, the arrival that hands the buffer back, each in the shadow of the
@@ -54,7 +54,16 @@
 namespace {
 
 constexpr int kMaxRows = 256, kNarrowRows = 128, kThreads = 512;
-constexpr int kBytesA = 128 * 128, kBytesB = kMaxRows / 2 * 128, kStage = kBytesA + kBytesB;
+constexpr int kBytesA = 128 * 128;
+// Bytes and number of the ring's stages.  kFew: a call whose experts have room for
+// kNarrowRows rows at most, so that no tile is wide; a stage then has half the room
+// for rows, and there are more of them under way (one token, 128 tiles: 44.0 us
+// against 45.1 with the other kernel).
+template <bool kFew>
+constexpr int kStage = kBytesA + (kFew ? kNarrowRows : kMaxRows) / 2 * 128;
+template <bool kFew>
+constexpr int kRing = kFew ? 8 : kStages;
+static_assert(kRing<true> * kStage<true> == kRing<false> * kStage<false>, "the same room");
 constexpr int kManyRegisters = 200, kFewRegisters = 56;
 static_assert(256 * (kManyRegisters + kFewRegisters) <= 65536, "what a launch of 512 threads has");
 constexpr int kBuffers = 8;  // of tensor memory: 8 of 64 columns, 4 of 128 or, for wide tiles, 2 of 256
@@ -74,16 +83,16 @@ struct ScaledArgs {
 struct ScaledSmem {
   uint32_t scales, amax, row_max, boxes, rows, tiles, bars, tmem, part, prefix, total;
 };
-__host__ __device__ inline ScaledSmem scaled_smem(int stages, int E) {
+__host__ __device__ inline ScaledSmem scaled_smem(int stages, int stage, int E) {
   ScaledSmem l;
-  uint32_t at = stages * kStage;
+  uint32_t at = stages * stage;
   l.scales = at, at += kSlots * kSlot;
   l.amax = at, at += 8 * kNarrowRows * 4;   // narrow: [warp of the pair's set][row]
   l.row_max = at, at += 2 * 2 * 128 * 4;    // wide: [tile's parity][set][row]
   l.boxes = at, at += kPlanDepth * 32 * 16;
   l.rows = at, at += kPlanDepth * kMaxRows * 4;
   l.tiles = at, at += kPlanDepth * (uint32_t)sizeof(Tile);
-  l.bars = at, at += (2 * kStages + 2 * kBuffers + 2 * kPlanDepth + 2 * kSlots + 4 + 4) * 8;
+  l.bars = at, at += (2 * kRing<true> + 2 * kBuffers + 2 * kPlanDepth + 2 * kSlots + 4 + 4) * 8;
   l.tmem = at, at += 16;
   l.part = at, at += 64;
   l.prefix = at, at += (E + 1) * 4;
@@ -369,7 +378,7 @@ struct Sums {
 // ---------------------------------------------------------------------------
 // the kernel
 // ---------------------------------------------------------------------------
-template <bool kSwiglu>
+template <bool kSwiglu, bool kFew>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     scaled_kernel(const __grid_constant__ ScaledArgs s, const __grid_constant__ ProductMaps maps) {
   extern __shared__ uint8_t smem_raw[];
@@ -377,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   const uint32_t raw = smem_addr(smem_raw);
   uint8_t* smem = smem_raw + ((1024 - raw % 1024) % 1024);
   const uint32_t sbase = smem_addr(smem);
-  const ScaledSmem l = scaled_smem(a.stages, a.E);
+  const ScaledSmem l = scaled_smem(a.stages, kStage<kFew>, a.E);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
@@ -386,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   Box* boxes = reinterpret_cast<Box*>(smem + l.boxes);
   Tile* tiles = reinterpret_cast<Tile*>(smem + l.tiles);
   int* prefix = reinterpret_cast<int*>(smem + l.prefix);
-  const uint32_t full = sbase + l.bars, empty = full + 8 * kStages, acc_full = empty + 8 * kStages,
+  const uint32_t full = sbase + l.bars, empty = full + 8 * kRing<kFew>, acc_full = empty + 8 * kRing<kFew>,
                  acc_empty = acc_full + 8 * kBuffers, plan_full = acc_empty + 8 * kBuffers,
                  plan_empty = plan_full + 8 * kPlanDepth, scale_full = plan_empty + 8 * kPlanDepth,
                  scale_empty = scale_full + 8 * kSlots, amax_full = scale_empty + 8 * kSlots, amax_empty = amax_full + 16,
@@ -438,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     fewer_registers<kFewRegisters>();
     if (warp == 0 || warp == 3) {
       if (elect_one())
-        load_tiles<kStage, kBytesA, 128, kSwiglu, 4>(a, maps, sbase, bars, tiles, boxes, warp == 3, rank, pair_id, pairs,
+        load_tiles<kStage<kFew>, kBytesA, 128, kSwiglu, 4>(a, maps, sbase, bars, tiles, boxes, warp == 3, rank, pair_id, pairs,
                                                   ntiles);
     } else if (warp == 1) {
       // ---- products: one thread -----------------------------------------------------
@@ -452,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           const int slot = i % kPlanDepth;
           if (!(ok = mbar_wait_cta(plan_full + 8 * slot, (i / kPlanDepth) & 1, a.err))) break;
           const int rows_n = columns(tiles[slot].groups), was = count;
-          const bool wide = rows_n > kNarrowRows;
+          const bool wide = !kFew && rows_n > kNarrowRows;
           const uint32_t n = wide ? kTileFeatures : rows_n, idesc = a.idesc | (n >> 3) << 17;
           mbar_arrive(plan_empty + 8 * slot);
           count = buffers_of(rows_n);
@@ -460,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           if (count != was)  // other columns: every buffer has to be handed back
             for (int b = 0; b < kBuffers && ok; ++b) ok = mbar_wait_cta(acc_empty + 8 * b, (phases >> b & 1) ^ 1, a.err);
           for (int k = 0; k < a.steps && ok; ++k) {
-            const uint32_t w = desc + (uint32_t)(stage * (kStage >> 4)), x = w + (kBytesA >> 4);
+            const uint32_t w = desc + (uint32_t)(stage * (kStage<kFew> >> 4)), x = w + (kBytesA >> 4);
             const uint32_t m_side = wide ? x : w, n_side = wide ? w : x;
             const int b = k & (count - 1);
             // the later of the two, most often, last
@@ -508,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       const int slot = i % kPlanDepth;
       mbar_wait_cta_warp(plan_full + 8 * slot, (i / kPlanDepth) & 1, ok, a.err);
       const Tile tile = tiles[slot];
-      if (!ok || !is_wide(tile)) return;
+      if (!ok || kFew || !is_wide(tile)) return;
       const int half = columns(tile.groups) / 2;  // the pair's halves of the list
       row = 32 * w + lane < half ? rows[slot * kMaxRows + (int)rank * half + 32 * w + lane] : -1;
       scales.row = reinterpret_cast<const float4*>(a.x + (uint64_t)max(row, 0) * a.x_row + a.in);
@@ -524,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       const Tile tile = tiles[slot];
       const int* list = rows + slot * kMaxRows;
       ++i;
-      if (is_wide(tile)) {
+      if (!kFew && is_wide(tile)) {
         // set: which half of each CTA's features
         const bool some = 32 * w < columns(tile.groups) / 2;
         constexpr int kChunks = 4;
@@ -747,7 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-template <bool kSwiglu>
+template <bool kSwiglu, bool kFew>
 int launch_scaled(ScaledArgs& s, llmoe_stream_t stream) {
   ProductArgs& a = s.p;
   a.steps = s.across;
@@ -756,9 +765,9 @@ int launch_scaled(ScaledArgs& s, llmoe_stream_t stream) {
   const uint64_t groups = (uint64_t)((a.T + kGroup - 1) / kGroup) * a.R, share = kMaxRows / kGroup;
   const uint64_t most = (groups + share - 1) / share * a.E * a.blocks;
   if (most > INT32_MAX) return LLMOE_ERR_INVALID_ARGUMENT;
-  a.stages = kStages;
-  while (scaled_smem(a.stages, a.E).total > kMaxSmem) --a.stages;
-  const size_t smem = scaled_smem(a.stages, a.E).total;
+  a.stages = kRing<kFew>;
+  while (scaled_smem(a.stages, kStage<kFew>, a.E).total > kMaxSmem) --a.stages;
+  const size_t smem = scaled_smem(a.stages, kStage<kFew>, a.E).total;
   a.idesc = (uint32_t)(kTileFeatures >> 4) << 24 | 1u << 4;  // e4m3 operands, fp32 sums, M = 256
 
   ProductMaps maps;
@@ -781,10 +790,10 @@ int launch_scaled(ScaledArgs& s, llmoe_stream_t stream) {
     const cuuint32_t box[3] = {128, 128, 1};
     if (!make_map(&maps.w, a.w, a.dtype, dims, strides, box, 3)) return LLMOE_ERR_CUDA;
   }
-  static_assert((kStages - 1) * kStage > kMaxSmem / 2, "one CTA per SM");
-  const int pairs = resident_pairs<scaled_kernel<kSwiglu>>(kThreads);
+  static_assert((kRing<kFew> - 1) * kStage<kFew> > kMaxSmem / 2, "one CTA per SM");
+  const int pairs = resident_pairs<scaled_kernel<kSwiglu, kFew>>(kThreads);
   if (pairs < 1) return LLMOE_ERR_CUDA;
-  return launch_block(scaled_kernel<kSwiglu>, 2 * (unsigned)std::min<uint64_t>(most, pairs), kThreads, smem, stream, s,
+  return launch_block(scaled_kernel<kSwiglu, kFew>, 2 * (unsigned)std::min<uint64_t>(most, pairs), kThreads, smem, stream, s,
                       maps);
 }
 
@@ -811,5 +820,7 @@ extern "C" int llmoe_expert_product_fp8b(const void* x, const void* w, const flo
     return LLMOE_ERR_INVALID_ARGUMENT;
   a.w = static_cast<const uint8_t*>(w);
   s.w_scale = w_scale;
-  return swiglu ? launch_scaled<true>(s, stream) : launch_scaled<false>(s, stream);
+  if ((int64_t)((a.T + kGroup - 1) / kGroup) * a.R <= kNarrowRows / kGroup)
+    return swiglu ? launch_scaled<true, true>(s, stream) : launch_scaled<false, true>(s, stream);
+  return swiglu ? launch_scaled<true, false>(s, stream) : launch_scaled<false, false>(s, stream);
 }
