@@ -447,8 +447,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     fewer_registers<kFewRegisters>();
     if (warp == 0 || warp == 3) {
       if (elect_one())
-        load_tiles<kStage<kFew>, kBytesA, 128, kSwiglu, 4>(a, maps, sbase, bars, tiles, boxes, warp == 3, rank, pair_id, pairs,
-                                                  ntiles);
+        load_tiles<kStage<kFew>, kBytesA, 128, kSwiglu, 4>(a, maps, sbase, bars, tiles, boxes, warp == 3, rank, pair_id,
+                                                           pairs, ntiles);
     } else if (warp == 1) {
       // ---- products: one thread -----------------------------------------------------
       if (leader && elect_one()) {

@@ -493,6 +493,25 @@ def test_product_many_tiles(L, out_dtype, swiglu):
     check_product(L, 2, 300, 4, 784, 2320, out_dtype, swiglu, some_counts(4, 2, 300, "ragged", 5))
 
 
+@pytest.mark.parametrize("out_dtype,swiglu", [("bf16", False), ("fp16", True), ("fp8b", True)])
+@pytest.mark.parametrize("R,T", [(2, 64), (2, 68)])
+def test_product_few_rows_and_many_steps(L, R, T, out_dtype, swiglu):
+    """Room for 128 rows an expert, or for more: both kinds of ring, gone around in a tile."""
+    c = some_counts(6, R, T, "ragged", R + T)
+    c[2] = [T, 0]
+    check_product(L, R, T, 6, 1168, 1040, out_dtype, swiglu, c)
+    check_product(L, R, T, 6, 1168, 1040, out_dtype, swiglu, np.minimum(c, 3))
+
+
+@pytest.mark.parametrize("T", [1, 40, 132])
+def test_product_most_experts_of_few_rows(L, T):
+    """Sums over 8192 experts take room of the ring."""
+    c = some_counts(8192, 1, T, "ragged", T)
+    c[np.random.RandomState(T).rand(8192, 1) < 0.9] = 0
+    c[[0, 4095, 8191]] = T
+    check_product(L, 1, T, 8192, 1168 if T == 1 else 16, 16, "bf16", False, c)
+
+
 def test_product_on_another_stream(L):
     s = torch.cuda.Stream()
     check_product(L, 2, 17, 4, 128, 128, "bf16", True, some_counts(4, 2, 17, "ragged", 9), stream=s)
