@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(Shape<kMx>::kThreads, 1) __cluster_dims__(2, 1
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive_peer(map_rank(acc_empty + 8 * buf, 0));
+        mbar_arrive_tensor(map_rank(acc_empty + 8 * buf, 0));
         mbar_arrive(plan_empty + 8 * slot);
       }
     }

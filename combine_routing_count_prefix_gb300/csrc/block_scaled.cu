@@ -25,13 +25,13 @@
 //   warp 2      plans
 //   warps 4-11  sums, then the tile's epilogue
 //   warps 12-15 make narrow tiles' products of scales in shared memory, four steps at
-//               a time
+//               a time, and tell the peer which swaps of magnitudes have been read
 // The eight warps have kManyRegisters registers a thread, the others kFewRegisters.
 // Every wait is bounded, as there.
 //
 // What bounds it, on one GB300:
 // - few rows per expert: the weights' bytes.  256 experts x ~32 rows, 7168 -> 2 x
-//   2048, rows to rows: 1.19-1.22 ms of 1.14 (6.2-6.4 TB/s); 2048 -> 7168, 0.59 of
+//   2048, rows to rows: 1.17 ms of 1.14 (6.5 TB/s); 2048 -> 7168, 0.59 of
 //   0.58.  One row: eight experts' weights, 44 us of 35; 6 are launch, plan, first
 //   load and last stores, and the tiles are 1.7 rounds of the pairs.
 // - many rows: the summing warps.  A step of a wide tile is 505 cycles of the tensor
@@ -87,12 +87,12 @@ __host__ __device__ inline ScaledSmem scaled_smem(int stages, int stage, int E) 
   ScaledSmem l;
   uint32_t at = stages * stage;
   l.scales = at, at += kSlots * kSlot;
-  l.amax = at, at += 8 * kNarrowRows * 4;   // narrow: [warp of the pair's set][row]
-  l.row_max = at, at += 2 * 2 * 128 * 4;    // wide: [tile's parity][set][row]
+  l.amax = at, at += 2 * 8 * kNarrowRows * 4;  // narrow: [tile's parity][warp of the pair's set][row]
+  l.row_max = at, at += 2 * 2 * 128 * 4;       // wide: [tile's parity][set][row]
   l.boxes = at, at += kPlanDepth * 32 * 16;
   l.rows = at, at += kPlanDepth * kMaxRows * 4;
   l.tiles = at, at += kPlanDepth * (uint32_t)sizeof(Tile);
-  l.bars = at, at += (2 * kRing<true> + 2 * kBuffers + 2 * kPlanDepth + 2 * kSlots + 4 + 4) * 8;
+  l.bars = at, at += (2 * kRing<true> + 2 * kBuffers + 2 * kPlanDepth + 2 * kSlots + 12 + 4) * 8;
   l.tmem = at, at += 16;
   l.part = at, at += 64;
   l.prefix = at, at += (E + 1) * 4;
@@ -217,19 +217,19 @@ struct Sums {
 
   // ok is a lane's own until the tile's end: a vote in every step took 4% of a dense call.
   __device__ __forceinline__ void wait(const ProductArgs& a, int buffer) {
-    if (!next_done && ok) ok = mbar_wait_cta(acc_full + 8 * buffer, phases >> buffer & 1, a.err);
+    if (!next_done && ok) ok = mbar_wait_tensor(acc_full + 8 * buffer, phases >> buffer & 1, a.err);
     __syncwarp();
     phases ^= 1u << buffer;
     tc_fence_after();
   }
   __device__ __forceinline__ void look(int buffer) {
-    next_done = mbar_test_cta(acc_full + 8 * buffer, phases >> buffer & 1);
+    next_done = mbar_test_tensor(acc_full + 8 * buffer, phases >> buffer & 1);
   }
   // this warp has read the buffer
   __device__ __forceinline__ void release(int buffer) {
     tc_fence_before();
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive_peer(leader_empty + 8 * buffer);
+    if ((threadIdx.x & 31) == 0) mbar_arrive_tensor(leader_empty + 8 * buffer);
   }
   static_assert(kSlots == 2, "slots alternate");
   __device__ __forceinline__ uint32_t slot() const { return slots & 1; }
@@ -398,8 +398,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   const uint32_t full = sbase + l.bars, empty = full + 8 * kRing<kFew>, acc_full = empty + 8 * kRing<kFew>,
                  acc_empty = acc_full + 8 * kBuffers, plan_full = acc_empty + 8 * kBuffers,
                  plan_empty = plan_full + 8 * kPlanDepth, scale_full = plan_empty + 8 * kPlanDepth,
-                 scale_empty = scale_full + 8 * kSlots, amax_full = scale_empty + 8 * kSlots, amax_empty = amax_full + 16,
-                 row_full = amax_empty + 16;
+                 scale_empty = scale_full + 8 * kSlots,
+                 // [set][tile's parity]
+                 amax_full = scale_empty + 8 * kSlots, amax_read = amax_full + 32, amax_empty = amax_read + 32,
+                 row_full = amax_empty + 32;
 
   if (threadIdx.x == 0) {
     tma_prefetch_map(&maps.w);
@@ -415,9 +417,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       mbar_init(scale_full + 8 * i, 4);
       mbar_init(scale_empty + 8 * i, 8);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(amax_full + 8 * i, 4);   // a set's warps, and the bytes that the peer's send
-      mbar_init(amax_empty + 8 * i, 8);  // a set's warps of both CTAs
+      mbar_init(amax_read + 8 * i, 4);   // a set's warps
+      mbar_init(amax_empty + 8 * i, 1);  // the peer's warp that waits for its set's
     }
     for (int i = 0; i < 4; ++i) mbar_init(row_full + 8 * i, 2);  // the two warps of 32 rows
     for (int i = 0; i < kPlanDepth; ++i) {
@@ -467,14 +470,14 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           count = buffers_of(rows_n);
           const uint32_t stride = 512 / count;
           if (count != was)  // other columns: every buffer has to be handed back
-            for (int b = 0; b < kBuffers && ok; ++b) ok = mbar_wait_cta(acc_empty + 8 * b, (phases >> b & 1) ^ 1, a.err);
+            for (int b = 0; b < kBuffers && ok; ++b) ok = mbar_wait_tensor(acc_empty + 8 * b, (phases >> b & 1) ^ 1, a.err);
           for (int k = 0; k < a.steps && ok; ++k) {
             const uint32_t w = desc + (uint32_t)(stage * (kStage<kFew> >> 4)), x = w + (kBytesA >> 4);
             const uint32_t m_side = wide ? x : w, n_side = wide ? w : x;
             const int b = k & (count - 1);
             // the later of the two, most often, last
-            if (!(ok = mbar_wait_cta(full + 8 * stage, phase, a.err))) break;
-            if (!(ok = mbar_wait_cta(acc_empty + 8 * b, (phases >> b & 1) ^ 1, a.err))) break;
+            if (!(ok = mbar_wait(full + 8 * stage, phase, a.err))) break;
+            if (!(ok = mbar_wait_tensor(acc_empty + 8 * b, (phases >> b & 1) ^ 1, a.err))) break;
             tc_fence_after();
 #pragma unroll
             for (int j = 0; j < 4; ++j) mma_8bit(tmem + b * stride, m_side + 2 * j, n_side + 2 * j, idesc, j > 0);
@@ -508,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     sums.phases = sums.slots = 0;
     sums.ok = true;
     bool& ok = sums.ok;
-    int i = 0, narrow_tiles = 0, wide_tiles = 0;
+    int i = 0, swaps = 0, wide_tiles = 0;  // swaps: of largest magnitudes with the peer
     // the i-th tile's plan; of a wide one this thread's row and first scales, which are
     // asked for before the tile before it is stored
     int row = -1;
@@ -635,15 +638,19 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
               else
                 store_plain(a, acc[c], first, list + 64 * c);
             }
-        } else {
-          // a block of 128 outputs is the pair's: its eight warps of this set swap
-          // their largest magnitudes, once the last tile's have been read
-          mbar_wait_cta_warp(amax_empty + 8 * set, (narrow_tiles & 1) ^ 1, ok, a.err);
+        } else if (chunks > 0) {
+          // A block of 128 outputs is the pair's: its eight warps of this set swap their
+          // largest magnitudes, through one of two buffers in turn.  The peer may still
+          // read the other one, and has read this one when amax_empty says so (below, at
+          // the scales): its reads come before this warp's stores only by a release to
+          // the cluster there and an acquire of it here.
+          const uint32_t turn = 16 * set + 8 * (swaps & 1), swapped = amax_full + turn;
+          if (ok && swaps > 1) ok = mbar_wait_warp(amax_empty + turn, (swaps >> 1 & 1) ^ 1, a.err);
           if (!ok) break;
-          uint32_t* amax = reinterpret_cast<uint32_t*>(smem + l.amax) + 32 * set;
+          uint32_t* amax = reinterpret_cast<uint32_t*>(smem + l.amax) + (swaps & 1) * 8 * kNarrowRows + 32 * set;
           const int source = ((int)rank * 4 + w) * kNarrowRows;
-          const uint32_t peer = map_rank(smem_addr(amax + source), rank ^ 1), told = map_rank(amax_full + 8 * set, rank ^ 1);
-          if (lane == 0) mbar_expect_bytes(amax_full + 8 * set, 128 * chunks);
+          const uint32_t peer = map_rank(smem_addr(amax + source), rank ^ 1), told = map_rank(swapped, rank ^ 1);
+          if (lane == 0) mbar_expect_bytes(swapped, 128 * chunks);
           float h[kChunks][16];
 #pragma unroll
           for (int c = 0; c < kChunks; ++c)
@@ -656,8 +663,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
               shared_store_peer(peer + 4 * column, most, told);
             }
           __syncwarp();
-          if (lane == 0) mbar_arrive(amax_full + 8 * set);
-          mbar_wait_cta_warp(amax_full + 8 * set, narrow_tiles & 1, ok, a.err);  // counted bytes, as loads are
+          if (lane == 0) mbar_arrive(swapped);
+          ok = mbar_wait_warp(swapped, swaps >> 1 & 1, a.err);  // counted bytes, as loads are
           if (!ok) break;
           float scale[kChunks];  // of row `lane` of each 32
 #pragma unroll
@@ -669,10 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
               scale[c] = block_scale(__uint_as_float(most));
             }
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(amax_empty + 8 * set);
-            mbar_arrive_peer(map_rank(amax_empty + 8 * set, rank ^ 1));
-          }
+          if (lane == 0) mbar_arrive(amax_read + turn);
 #pragma unroll
           for (int c = 0; c < kChunks; ++c)
             if (c < chunks) {
@@ -689,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                   for (uint8_t* end = in_row(a, a.y + a.y_row, row); (at += 4) < end;) *reinterpret_cast<uint32_t*>(at) = 0;
               }
             }
-          ++narrow_tiles;
+          ++swaps;
         }
       }
       __syncwarp();
@@ -702,7 +706,14 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     // list, 16 bytes of it (four steps) at a time, the next on their way; lane % 4
     // brings w's of a step (with SwiGLU of gate or, lane & 4, up).
     const int q = warp & 3, chunks = (a.steps + 3) / 4;
-    int i = 0, sslot = 0;
+    // Warps 14 and 15 also tell the peer, once in a tile, that a set here has read the
+    // largest magnitudes of the swap before the last, so that the next may take their
+    // buffer.  A release to the cluster takes 1500 cycles and more, which the summing
+    // warps do not have (decode 1257 us with it there, 1166 here).  Behind a tile's
+    // second slot of scales they are at the end of the tile before, and the next slot is
+    // long to come (8 steps a tile, 302 us; behind the first, 322).
+    const int set = q - 2;
+    int i = 0, sslot = 0, swaps = 0;
     uint32_t sphase = 0;
     bool ok = true;
     for (int t = pair_id; t < ntiles && ok; t += pairs, ++i) {
@@ -742,6 +753,15 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(scale_full + 8 * sslot);
         if (++sslot == kSlots) sslot = 0, sphase ^= 1;
+        if (kSwiglu && c == min(1, chunks - 1) && a.out_dtype == LLMOE_DTYPE_FP8B && set >= 0 && columns(tile.groups) > 32 * set) {
+          const uint32_t turn = 16 * set + 8 * (swaps & 1);
+          if (swaps > 1) {
+            mbar_wait_cta_warp(amax_read + turn, (swaps >> 1 & 1) ^ 1, ok, a.err);
+            if (!ok) break;
+            if (lane == 0) mbar_arrive_peer_release(map_rank(amax_empty + turn, rank ^ 1));
+          }
+          ++swaps;
+        }
       }
     }
   }

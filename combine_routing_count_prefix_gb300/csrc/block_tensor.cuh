@@ -55,11 +55,20 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
 // Arrival on a barrier of the cluster's window (map_rank), possibly the peer's.
 // It publishes nothing to the peer's threads: a release to the cluster waits
 // for all of the thread's memory operations in flight (2600 cycles in a warp
-// that loads ahead).  Its uses need none: tensor memory that has been read, and
-// shared memory that only the tensor core of this SM reads, which the writers'
-// fence_async_shared has made visible to it.
+// that loads ahead).  Its use needs none: shared memory that only the tensor core
+// of this SM reads, which the writers' fence_async_shared has made visible to it.
 __device__ __forceinline__ void mbar_arrive_peer(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// The same where the peer's threads go on to write shared memory that this thread has
+// read, or whose readers' arrivals it has waited for.
+__device__ __forceinline__ void mbar_arrive_peer_release(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// The same where what is handed over is tensor memory, which tc_fence_before and
+// tc_fence_after order: the barrier has to be of the cluster's scope and no more.
+__device__ __forceinline__ void mbar_arrive_tensor(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   uint32_t done;
@@ -86,9 +95,8 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int32_t
   return true;
 }
 
-// The same where what the barrier guards is not another CTA's writes to shared
-// memory: an acquire of the cluster costs 200 cycles on a phase that is complete,
-// this one 20.
+// The same where all arrivals are this CTA's threads', and what the barrier guards is
+// theirs.
 __device__ __forceinline__ bool mbar_try_wait_cta(uint32_t bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
@@ -110,12 +118,35 @@ __device__ __forceinline__ bool mbar_wait_cta(uint32_t bar, uint32_t parity, int
     }
   return true;
 }
-// Whether the phase is complete, without waiting.
-__device__ __forceinline__ uint32_t mbar_test_cta(uint32_t bar, uint32_t parity) {
+// The same where the barrier guards tensor memory: products that a commit has announced
+// or loads that mbar_arrive_tensor has; tc_fence_after follows.
+__device__ __forceinline__ bool mbar_try_wait_tensor(uint32_t bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+__device__ __forceinline__ bool mbar_wait_tensor(uint32_t bar, uint32_t parity, int32_t* err) {
+  if (mbar_try_wait_tensor(bar, parity)) return true;
+  const long long start = clock64();
+  while (!mbar_try_wait_tensor(bar, parity))
+    if (clock64() - start > kSpinLimit) {
+      report(err, LLMOE_DEV_TIMEOUT);
+      return false;
+    }
+  return true;
+}
+// Whether the phase is complete, without waiting.
+__device__ __forceinline__ uint32_t mbar_test_tensor(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(done)
       : "r"(bar), "r"(parity)
