@@ -79,18 +79,6 @@ __device__ __forceinline__ void store_choice(const GroupRouterArgs& a, int64_t r
   }
 }
 
-// 1 / d to the nearest fp32, what __frcp_rn gives, for d from 1 to 2^126 (all of them
-// compared): the hardware's reciprocal and one step of Newton's, whose remainder is
-// exact in a fused multiply-add.  Without the general one's other ranges, which a
-// lane's experts would each have in line: one token 2.9 us against 3.8, 8192 tokens
-// 9.1 against 9.9.  So 1 / (1 + exp(-v)) for v from -87 on; a token with a logit below
-// (-infinity among them) takes the general one.
-__device__ __forceinline__ float one_over(float d) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
-  return fmaf(fmaf(-d, r, 1.0f), r, r);
-}
-
 template <int W, bool kSoftmax>
 __global__ void __launch_bounds__(256) rows_kernel(GroupRouterArgs a) {
   extern __shared__ uint32_t smem[];

@@ -35,6 +35,17 @@ __device__ __forceinline__ float load_logit(const void* logits, int dtype, int64
 }
 
 __device__ __forceinline__ float sigmoid_score(float l) { return __frcp_rn(1.0f + expf(-l)); }
+// 1 / d to the nearest fp32, what __frcp_rn gives, for d from 1 to 2^126 (each of them
+// compared by tests/test_gpu_reciprocal.py): the hardware's reciprocal and one step of
+// Newton's, whose remainder is exact in a fused multiply-add.  Without the general
+// one's other ranges, which a lane's experts would each have in line: one token 2.9 us
+// against 3.8, 8192 tokens 9.1 against 9.9.  So 1 / (1 + exp(-v)) for v from -87 on; a
+// token with a logit below (-infinity among them) takes the general one.
+__device__ __forceinline__ float one_over(float d) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+  return fmaf(fmaf(-d, r, 1.0f), r, r);
+}
 // Of a row whose largest logit is top; logits of +infinity are the limit of
 // equal large ones.
 __device__ __forceinline__ float softmax_score(float l, float top) {
