@@ -78,6 +78,14 @@ def _tensor(name: str, t: torch.Tensor, shape: tuple, dtypes: tuple, device: tor
         raise ValueError(f"{name} is not contiguous")
 
 
+def _weight(name: str, t: torch.Tensor, shape: tuple, dtypes: tuple, device: torch.device, laid_out: bool = True) -> None:
+    """A weight, which a call behind others must not refuse.  What is not laid out is
+    packed, from a copy where it is not contiguous."""
+    _tensor(name, t, shape, dtypes, device, laid_out)
+    if t.is_contiguous() and t.data_ptr() % 16:
+        raise ValueError(f"{name} is not 16-byte aligned")
+
+
 class MoEBlock:
     """
     num_max_tokens  T: tokens per rank a call may have
@@ -124,10 +132,10 @@ class MoEBlock:
             _tensor("gate_up_scale", gate_up_scale, (E, 2, _blocks(I), _blocks(H)), (torch.float32,), dev)
             _tensor("down_scale", down_scale, (E, _blocks(H), _blocks(I)), (torch.float32,), dev)
             packed = (torch.uint8, torch.float8_e4m3fn)
-        _tensor("norm_weight", norm_weight, (H,), own, dev)
-        _tensor("router_weight", router_weight, (E, H), own, dev)
-        _tensor("gate_up", gate_up, (E, 2 * I, H), packed, dev, rows == "same" or coded)
-        _tensor("down", down, (E, H, I), packed, dev, rows == "same" or coded)
+        _weight("norm_weight", norm_weight, (H,), own, dev)
+        _weight("router_weight", router_weight, (E, H), own, dev)
+        _weight("gate_up", gate_up, (E, 2 * I, H), packed, dev, rows == "same" or coded)
+        _weight("down", down, (E, H, I), packed, dev, rows == "same" or coded)
         if router_bias is not None:
             _tensor("router_bias", router_bias, (E,), (torch.float32,), dev)
         if self.T < 1:
