@@ -149,6 +149,8 @@ class MoEBlock:
             raise ValueError(f"num_groups is {self.G} of {E} experts, at most {llmoe.LLMOE_MAX_GROUPS}")
         if not 1 <= self.kept <= self.G or self.K > E // self.G * self.kept:
             raise ValueError(f"kept_groups is {self.kept} of {self.G}, num_topk {self.K}")
+        if scoring not in (llmoe.LLMOE_SCORE_SIGMOID, llmoe.LLMOE_SCORE_SOFTMAX):
+            raise ValueError(f"scoring is {scoring!r}")
         if group_top2 and scoring != llmoe.LLMOE_SCORE_SIGMOID:
             raise ValueError("group_top2 goes with sigmoid scores")
         self.router_flags = llmoe.LLMOE_ROUTER_RENORM | (llmoe.LLMOE_ROUTER_GROUP_TOP2 if group_top2 else 0)

@@ -1,4 +1,4 @@
-"""MoEBlock refuses weights that its calls would refuse, when it is made: a call that
+"""MoEBlock refuses what its calls would refuse, when it is made: a call that
 is refused behind the norm would leave the residual changed and no output."""
 import pytest
 import torch
@@ -49,3 +49,9 @@ def test_weights_off_16_bytes(Block, rows, name, shape, by):
 @pytest.mark.parametrize("rows", ["same", "fp8b"])
 def test_weights_on_16_bytes(Block, rows):
     Block(**arguments(rows, norm_weight=off(H, by=0)))
+
+
+@pytest.mark.parametrize("scoring", [-1, 2, None])
+def test_scoring(Block, scoring):
+    with pytest.raises(ValueError, match="scoring"):
+        Block(**arguments("same", scoring=scoring))
