@@ -102,6 +102,8 @@ class MoEBlock:
     num_groups      groups of experts, of which a token chooses from kept_groups (all of
                     them, unless given); group_top2: a group's score is the sum of its two
                     largest keys, else its largest
+    renorm          a token's weights are scale * score / (the sum of its chosen scores), else
+                    scale * score: what a softmax over all experts leaves to the chosen
     gate_up_scale   [E, 2, ceil(I / 128), ceil(H / 128)] fp32, with gate_up as codes (uint8 or
                     float8_e4m3fn); down_scale [E, ceil(H / 128), ceil(I / 128)]
     """
@@ -111,7 +113,8 @@ class MoEBlock:
                  router_bias: torch.Tensor | None = None, dtype: str = "bf16", rows: str = "same",
                  eps: float = 1e-6, scale: float = 1.0, scoring: int = llmoe.LLMOE_SCORE_SIGMOID, err=None,
                  num_groups: int = 1, kept_groups: int | None = None, group_top2: bool = False,
-                 gate_up_scale: torch.Tensor | None = None, down_scale: torch.Tensor | None = None):
+                 gate_up_scale: torch.Tensor | None = None, down_scale: torch.Tensor | None = None,
+                 renorm: bool = True):
         if rows not in ("same", "mx8", "fp8b"):
             raise ValueError(f'rows is "same", "mx8" or "fp8b", not {rows!r}')
         if dtype not in _TORCH:
@@ -153,7 +156,8 @@ class MoEBlock:
             raise ValueError(f"scoring is {scoring!r}")
         if group_top2 and scoring != llmoe.LLMOE_SCORE_SIGMOID:
             raise ValueError("group_top2 goes with sigmoid scores")
-        self.router_flags = llmoe.LLMOE_ROUTER_RENORM | (llmoe.LLMOE_ROUTER_GROUP_TOP2 if group_top2 else 0)
+        self.renorm_flag = llmoe.LLMOE_ROUTER_RENORM if renorm else 0
+        self.group_flag = llmoe.LLMOE_ROUTER_GROUP_TOP2 if group_top2 else 0
         for width in (H, I):
             if llmoe.llmoe_row_bytes(width, llmoe.ROW_DTYPE_CODES[dtype if rows == "same" else rows]) == 0:
                 raise ValueError(f"a hidden size of {width}: a row is whole 16 bytes, MX8 rows multiples of 32 values, "
@@ -221,10 +225,11 @@ class MoEBlock:
                                L.LLMOE_DTYPE_FP32, 0, L.geometry(max(1, R * self.T), 1, 1, self.err))
         if self.kept < self.G:
             L.llmoe_group_router(self.logits, self.router_bias, active, self.topk_idx, self.topk_w, tokens, E, self.K,
-                                 self.G, self.kept, L.LLMOE_DTYPE_FP32, self.scoring, self.router_flags, self.scale)
+                                 self.G, self.kept, L.LLMOE_DTYPE_FP32, self.scoring,
+                                 self.renorm_flag | self.group_flag, self.scale)
         else:
             L.llmoe_topk_router(self.logits, self.router_bias, active, self.topk_idx, self.topk_w, tokens, E, self.K,
-                                L.LLMOE_DTYPE_FP32, self.scoring, L.LLMOE_ROUTER_RENORM, self.scale)
+                                L.LLMOE_DTYPE_FP32, self.scoring, self.renorm_flag, self.scale)
         d = self.rb_dispatch.buf_set(0, self.K, n, self.err)
         c = self.rb_combine.buf_set(1, self.K, n, self.err)
         L.llmoe_clean(d)
