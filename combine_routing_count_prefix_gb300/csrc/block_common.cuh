@@ -139,28 +139,6 @@ __device__ __forceinline__ uint4 pack_quad(const float (&v)[Quad<DT>::kValues]) 
   return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
-// Pairs of fp32 values in one register pair: one instruction for both.
-using Pair = unsigned long long;
-__device__ __forceinline__ Pair pair(float a, float b) {
-  Pair p;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(a), "f"(b));
-  return p;
-}
-__device__ __forceinline__ float2 unpair(Pair p) {
-  float2 v;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(p));
-  return v;
-}
-__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
-  Pair d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
-  Pair d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
 // |v| as an integer that orders like the magnitude, a NaN above infinity: the
 // maximum of these over a group finds its largest value or its NaN.
 __device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }

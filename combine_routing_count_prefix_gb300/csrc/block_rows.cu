@@ -30,6 +30,28 @@ struct RowsArgs {
   uint64_t out_stride;  // bytes of an output row
 };
 
+// Pairs of fp32 values in one register pair: one instruction for both.
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair pair(float a, float b) {
+  Pair p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(a), "f"(b));
+  return p;
+}
+__device__ __forceinline__ float2 unpair(Pair p) {
+  float2 v;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+  Pair d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  Pair d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
 // The larger magnitude; NaN where either is.
 __device__ __forceinline__ float max_magnitude(float a, float b) {
   float d;
@@ -217,7 +239,6 @@ int launch_rows_dtype(const RowsArgs& a, int dtype, llmoe_stream_t stream) {
     default: return launch_rows<LLMOE_DTYPE_BF16, k8Bit ? OUT : LLMOE_DTYPE_BF16, kNorm>(a, stream);
   }
 }
-
 
 // Fills the geometry of a call on `rows` rows of `hidden` values; false where
 // the arguments are not valid.

@@ -255,18 +255,6 @@ __device__ __forceinline__ void tmem_load_end(uint32_t (&v)[32]) {
                : "memory");
 }
 template <int kOffset>
-__device__ __forceinline__ float shared_load(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cta.f32 %0, [%1 + %2];" : "=f"(v) : "r"(addr), "n"(kOffset));
-  return v;
-}
-template <int kOffset>
-__device__ __forceinline__ float2 shared_load2(uint32_t addr) {
-  float2 v;
-  asm volatile("ld.shared::cta.v2.f32 {%0, %1}, [%2 + %3];" : "=f"(v.x), "=f"(v.y) : "r"(addr), "n"(kOffset));
-  return v;
-}
-template <int kOffset>
 __device__ __forceinline__ float4 shared_load4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared::cta.v4.f32 {%0, %1, %2, %3}, [%4 + %5];"
