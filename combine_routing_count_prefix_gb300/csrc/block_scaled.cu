@@ -31,24 +31,18 @@
 //
 // What bounds it, on one GB300:
 // - few rows per expert: the weights' bytes.  256 experts x ~32 rows, 7168 -> 2 x
-//   2048, rows to rows: 1.17 ms of 1.14 (6.5 TB/s); 2048 -> 7168, 0.59 of
+//   2048, rows to rows: 1.14-1.17 ms of 1.14 (6.5-6.7 TB/s); 2048 -> 7168, 0.59 of
 //   0.58.  One row: eight experts' weights, 44 us of 35; 6 are launch, plan, first
 //   load and last stores, and the tiles are 1.7 rounds of the pairs.
 // - many rows: the summing warps.  A step of a wide tile is 505 cycles of the tensor
 //   core and 750 to 800 of a warp: a wait, loads of 128 columns, 128
 //   multiply-adds, the arrival that hands the buffer back, each in the shadow of the
 //   tensor core's and the loads' traffic (an access to shared memory takes 140 cycles
-//   there).  16 experts x ~1024 rows, 7168 -> 2 x 2048: 409-417 us in a burst (2.3-2.4
-//   PFLOP/s), 445 steadily; 2048 -> 7168: 264-272, a quarter of it the epilogues of
+//   there).  16 experts x ~1024 rows, 7168 -> 2 x 2048: 442-452 us steadily, 403-414 in
+//   a burst (2.3-2.4 PFLOP/s); 2048 -> 7168: 264-274, a quarter of it the epilogues of
 //   tiles of 16 steps.
-// What the structure bought, in microseconds (dense gate / up, dense down, decode):
-// the features on the M side of all tiles 963 / 436 / 1866; wide tiles, waits that
-// acquire no cluster 622 / 405 / 1827; the steps of four unrolled 534 / 412 / 1319; a
-// step's tests and scales issued in the step before 472 / 361 / 1304; scalar instead
-// of packed multiply-adds, which cost a move for every loaded pair 454 / 286 / 1278;
-// row scales from memory, no vote in a step 414 / 277 / 1239; eight buffers for tiles
-// of up to 64 rows 413 / 274 / 1218; a plain product's sums read 16 columns at a time
-// 410 / 264 / 1219.
+// Three of the four kernels spill a few registers (bytes stored / loaded): with wide
+// tiles 116 / 152 with SwiGLU and 48 / 136 plain, without them 40 / 100 plain.
 #include "block_plan.cuh"
 
 namespace {
