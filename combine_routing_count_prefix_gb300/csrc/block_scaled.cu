@@ -81,7 +81,7 @@ __host__ __device__ inline ScaledSmem scaled_smem(int stages, int stage, int E) 
   ScaledSmem l;
   uint32_t at = stages * stage;
   l.scales = at, at += kSlots * kSlot;
-  l.amax = at, at += 2 * 8 * kNarrowRows * 4;  // narrow: [tile's parity][warp of the pair's set][row]
+  l.amax = at, at += 2 * 8 * kNarrowRows * 4;  // narrow: [swap's parity][warp of the pair's set][row]
   l.row_max = at, at += 2 * 2 * 128 * 4;       // wide: [tile's parity][set][row]
   l.boxes = at, at += kPlanDepth * 32 * 16;
   l.rows = at, at += kPlanDepth * kMaxRows * 4;
@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                  acc_empty = acc_full + 8 * kBuffers, plan_full = acc_empty + 8 * kBuffers,
                  plan_empty = plan_full + 8 * kPlanDepth, scale_full = plan_empty + 8 * kPlanDepth,
                  scale_empty = scale_full + 8 * kSlots,
-                 // [set][tile's parity]
+                 // [set][swap's parity]
                  amax_full = scale_empty + 8 * kSlots, amax_read = amax_full + 32, amax_empty = amax_read + 32,
                  row_full = amax_empty + 32;
 

@@ -91,8 +91,10 @@ class MoEBlock:
     num_max_tokens  T: tokens per rank a call may have
     norm_weight     [H]
     router_weight   [E, H], E a multiple of 4 (fp32 logits rows of whole 16 bytes);
-                    router_bias [E] fp32 or None (added to the scores for the choice only)
-    gate_up         [E, 2 I, H], gate rows first; down [E, H, I]
+                    router_bias [E] fp32 or None (added to what is chosen by, the sigmoids or,
+                    with softmax, the logits; not to the weights)
+    gate_up         [E, 2 I, H], gate rows first; down [E, H, I].  These four start at 16-byte
+                    boundaries; gate_up and down that are packed may be of any layout
     dtype           "bf16" or "fp16": x, weights and output (with rows="mx8"
                     gate_up and down, which are packed, may be bf16, fp16 or fp32;
                     with rows="fp8b" the same, or e4m3 codes with gate_up_scale and
